@@ -16,7 +16,9 @@
  *                      (pa_prefill_store_varlen: with the chunks' store);
  * pa_store_decode fuses pa_store_kv and pa_decode for a decode step; and an
  * FP8 (E4M3) KV cache: pa_store_kv_fp8 quantises into it, pa_decode_fp8
- * decodes over it and pa_store_decode_fp8 does both for a decode step.
+ * decodes over it and pa_store_decode_fp8 does both for a decode step.  A
+ * second FP8 cache has scales that follow the data, one per (block, kv head):
+ * pa_store_kv_fp8_block appends to it and pa_decode_fp8_block decodes over it.
  *
  * Sources (web pages that describe the method):
  *   [EAS] koas-w, "errors and solutions" (Qwen2.5-1.5B inference from
@@ -116,8 +118,8 @@ typedef int32_t pa_status;
 /*
  * Launch flags (the `flags` argument of pa_store_kv, pa_store_kv_fp8,
  * pa_rope_store_kv, pa_decode, pa_store_decode, pa_rope_store_decode,
- * pa_decode_fp8, pa_store_decode_fp8 and pa_decode_noalloc).  Any other bit returns
- * PA_ERR_INVALID_ARG.
+ * pa_decode_fp8, pa_store_decode_fp8, pa_decode_noalloc, pa_store_kv_fp8_block
+ * and pa_decode_fp8_block).  Any other bit returns PA_ERR_INVALID_ARG.
  *
  * PA_LAUNCH_PDL: programmatic dependent launch.  The call's kernel may begin
  * while the kernel launched just before it on the same stream is still
@@ -503,6 +505,77 @@ PA_API pa_status pa_decode_fp8(void *out, int32_t out_dtype, const void *q, cons
                                int32_t head_dim, int32_t block_size, float scale,
                                int32_t num_splits, void *workspace, size_t workspace_bytes,
                                uint32_t flags, void *stream);
+
+/*
+ * Block-scaled FP8 KV cache: the pools of the FP8 cache above (E4M3 codes, K
+ * token-major, V dim-major inside a block) with one scale per (block, kv
+ * head), K and V apart, that follows the data ([CEB] keeps scales beside the
+ * caches and fixes no granularity).  k_scale and v_scale are uint8
+ * [num_blocks][num_kv_heads] device arrays of biased exponents: the value of
+ * a code of head h in block b is code * 2^(k_scale[b][h] - 127).  Scales are
+ * powers of two, so re-coding a block to a larger scale is exact except for
+ * codes that become subnormal.  The exponents the library stores lie in
+ * [-40, 40]; a reader clamps other bytes to that span.  A block that nothing
+ * was stored into may hold anything.
+ *
+ * pa_store_kv_fp8_block -- appends the new rows of cu_seqlens-packed
+ * sequences.  Token t of sequence s (cu_seqlens[s] <= t < cu_seqlens[s + 1])
+ * sits at position context_lens[s] - q_len_s + (t - cu_seqlens[s]) and goes
+ * to the block that block_tables names for it (there is no slot_mapping: the
+ * scale belongs to a block, so a block's new rows are handled together).
+ * For each block it touches, each kv head, and K and V apart, with r0 .. r1 - 1
+ * the rows of the block that it writes and a the largest finite |x| of them:
+ *   e     = the smallest exponent in [-40, 40] with a <= 448 * 2^e (40 if
+ *           none), and, where r0 > 0, at least the exponent the block has;
+ *   code  = E4M3(x * 2^-e) of the new rows, nearest even, magnitudes past
+ *           448 (infinities among them) saturated, NaN kept;
+ *   rows 0 .. r0 - 1 keep their values: their codes are E4M3(code *
+ *           2^(e_old - e)) where e grew and stay as they are otherwise;
+ *   rows r1 .. 15 keep their bytes, and the scale byte becomes e + 127.
+ * With r0 = 0 the block's old scale and contents do not matter.
+ *
+ *   k, v           bf16 source rows, element (t, h, d) at k + t *
+ *                  k_tok_stride + h * k_head_stride + d, same for v.
+ *   cu_seqlens     int32 [num_seqs + 1], non-decreasing, from 0; tokens at or
+ *                  past cu_seqlens[num_seqs] are not read.
+ *   total_tokens   rows of k and v (sizes the launch grid).
+ *   context_lens   int32 [num_seqs], the new tokens included.
+ *   error_flags    optional int32 word (may be NULL): a chunk outside k / v,
+ *                  longer than its context or past its table row sets
+ *                  PA_DEVERR_SHAPE, a table entry outside the pool sets
+ *                  PA_DEVERR_BLOCK_INDEX; that sequence or block is skipped.
+ *   flags          0 or PA_LAUNCH_PDL.
+ * k_cache and v_cache must be 16-byte aligned.  A block written by two
+ * sequences of one call is a caller error (fork it first: one of the results,
+ * or a mix of both, ends up in it).
+ * Supported: head_dim 128, block_size 16, 1 <= num_kv_heads <= 64.
+ */
+PA_API pa_status pa_store_kv_fp8_block(
+    const void *k, const void *v, int64_t k_tok_stride, int64_t k_head_stride,
+    int64_t v_tok_stride, int64_t v_head_stride, const int32_t *cu_seqlens, int32_t num_seqs,
+    int32_t total_tokens, void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale,
+    int64_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+    const int32_t *block_tables, int32_t block_table_stride, const int32_t *context_lens,
+    int32_t *error_flags, uint32_t flags, void *stream);
+
+/*
+ * pa_decode_fp8_block -- pa_decode over a block-scaled FP8 cache: the
+ * attention over the values code * 2^(scale byte - 127).  Products run on the
+ * tensor cores in f16 as in pa_decode_fp8 (codes exact, q rounded to f16);
+ * the softmax weights are rounded to f16 (11 bits) after taking in the V
+ * scale of their block, the scores, sums and outputs stay fp32.  Same
+ * workspace, splits, flags and outputs as pa_decode (with
+ * PA_LAUNCH_EARLY_KV the pools must not be written by the kernel before; the
+ * scale arrays are read after it).  k_scale and v_scale must be 8-byte
+ * aligned; NULL or unaligned: PA_ERR_INVALID_ARG.
+ */
+PA_API pa_status pa_decode_fp8_block(
+    void *out, int32_t out_dtype, const void *q, const void *k_cache, const void *v_cache,
+    const uint8_t *k_scale, const uint8_t *v_scale, int64_t num_blocks,
+    const int32_t *block_tables, int32_t block_table_stride, const int32_t *context_lens,
+    int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, float scale, int32_t num_splits, void *workspace,
+    size_t workspace_bytes, uint32_t flags, void *stream);
 
 /*
  * pa_decode_merge -- log-sum-exp merge of decode partials (flash-decoding).

@@ -280,6 +280,8 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   p.err = err;
   p.k_scale = r.k_scale;
   p.v_scale = r.v_scale;
+  p.k_bscale = r.k_bscale;
+  p.v_bscale = r.v_bscale;
   p.v_pool = r.fp8 ? static_cast<const uint8_t *>(r.v_cache) : nullptr;
   p.new_k = static_cast<const uint16_t *>(r.new_k);
   p.new_v = static_cast<const uint16_t *>(r.new_v);
@@ -308,7 +310,20 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   const bool split_merge = !r.positions && r.num_kv_heads >= 4 &&
                            (long long)r.splits >= 8LL * r.batch;
   cudaError_t e;
-  if (r.fp8) {
+  if (r.k_bscale) {
+    switch (r.num_kv_heads) {
+      case 1: e = launch_decode<1, true, false, false, true>(G, tk, tv, p, s, device, pdl); break;
+      case 2: e = launch_decode<2, true, false, false, true>(G, tk, tv, p, s, device, pdl); break;
+      case 4:
+        e = split_merge ? launch_decode<4, true, false, true, true>(G, tk, tv, p, s, device, pdl)
+                        : launch_decode<4, true, false, false, true>(G, tk, tv, p, s, device, pdl);
+        break;
+      default:
+        e = split_merge ? launch_decode<8, true, false, true, true>(G, tk, tv, p, s, device, pdl)
+                        : launch_decode<8, true, false, false, true>(G, tk, tv, p, s, device, pdl);
+        break;
+    }
+  } else if (r.fp8) {
     switch (r.num_kv_heads) {
       case 1: e = launch_decode<1, true>(G, tk, tv, p, s, device, pdl); break;
       case 2: e = launch_decode<2, true>(G, tk, tv, p, s, device, pdl); break;
@@ -555,6 +570,33 @@ extern "C" pa_status pa_decode_fp8(void *out, int32_t out_dtype, const void *q,
   r.k_scale = k_scale;
   r.v_scale = v_scale;
   if (batch > 0 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  int device = -1;
+  const pa_status st = check_decode_request(r, &device);
+  if (st != PA_OK || batch == 0) return st;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < pa_decode_workspace_size(r.splits, num_q_heads, head_dim))
+    return PA_ERR_WORKSPACE;
+  return run_decode(r, workspace, static_cast<int32_t *>(workspace), device, false);
+}
+
+extern "C" pa_status pa_decode_fp8_block(
+    void *out, int32_t out_dtype, const void *q, const void *k_cache, const void *v_cache,
+    const uint8_t *k_scale, const uint8_t *v_scale, int64_t num_blocks,
+    const int32_t *block_tables, int32_t block_table_stride, const int32_t *context_lens,
+    int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, float scale, int32_t num_splits, void *workspace,
+    size_t workspace_bytes, uint32_t flags, void *stream) {
+  using namespace pa;
+  DecodeRequest r{out, out_dtype, q, k_cache, v_cache, num_blocks, block_tables,
+                  block_table_stride, context_lens, batch, num_q_heads, num_kv_heads, head_dim,
+                  block_size, scale, num_splits, 0, flags, stream};
+  r.fp8 = true;
+  r.k_bscale = k_scale;
+  r.v_bscale = v_scale;
+  if (batch > 0 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  // a block's scale bytes are read as one word
+  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 7)
+    return PA_ERR_INVALID_ARG;
   int device = -1;
   const pa_status st = check_decode_request(r, &device);
   if (st != PA_OK || batch == 0) return st;

@@ -1,0 +1,5 @@
+// decode_kernel instantiations for block-scaled FP8 pools, 1 kv head(s) per sequence.
+#define PA_HKV 1
+#define PA_F8 true
+#define PA_BS true
+#include "pa_decode_inst.cuh"

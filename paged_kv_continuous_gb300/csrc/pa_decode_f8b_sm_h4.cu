@@ -1,0 +1,7 @@
+// decode_kernel instantiations for block-scaled FP8 pools, 4 kv heads per
+// sequence, merges of cut sequences left to merge_kernel.
+#define PA_HKV 4
+#define PA_F8 true
+#define PA_SPLIT true
+#define PA_BS true
+#include "pa_decode_inst.cuh"

@@ -42,6 +42,9 @@ struct DecodeRequest {
   bool fp8 = false;
   const float *k_scale = nullptr;
   const float *v_scale = nullptr;
+  // block-scaled FP8 pools (with fp8): scale bytes per (block, kv head)
+  const uint8_t *k_bscale = nullptr;
+  const uint8_t *v_bscale = nullptr;
   // fused store of each sequence's new token (bf16 pools; null: none)
   const void *new_k = nullptr;
   const void *new_v = nullptr;

@@ -60,6 +60,15 @@
 // token order of the score rows that makes every V operand register one
 // 32-bit load, K rows read as 16-byte chunks (a dim order per fragment
 // column shared with q), and P as one f16 term (see the F8 branches).
+// Block scales (BS, on top of F8, pa_decode_fp8_block): the scales are powers
+// of two per (block, kv head).  The producer that fills a stage writes the
+// block's scale bytes beside it; a consumer folds K's into the score scale
+// and V's, 2^ev, into the exponent: with t = s + ev (base 2) and m the
+// running reference of t,
+//   P' = 2^(t - m),  O += P' code_v,  l += 2^-ev P',  out = O / l,
+// so the f16 weights carry the V scale relative to the largest weight times
+// scale and stay <= 256, the sum stays the plain softmax sum, and the lse
+// m + log2 l is that of the scores.
 // Early K/V requests (p.early_kv, a
 // launch flag): the producers issue the first ring stages' pages before the
 // wait for the previous kernel.
@@ -70,7 +79,7 @@
 
 #include <type_traits>
 
-#include "pa_common.cuh"
+#include "pa_fp8_block.cuh"
 
 namespace pa {
 
@@ -92,6 +101,8 @@ struct DecodeParams {
   const float *k_scale;  // FP8 pools only: per kv head, value = code * scale
   const float *v_scale;
   const uint8_t *v_pool;  // FP8 pools only: V, [num_blocks][Hkv][128][16] bytes
+  const uint8_t *k_bscale;  // block scales (BS kernels): biased exponents [num_blocks][Hkv]
+  const uint8_t *v_bscale;
   // Fused store (bf16 pools; new_k == nullptr: none).  Sequence b's new
   // token (position context_lens[b] - 1) has K/V rows new_k / new_v + b *
   // new_tok + h * 128; it goes to pool slot slot_mapping[b] (< 0: none) and,
@@ -145,7 +156,9 @@ __host__ __device__ constexpr int align_up(int x, int a) { return (x + a - 1) / 
 // F8: the pools hold E4M3 codes (one byte per element) with per-kv-head
 // scales; K pages keep the token-major layout, V pages are dim-major inside a
 // block ([Hkv][128 dims][16 tokens]).
-template <int G, int HKV, bool F8 = false, bool ROPE = false>
+// BS (with F8): one scale byte per (block, kv head) instead; 16 bytes per
+// stage hold the block's (K's in the first eight, V's in the last eight).
+template <int G, int HKV, bool F8 = false, bool ROPE = false, bool BS = false>
 struct DecodeShape {
   static constexpr int HQ = G * HKV;
   static constexpr int CW = kDecodeConsumerWarps;
@@ -184,12 +197,13 @@ struct DecodeShape {
   static constexpr int DEF_MAX_PIECES = 512 / HQ - 1;  // weights room of the owed merge
   // the epilogue warp's combine weights: NPH per query head (NPH * HQ = CW * G)
   static constexpr int EWW_BYTES = 256;
+  static constexpr int SC_BYTES = BS ? 256 : 0;  // block scales, 16 bytes per stage
   // merge scratch: one weight per (piece, query head), up to MERGE_MAX_PIECES
   static constexpr int MERGE_FLOATS = 2048;
   static constexpr int MERGE_MAX_PIECES = MERGE_FLOATS / HQ - 1;  // + one row of 1 / sums
   static constexpr int MERGE_BYTES = MERGE_FLOATS * 4;
   static constexpr int NST_FIT =
-      (kDecodeSmemBudget - 1024 - RED_BYTES - MERGE_BYTES - CTL_BYTES - EWW_BYTES) /
+      (kDecodeSmemBudget - 1024 - RED_BYTES - MERGE_BYTES - CTL_BYTES - EWW_BYTES - SC_BYTES) /
       (STAGE_BYTES + 16);
   static constexpr int NST_CAP = NST_FIT > 12 ? 12 : NST_FIT;
   // The ring is a multiple of 2 (each slot is always filled by the same one
@@ -200,7 +214,8 @@ struct DecodeShape {
   static constexpr int NST = NST_CAP - NST_CAP % RING_MULT;
   // +1024: the dynamic smem base is realigned to 1024 bytes for the swizzle
   static constexpr int SMEM =
-      1024 + NST * STAGE_BYTES + RED_BYTES + MERGE_BYTES + NST * 16 + CTL_BYTES + EWW_BYTES;
+      1024 + NST * STAGE_BYTES + RED_BYTES + MERGE_BYTES + NST * 16 + CTL_BYTES + EWW_BYTES +
+      SC_BYTES;
   static_assert(NST >= RING_MULT && NST % RING_MULT == 0, "stage ring does not fit");
   static_assert(CW % HKV == 0, "unsupported kv head count");
   static_assert(SMEM <= kDecodeSmemBudget, "shared memory over budget");
@@ -211,6 +226,7 @@ struct DecodeShape {
   static_assert((NPH + 1) * HQ <= MERGE_FLOATS, "combine weights do not fit");
   static_assert(CW * G * 4 <= EWW_BYTES, "epilogue warp weights do not fit");
   static_assert(!(F8 && ROPE), "rotary embedding is fused for bf16 pools only");
+  static_assert(!BS || (F8 && NST * 16 <= SC_BYTES), "block scales: FP8 pools, 16 bytes a stage");
   static_assert(PF_W + (PF_PIECES + 1) * HQ <= DEF_W && DEF_W + 512 <= MERGE_FLOATS,
                 "prefetched lse and owed-merge weights do not fit the merge scratch");
   static_assert(DEF_MAX_PIECES >= 1, "owed-merge weights do not fit");
@@ -438,6 +454,29 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The HKV scale bytes of a block (1, 2, 4 or 8, at a multiple of HKV bytes
+// from a base aligned to 8).
+template <int HKV>
+__device__ __forceinline__ void load_scale_bytes(const uint8_t *src, uint32_t (&w)[2]) {
+  if constexpr (HKV == 8) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+    w[0] = x.x;
+    w[1] = x.y;
+  } else if constexpr (HKV == 4) {
+    w[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+  } else if constexpr (HKV == 2) {
+    w[0] = __ldg(reinterpret_cast<const uint16_t *>(src));
+  } else {
+    w[0] = __ldg(src);
+  }
 }
 
 // Byte offset of (row, 16-byte chunk) in a tile written by TMA with the
@@ -835,11 +874,12 @@ __device__ bool merge_sequence_bulk(const DecodeParams &p, int b, long long c0, 
 
 // SPLIT_MERGE: cut pieces only write their partials; merge_kernel, launched
 // behind this kernel, merges them (no counters, no merges in this kernel).
-template <int G, int HKV, bool F8 = false, bool ROPE = false, bool SPLIT_MERGE = false>
+template <int G, int HKV, bool F8 = false, bool ROPE = false, bool SPLIT_MERGE = false,
+          bool BS = false>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const DecodeParams p) {
-  using S = DecodeShape<G, HKV, F8, ROPE>;
+  using S = DecodeShape<G, HKV, F8, ROPE, BS>;
   extern __shared__ uint8_t smem_raw[];
   // realign to 1024 bytes: the 128-byte swizzle pattern repeats every 1 KB
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -851,6 +891,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   uint64_t *empty = full + S::NST;
   DecodeCtl *ctl = reinterpret_cast<DecodeCtl *>(empty + S::NST);
   float *eww = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ctl) + S::CTL_BYTES);
+  // block scales of the ring's stages (BS), 16 bytes each
+  const uint32_t scale0 = smem_addr(eww) + S::EWW_BYTES;
   volatile int *abort_flag = &ctl->abort;
 
   const int tid = threadIdx.x;
@@ -1080,6 +1122,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         wait_prev_then_release();
         waited = true;
       }
+      // BS: lane L loads the scale bytes of block L (K's Hkv bytes in sk, V's
+      // in sv); they are needed only when a stage is armed, behind its copies
+      uint32_t sk[2] = {0u, 0u}, sv[2] = {0u, 0u};
+      if constexpr (BS) {
+        if (phys >= 0 && phys < p.num_blocks) {
+          load_scale_bytes<HKV>(p.k_bscale + phys * HKV, sk);
+          load_scale_bytes<HKV>(p.v_bscale + phys * HKV, sv);
+        }
+      }
       // the q rows go with the first NPH stages of every piece: each consumer
       // warp reads them from its own first stage of the piece
       const bool with_q = min(gb + lane - lo, (long long)lj) < S::NPH;
@@ -1103,6 +1154,32 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const uint32_t dst = stage0 + st * S::STAGE_BYTES;
         const uint32_t bar = full0 + 8 * st;
         const bool pre = i < n_early;  // K/V already requested and counted
+        if constexpr (BS) {
+          // raise the expected bytes, issue the copies, then write the scales
+          // and arrive: the loads of the scales and the copies overlap
+          if (lane == 0 && q_i) mbar_expect_tx(bar, S::Q_BYTES);
+          __syncwarp();
+          if (!pre) issue_kv_stage(st, ph_i, true);
+          if (q_i)
+            bulk_load_elect(dst + 2 * S::KV_BYTES, q_base + (long long)b_i * S::HQ * kHeadDim,
+                            S::Q_BYTES, bar, pol_q);
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            w[x] = __shfl_sync(0xffffffffu, sk[x], i);
+            w[2 + x] = __shfl_sync(0xffffffffu, sv[x], i);
+          }
+          if (lane == 0) {
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(scale0 + 16 * st),
+                         "r"(clamp_scales4(w[0])), "r"(clamp_scales4(w[1])),
+                         "r"(clamp_scales4(w[2])), "r"(clamp_scales4(w[3]))
+                         : "memory");
+            mbar_arrive(bar);
+            if (!ok) report(p.err, row_i ? PA_DEVERR_BLOCK_INDEX : PA_DEVERR_SHAPE);
+          }
+          __syncwarp();
+          continue;
+        }
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, (ok && !pre ? 2u * S::KV_BYTES : 0u) +
                                          (q_i ? S::Q_BYTES + S::ROPE_BYTES : 0u));
@@ -1432,7 +1509,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       // read the FP8 scales
       cons_waited = true;
       wait_prev_then_release();
-      if constexpr (F8) {
+      if constexpr (F8 && !BS) {
         cl2 *= __ldg(p.k_scale + g);
         vsc = __ldg(p.v_scale + g);
       }
@@ -1709,10 +1786,23 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           // scaled scores (base 2): [0] (token tok0, head 2qd) [1] (tok0, 2qd+1)
           // [2] (tok1, 2qd) [3] (tok1, 2qd+1); keys past the end are -inf
           const bool v0 = tok0 < valid, v1 = tok1 < valid;
-          const float s0 = v0 ? (sa[0] + sb[0]) * cl2 : -INFINITY;
-          const float s1 = v0 ? (sa[1] + sb[1]) * cl2 : -INFINITY;
-          const float s2 = v1 ? (sa[2] + sb[2]) * cl2 : -INFINITY;
-          const float s3 = v1 ? (sa[3] + sb[3]) * cl2 : -INFINITY;
+          // (BS: with the block's K scale, plus the exponent of its V scale)
+          float s0, s1, s2, s3, inv_v = 1.f;
+          if constexpr (BS) {
+            const int bk = (int)lds8(scale0 + 16 * sidx + g);
+            const int bv = (int)lds8(scale0 + 16 * sidx + 8 + g);
+            const float ck = cl2 * scale_of(bk), ev = (float)(bv - kScaleBias);
+            inv_v = inv_scale_of(bv);
+            s0 = v0 ? fmaf(sa[0] + sb[0], ck, ev) : -INFINITY;
+            s1 = v0 ? fmaf(sa[1] + sb[1], ck, ev) : -INFINITY;
+            s2 = v1 ? fmaf(sa[2] + sb[2], ck, ev) : -INFINITY;
+            s3 = v1 ? fmaf(sa[3] + sb[3], ck, ev) : -INFINITY;
+          } else {
+            s0 = v0 ? (sa[0] + sb[0]) * cl2 : -INFINITY;
+            s1 = v0 ? (sa[1] + sb[1]) * cl2 : -INFINITY;
+            s2 = v1 ? (sa[2] + sb[2]) * cl2 : -INFINITY;
+            s3 = v1 ? (sa[3] + sb[3]) * cl2 : -INFINITY;
+          }
           float x0 = fmaxf(s0, s2), x1 = fmaxf(s1, s3);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
@@ -1738,8 +1828,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
           const float p0 = exp2f(s0 - m0), p1 = exp2f(s1 - m1);
           const float p2 = exp2f(s2 - m0), p3 = exp2f(s3 - m1);
-          l0 += p0 + p2;
-          l1 += p1 + p3;
+          if constexpr (BS) {
+            l0 = fmaf(p0 + p2, inv_v, l0);
+            l1 = fmaf(p1 + p3, inv_v, l1);
+          } else {
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+          }
           // P^T fragments: bf16 hi + lo split, or with F8 pools one f16
           // term (11-bit significand, far finer than the E4M3 values it
           // weighs)
@@ -1822,7 +1917,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (!piece_last) continue;
 
       // ---- end of a piece: merge the warps of each kv head, write rows -------
-      if constexpr (F8) {
+      if constexpr (F8 && !BS) {
         // the V scale of this warp's kv head, once per piece
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt)
@@ -2158,10 +2253,11 @@ consumers_done:
   }
 }
 
-// Launches decode_kernel<G, HKV, F8, ROPE, SPLIT_MERGE> for one G (defined per
-// HKV and variant in pa_decode_h*.cu, pa_decode_f8_h*.cu, pa_decode_rope_h*.cu
-// and, with SPLIT_MERGE, pa_decode_sm_h{4,8}.cu and pa_decode_f8_sm_h{4,8}.cu).
-template <int HKV, bool F8, bool ROPE = false, bool SPLIT_MERGE = false>
+// Launches decode_kernel<G, HKV, F8, ROPE, SPLIT_MERGE, BS> for one G (defined
+// per HKV and variant in pa_decode_h*.cu, pa_decode_f8_h*.cu, pa_decode_rope_h*.cu,
+// pa_decode_f8b_h*.cu (BS) and, with SPLIT_MERGE, pa_decode_sm_h{4,8}.cu,
+// pa_decode_f8_sm_h{4,8}.cu and pa_decode_f8b_sm_h{4,8}.cu).
+template <int HKV, bool F8, bool ROPE = false, bool SPLIT_MERGE = false, bool BS = false>
 cudaError_t launch_decode(int G, const CUtensorMap &tk, const CUtensorMap &tv,
                           const DecodeParams &p, cudaStream_t s, int device, bool pdl);
 

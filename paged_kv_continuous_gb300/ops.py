@@ -34,7 +34,8 @@ EXPORTED = (
     "pa_decode_default_splits", "pa_decode", "pa_decode_merge", "pa_prefill_varlen",
     "pa_decode_noalloc", "pa_rope_store_kv", "pa_store_kv_fp8", "pa_decode_fp8",
     "pa_store_decode", "pa_store_decode_fp8", "pa_prefill_store_varlen",
-    "pa_rope_store_decode", "pa_get_device_error", "pa_copy",
+    "pa_rope_store_decode", "pa_get_device_error", "pa_copy", "pa_store_kv_fp8_block",
+    "pa_decode_fp8_block",
 )
 
 
@@ -86,6 +87,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_store_kv_fp8.restype = i32
     lib.pa_store_kv_fp8.argtypes = [P, P, i64, i64, i64, i64, i64, P, P, P, P, i64, i32, i32,
                                     i32, P, P, u32, P]
+    lib.pa_store_kv_fp8_block.restype = i32
+    lib.pa_store_kv_fp8_block.argtypes = [P, P, i64, i64, i64, i64, P, i32, i32, P, P, P, P, i64,
+                                          i32, i32, i32, P, i32, P, P, u32, P]
+    lib.pa_decode_fp8_block.restype = i32
+    lib.pa_decode_fp8_block.argtypes = [P, i32, P, P, P, P, P, i64, P, i32, P, i32, i32, i32,
+                                        i32, i32, f32, i32, P, sz, u32, P]
     lib.pa_decode_merge.restype = i32
     lib.pa_decode_merge.argtypes = [P, i32, P, sz, P, i32, i32, i32, i32, i32, P]
     lib.pa_decode_noalloc.restype = i32
@@ -568,6 +575,166 @@ def store_decode_fp8(q, new_k, new_v, k_cache, v_cache, k_scale, v_scale, slot_m
                                    _decode_flags(pdl, early_kv), _stream(stream)),
            "pa_store_decode_fp8")
     return out
+
+
+class _Prepared:
+    """A prepared call: the tensors are checked once and the marshalled
+    arguments kept, so each call is one foreign call.  The caller updates the
+    tensors' contents in place between calls and keeps their storage; the
+    call is enqueued on ``stream`` (default: the current stream of the
+    tensors' device, which also becomes the device of the launch)."""
+
+    def _prepare(self, fn, what, args, keep, result=None):
+        self._fn, self._what, self._keep, self._result = fn, what, keep, result
+        # (pinned host memory, which the device reaches, counts for none)
+        devices = {t.device for t in keep if t is not None and t.is_cuda}
+        if len(devices) != 1:
+            raise PagedAttentionError(f"{what}: tensors on different devices")
+        self._device = devices.pop().index
+        # marshalled once: a call converts nothing but the stream
+        self._args = tuple(a if t is None else t(a) for a, t in zip(args, fn.argtypes))
+
+    def __call__(self, stream=None):
+        device = self._device
+        here = torch.cuda.current_device()
+        handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        if here == device:
+            status = self._fn(*self._args, handle)
+        else:
+            with torch.cuda.device(device):
+                status = self._fn(*self._args, handle)
+        if status != PA_OK:
+            _check(status, self._what)
+        return self._result
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need_contiguous(t, dtype, name, shape=None, dims=None):
+    _need(t, dtype, name, dims)
+    if not t.is_contiguous():
+        raise PagedAttentionError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise PagedAttentionError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_error_flags(t):
+    if t is not None:
+        _need(t, torch.int32, "error_flags")
+        if t.numel() < 1:
+            raise PagedAttentionError("error_flags must hold an int32 word")
+
+
+def _need_tables(block_tables, context_lens, batch):
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _need_contiguous(context_lens, torch.int32, "context_lens", (batch,))
+    if block_tables.shape[0] < batch:
+        raise PagedAttentionError("block_tables needs one row per sequence")
+    if batch and (block_tables.shape[1] < 1 or block_tables.stride(1) != 1 or
+                  block_tables.stride(0) < block_tables.shape[1]):
+        raise PagedAttentionError("block_tables rows must be contiguous and apart")
+
+
+def fp8_block_pools(num_blocks, num_kv_heads, head_dim=128, block_size=16, device=None):
+    """Empty block-scaled FP8 pools: K and V as ``fp8_pools``, and the scale
+    bytes k_scale / v_scale (uint8 [NB, Hkv], biased exponents)."""
+    k, v = fp8_pools(num_blocks, num_kv_heads, head_dim, block_size, device)
+    ks, vs = (torch.empty((num_blocks, num_kv_heads), dtype=torch.uint8, device=device)
+              for _ in range(2))
+    return k, v, ks, vs
+
+
+def _need_fp8_block_pools(k_cache, v_cache, k_scale, v_scale):
+    _need_contiguous(k_cache, torch.uint8, "k_cache", dims=4)
+    NB, bs, Hkv, D = k_cache.shape
+    _need_contiguous(v_cache, torch.uint8, "v_cache", (NB, Hkv, D, bs))
+    _need_contiguous(k_scale, torch.uint8, "k_scale", (NB, Hkv))
+    _need_contiguous(v_scale, torch.uint8, "v_scale", (NB, Hkv))
+    return NB, bs, Hkv, D
+
+
+class StoreKvFp8BlockCall(_Prepared):
+    """A prepared pa_store_kv_fp8_block (arguments as ``store_kv_fp8_block``)."""
+
+    def __init__(self, k, v, k_cache, v_cache, k_scale, v_scale, cu_seqlens, block_tables,
+                 context_lens, error_flags=None, pdl=False):
+        NB, bs, Hkv, D = _need_fp8_block_pools(k_cache, v_cache, k_scale, v_scale)
+        _need(k, torch.bfloat16, "k", 3)
+        _need(v, torch.bfloat16, "v", 3)
+        if tuple(k.shape[1:]) != (Hkv, D) or v.shape != k.shape:
+            raise PagedAttentionError("shape mismatch between k/v and the pools")
+        if k.numel() and (k.stride(2) != 1 or v.stride(2) != 1):
+            raise PagedAttentionError("k/v need a unit stride along head_dim")
+        _need_contiguous(cu_seqlens, torch.int32, "cu_seqlens", dims=1)
+        B = cu_seqlens.shape[0] - 1
+        if B < 0:
+            raise PagedAttentionError("cu_seqlens needs num_seqs + 1 entries")
+        _need_tables(block_tables, context_lens, B)
+        _need_error_flags(error_flags)
+        self._prepare(
+            lib.pa_store_kv_fp8_block, "pa_store_kv_fp8_block",
+            (_address(k), _address(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+             _address(cu_seqlens), B, k.shape[0], _address(k_cache), _address(v_cache),
+             _address(k_scale), _address(v_scale), NB, bs, Hkv, D, _address(block_tables),
+             block_tables.stride(0), _address(context_lens), _address(error_flags),
+             PA_LAUNCH_PDL if pdl else 0),
+            (k, v, k_cache, v_cache, k_scale, v_scale, cu_seqlens, block_tables, context_lens,
+             error_flags))
+
+
+def store_kv_fp8_block(k, v, k_cache, v_cache, k_scale, v_scale, cu_seqlens, block_tables,
+                       context_lens, error_flags=None, stream=None, pdl=False):
+    """pa_store_kv_fp8_block: append k/v bf16 [T, Hkv, D] (any token/head
+    strides, unit dim stride), packed by cu_seqlens (int32 [B + 1]), as the
+    last positions of sequences of context_lens (int32 [B], the new tokens
+    included), to block-scaled FP8 pools (see fp8_block_pools)."""
+    StoreKvFp8BlockCall(k, v, k_cache, v_cache, k_scale, v_scale, cu_seqlens, block_tables,
+                        context_lens, error_flags, pdl)(stream)
+
+
+class DecodeFp8BlockCall(_Prepared):
+    """A prepared pa_decode_fp8_block (arguments as ``decode_fp8_block``); the
+    output tensor and, if none is given, the workspace are kept with it."""
+
+    def __init__(self, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                 out, num_splits=0, workspace=None, pdl=False, early_kv=False):
+        NB, bs, Hkv, D = _need_fp8_block_pools(k_cache, v_cache, k_scale, v_scale)
+        _need_contiguous(q, torch.bfloat16, "q", dims=3)
+        B, Hq, Dq = q.shape
+        if Dq != D:
+            raise PagedAttentionError("q and the pools differ in head_dim")
+        _need_tables(block_tables, context_lens, B)
+        code = _out_code(out.dtype)
+        if not (out.is_cuda or out.is_pinned()):
+            raise PagedAttentionError("out must be a CUDA tensor or pinned host memory")
+        if out.shape != q.shape or not out.is_contiguous():
+            raise PagedAttentionError("out must be a contiguous [B, Hq, D] tensor")
+        if workspace is None:
+            workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+        _need_contiguous(workspace, workspace.dtype, "workspace")
+        self.out, self.workspace = out, workspace
+        self._prepare(
+            lib.pa_decode_fp8_block, "pa_decode_fp8_block",
+            (_address(out), code, _address(q), _address(k_cache), _address(v_cache),
+             _address(k_scale), _address(v_scale), NB, _address(block_tables),
+             block_tables.stride(0), _address(context_lens), B, Hq, Hkv, D, bs, float(scale),
+             int(num_splits), _address(workspace), workspace.numel() * workspace.element_size(),
+             _decode_flags(pdl, early_kv)),
+            (q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace),
+            out)
+
+
+def decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                     out=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None,
+                     stream=None, pdl=False, early_kv=False):
+    """pa_decode_fp8_block: q bf16 [B, Hq, D] over block-scaled FP8 pools
+    (see fp8_block_pools); returns out [B, Hq, D]."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    return DecodeFp8BlockCall(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                              scale, out, num_splits, workspace, pdl, early_kv)(stream)
 
 
 def decode_merge(out, workspace, context_lens, num_splits, block_size=16, stream=None):
