@@ -19,6 +19,8 @@
  * decodes over it and pa_store_decode_fp8 does both for a decode step.  A
  * second FP8 cache has scales that follow the data, one per (block, kv head):
  * pa_store_kv_fp8_block appends to it and pa_decode_fp8_block decodes over it.
+ * Pages of any of the caches are managed by pa_fork_pages, pa_free_pages,
+ * pa_compact_pages and pa_copy_pages.
  *
  * Sources (web pages that describe the method):
  *   [EAS] koas-w, "errors and solutions" (Qwen2.5-1.5B inference from
@@ -114,12 +116,13 @@ typedef int32_t pa_status;
 #define PA_DEVERR_WAIT_TIMEOUT 4  /* a pipeline wait gave up after ~2 s */
 #define PA_DEVERR_SHAPE 8         /* context_lens / cu_seqlens inconsistent */
 #define PA_DEVERR_POSITION 16     /* a position outside the rotary tables */
+#define PA_DEVERR_PAGES 32        /* no free page left, or a page freed that nobody holds */
 
 /*
  * Launch flags (the `flags` argument of pa_store_kv, pa_store_kv_fp8,
  * pa_rope_store_kv, pa_decode, pa_store_decode, pa_rope_store_decode,
- * pa_decode_fp8, pa_store_decode_fp8, pa_decode_noalloc, pa_store_kv_fp8_block
- * and pa_decode_fp8_block).  Any other bit returns PA_ERR_INVALID_ARG.
+ * pa_decode_fp8, pa_store_decode_fp8, pa_decode_noalloc, pa_store_kv_fp8_block,
+ * pa_decode_fp8_block and the page operators).  Any other bit returns PA_ERR_INVALID_ARG.
  *
  * PA_LAUNCH_PDL: programmatic dependent launch.  The call's kernel may begin
  * while the kernel launched just before it on the same stream is still
@@ -636,6 +639,102 @@ PA_API pa_status pa_decode_noalloc(void *out, int32_t out_dtype, const void *q,
                                    int32_t head_dim, int32_t block_size, float scale,
                                    int32_t num_splits, int32_t *error_flags, uint32_t flags,
                                    void *stream);
+
+/*
+ * Pages shared by reference counts ([EAS] "KV Cache 管理": one global pool of
+ * blocks that sequences hold through their block tables; the page names no
+ * sharing).  Sequences are rows of a table: block_tables int32
+ * [num_rows][block_table_stride], context_lens int32 [num_rows], where a
+ * length below 1 is an empty row, and row r holds the pages of its first
+ * ceil(context_lens[r] / block_size) entries.  ref_counts int32 [num_blocks]
+ * counts the entries that hold each page; a count below 1 is a free page, and
+ * the counts are the allocator's whole state.  The caller keeps one such
+ * table for all layers: a page index stands for that page of every pool of
+ * every layer.  A row that is written to (pa_store_kv* and the fused stores)
+ * must hold its last, part-filled page alone: fork does that.  The operators
+ * change the tables on the device and read nothing back; a call must not
+ * overlap another that uses the same tables.  Results do not depend on the
+ * order in which threads run.  Arrays are 4-byte aligned; flags: 0 or
+ * PA_LAUNCH_PDL (nothing is read before the wait).
+ *
+ * pa_copy_pages -- for every pair i < n and every pool, page dst[i] becomes a
+ * copy of page src[i], n = num_pairs, or min(num_pairs, *count) where the
+ * device word `count` is given.  A pair with src[i] < 0 is skipped; another
+ * index outside [0, num_blocks) sets PA_DEVERR_BLOCK_INDEX and skips its
+ * pair.  A page that is a dst must be no other pair's src or dst.  `pools` is
+ * a HOST array, read before the call returns: the base address (device
+ * memory) and page size in bytes of each pool, num_blocks pages each (K, V
+ * and scale arrays of every layer; bases and sizes that are multiples of 16
+ * move fastest).  A null base or a page size outside [1, 2^31] returns
+ * PA_ERR_INVALID_ARG.
+ */
+typedef struct {
+  void *base;
+  int64_t page_bytes;
+} pa_page_pool;
+PA_API pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools, int64_t num_blocks,
+                               const int32_t *src, const int32_t *dst, int32_t num_pairs,
+                               const int32_t *count, int32_t *error_flags, uint32_t flags,
+                               void *stream);
+
+/*
+ * pa_fork_pages -- row children[i] becomes a copy of row parents[i], for i <
+ * num_forks: the parent's full pages are shared (their counts grow), and a
+ * part-filled last page is replaced by a free page of its own, which
+ * copy_src[i] -> copy_dst[i] names for pa_copy_pages (-1, -1: none).  The
+ * forks take the lowest free pages in the order of i.  forked[i] is the
+ * child's context length.  A fork is refused (forked[i] = -1, its child is
+ * left empty, the others proceed) when a row is outside [0, num_rows) or
+ * parent and child are the same, when the child is not empty or is the child
+ * of an earlier fork of the call, or when the parent's context does not fit
+ * its table row (all PA_DEVERR_SHAPE); and when no free page is left
+ * (PA_DEVERR_PAGES).  A parent that is empty when the call begins gives an
+ * empty child, whatever else the call does to it.  Table entries past the
+ * child's pages are left as they are.  An entry outside the pool is copied
+ * and reported (PA_DEVERR_BLOCK_INDEX).
+ *   copy_src, copy_dst, forked   int32 [num_forks], written.
+ */
+PA_API pa_status pa_fork_pages(int32_t *block_tables, int32_t block_table_stride,
+                               int32_t *context_lens, int32_t num_rows, const int32_t *parents,
+                               const int32_t *children, int32_t num_forks, int32_t *ref_counts,
+                               int64_t num_blocks, int32_t block_size, int32_t *copy_src,
+                               int32_t *copy_dst, int32_t *forked, int32_t *error_flags,
+                               uint32_t flags, void *stream);
+
+/*
+ * pa_free_pages -- rows seqs[0 .. num_seqs) let their pages go (each entry's
+ * count falls by one) and become empty (context_lens = 0).  An empty row is
+ * skipped, a row named twice is freed once.  A row outside [0, num_rows) or a
+ * context past its table row sets PA_DEVERR_SHAPE, an entry outside the pool
+ * PA_DEVERR_BLOCK_INDEX, and a page whose count is below 1 already
+ * PA_DEVERR_PAGES (the count stays).
+ */
+PA_API pa_status pa_free_pages(int32_t *block_tables, int32_t block_table_stride,
+                               int32_t *context_lens, int32_t num_rows, const int32_t *seqs,
+                               int32_t num_seqs, int32_t *ref_counts, int64_t num_blocks,
+                               int32_t block_size, int32_t *error_flags, uint32_t flags,
+                               void *stream);
+
+/*
+ * pa_compact_pages -- plans the move of the L live pages into [0, L): the k-th
+ * live page at or past L moves to the k-th free page before L (both
+ * ascending), copy_src[k] -> copy_dst[k] for pa_copy_pages, with counts[0]
+ * the number of moves and counts[1] = L.  remap[p] is where page p went (p
+ * itself if it stays).  ref_counts and the held entries of every row are
+ * brought up to date; the pages' contents move with pa_copy_pages, before
+ * anything reads them through the new tables.
+ *   copy_src, copy_dst  int32 [num_blocks / 2], written (-1 past the moves).
+ *   counts              int32 [2], written.
+ *   remap               int32 [num_blocks], written.
+ * A context past its table row sets PA_DEVERR_SHAPE (its entries in the row
+ * are remapped), an entry outside the pool PA_DEVERR_BLOCK_INDEX (it stays).
+ */
+PA_API pa_status pa_compact_pages(int32_t *block_tables, int32_t block_table_stride,
+                                  const int32_t *context_lens, int32_t num_rows,
+                                  int32_t *ref_counts, int64_t num_blocks, int32_t block_size,
+                                  int32_t *copy_src, int32_t *copy_dst, int32_t *counts,
+                                  int32_t *remap, int32_t *error_flags, uint32_t flags,
+                                  void *stream);
 
 /*
  * pa_prefill_varlen -- causal varlen attention over a paged prefix ([MVT]

@@ -28,6 +28,7 @@ DEVERR_SLOT_INDEX = 2
 DEVERR_WAIT_TIMEOUT = 4
 DEVERR_SHAPE = 8
 DEVERR_POSITION = 16
+DEVERR_PAGES = 32
 
 EXPORTED = (
     "pa_abi_version", "pa_status_string", "pa_store_kv", "pa_decode_workspace_size",
@@ -35,7 +36,8 @@ EXPORTED = (
     "pa_decode_noalloc", "pa_rope_store_kv", "pa_store_kv_fp8", "pa_decode_fp8",
     "pa_store_decode", "pa_store_decode_fp8", "pa_prefill_store_varlen",
     "pa_rope_store_decode", "pa_get_device_error", "pa_copy", "pa_store_kv_fp8_block",
-    "pa_decode_fp8_block",
+    "pa_decode_fp8_block", "pa_copy_pages", "pa_fork_pages", "pa_free_pages",
+    "pa_compact_pages",
 )
 
 
@@ -93,6 +95,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_decode_fp8_block.restype = i32
     lib.pa_decode_fp8_block.argtypes = [P, i32, P, P, P, P, P, i64, P, i32, P, i32, i32, i32,
                                         i32, i32, f32, i32, P, sz, u32, P]
+    lib.pa_copy_pages.restype = i32
+    lib.pa_copy_pages.argtypes = [P, i32, i64, P, P, i32, P, P, u32, P]
+    lib.pa_fork_pages.restype = i32
+    lib.pa_fork_pages.argtypes = [P, i32, P, i32, P, P, i32, P, i64, i32, P, P, P, P, u32, P]
+    lib.pa_free_pages.restype = i32
+    lib.pa_free_pages.argtypes = [P, i32, P, i32, P, i32, P, i64, i32, P, u32, P]
+    lib.pa_compact_pages.restype = i32
+    lib.pa_compact_pages.argtypes = [P, i32, P, i32, P, i64, i32, P, P, P, P, P, u32, P]
     lib.pa_decode_merge.restype = i32
     lib.pa_decode_merge.argtypes = [P, i32, P, sz, P, i32, i32, i32, i32, i32, P]
     lib.pa_decode_noalloc.restype = i32
@@ -735,6 +745,164 @@ def decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, contex
         out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     return DecodeFp8BlockCall(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                               scale, out, num_splits, workspace, pdl, early_kv)(stream)
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
+class PagePools:
+    """The pools whose pages move together (K, V and scale tensors of every
+    layer, any dtype): contiguous CUDA tensors with one page per index of the
+    first dimension, checked once.  Keeps the tensors alive."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        if not self.tensors:
+            raise PagedAttentionError("PagePools needs at least one pool")
+        self.num_blocks = self.tensors[0].shape[0] if self.tensors[0].dim() else 0
+        self.array = (_PagePool * len(self.tensors))()
+        for entry, t in zip(self.array, self.tensors):
+            if not t.is_cuda or not t.is_contiguous() or t.dim() < 1:
+                raise PagedAttentionError("pools must be contiguous CUDA tensors")
+            if t.shape[0] != self.num_blocks:
+                raise PagedAttentionError("pools must have the same number of pages")
+            if t.numel() == 0:
+                raise PagedAttentionError("pools must not be empty")
+            entry.base = t.data_ptr()
+            entry.page_bytes = t.numel() // self.num_blocks * t.element_size()
+
+
+class CopyPagesCall(_Prepared):
+    """A prepared pa_copy_pages (arguments as ``copy_pages``)."""
+
+    def __init__(self, pools, src, dst, count=None, error_flags=None, pdl=False):
+        _need_contiguous(src, torch.int32, "src", dims=1)
+        _need_contiguous(dst, torch.int32, "dst", src.shape)
+        if count is not None:
+            _need_contiguous(count, torch.int32, "count")
+            if count.numel() < 1:
+                raise PagedAttentionError("count must hold an int32 word")
+        _need_error_flags(error_flags)
+        self.pools = pools
+        self._prepare(
+            lib.pa_copy_pages, "pa_copy_pages",
+            (ctypes.addressof(pools.array), len(pools.tensors), pools.num_blocks, _address(src),
+             _address(dst), src.shape[0], _address(count), _address(error_flags),
+             PA_LAUNCH_PDL if pdl else 0),
+            (*pools.tensors, src, dst, count, error_flags))
+
+
+def copy_pages(pools, src, dst, count=None, error_flags=None, stream=None, pdl=False):
+    """pa_copy_pages: in every pool of ``pools`` (a PagePools), page dst[i]
+    becomes a copy of page src[i] (int32 [n]; src[i] < 0: skipped); with
+    ``count`` (int32 CUDA tensor) only the first count[0] pairs."""
+    CopyPagesCall(pools, src, dst, count, error_flags, pdl)(stream)
+
+
+def _need_rows(block_tables, context_lens, ref_counts, error_flags):
+    _need(block_tables, torch.int32, "block_tables", 2)
+    rows = block_tables.shape[0]
+    if rows and (block_tables.shape[1] < 1 or block_tables.stride(1) != 1 or
+                 (rows > 1 and block_tables.stride(0) < block_tables.shape[1])):
+        raise PagedAttentionError("block_tables rows must be contiguous and apart")
+    _need_contiguous(context_lens, torch.int32, "context_lens", (rows,))
+    _need_contiguous(ref_counts, torch.int32, "ref_counts", dims=1)
+    _need_error_flags(error_flags)
+    return rows, ref_counts.shape[0]
+
+
+def _i32_out(t, n, name, like):
+    if t is None:
+        return torch.empty(n, dtype=torch.int32, device=like.device)
+    _need_contiguous(t, torch.int32, name, (n,))
+    return t
+
+
+class ForkPagesCall(_Prepared):
+    """A prepared pa_fork_pages (arguments as ``fork_pages``); ``copy_src``,
+    ``copy_dst`` and ``forked`` hold the results of the latest call."""
+
+    def __init__(self, block_tables, context_lens, parents, children, ref_counts, copy_src=None,
+                 copy_dst=None, forked=None, error_flags=None, pdl=False, block_size=16):
+        rows, NB = _need_rows(block_tables, context_lens, ref_counts, error_flags)
+        _need_contiguous(parents, torch.int32, "parents", dims=1)
+        n = parents.shape[0]
+        _need_contiguous(children, torch.int32, "children", (n,))
+        self.copy_src = _i32_out(copy_src, n, "copy_src", parents)
+        self.copy_dst = _i32_out(copy_dst, n, "copy_dst", parents)
+        self.forked = _i32_out(forked, n, "forked", parents)
+        result = (self.copy_src, self.copy_dst, self.forked)
+        self._prepare(
+            lib.pa_fork_pages, "pa_fork_pages",
+            (_address(block_tables), block_tables.stride(0), _address(context_lens), rows,
+             _address(parents), _address(children), n, _address(ref_counts), NB, block_size,
+             *map(_address, result), _address(error_flags), PA_LAUNCH_PDL if pdl else 0),
+            (block_tables, context_lens, parents, children, ref_counts, *result, error_flags),
+            result)
+
+
+def fork_pages(block_tables, context_lens, parents, children, ref_counts, copy_src=None,
+               copy_dst=None, forked=None, error_flags=None, stream=None, pdl=False):
+    """pa_fork_pages: row children[i] of the tables becomes a copy of row
+    parents[i] (int32 [n]) that shares its full pages; the part-filled last
+    page gets a free page, to be filled by ``copy_pages(pools, copy_src,
+    copy_dst)``.  Returns (copy_src, copy_dst, forked), int32 [n] each."""
+    return ForkPagesCall(block_tables, context_lens, parents, children, ref_counts, copy_src,
+                         copy_dst, forked, error_flags, pdl)(stream)
+
+
+class FreePagesCall(_Prepared):
+    """A prepared pa_free_pages (arguments as ``free_pages``)."""
+
+    def __init__(self, block_tables, context_lens, seqs, ref_counts, error_flags=None, pdl=False,
+                 block_size=16):
+        rows, NB = _need_rows(block_tables, context_lens, ref_counts, error_flags)
+        _need_contiguous(seqs, torch.int32, "seqs", dims=1)
+        self._prepare(
+            lib.pa_free_pages, "pa_free_pages",
+            (_address(block_tables), block_tables.stride(0), _address(context_lens), rows,
+             _address(seqs), seqs.shape[0], _address(ref_counts), NB, block_size,
+             _address(error_flags), PA_LAUNCH_PDL if pdl else 0),
+            (block_tables, context_lens, seqs, ref_counts, error_flags))
+
+
+def free_pages(block_tables, context_lens, seqs, ref_counts, error_flags=None, stream=None,
+               pdl=False):
+    """pa_free_pages: rows seqs (int32 [n]) of the tables let their pages go
+    and become empty."""
+    FreePagesCall(block_tables, context_lens, seqs, ref_counts, error_flags, pdl)(stream)
+
+
+class CompactPagesCall(_Prepared):
+    """A prepared pa_compact_pages (arguments as ``compact_pages``);
+    ``copy_src``, ``copy_dst``, ``counts`` and ``remap`` hold the results of
+    the latest call."""
+
+    def __init__(self, block_tables, context_lens, ref_counts, copy_src=None, copy_dst=None,
+                 counts=None, remap=None, error_flags=None, pdl=False, block_size=16):
+        rows, NB = _need_rows(block_tables, context_lens, ref_counts, error_flags)
+        self.copy_src = _i32_out(copy_src, NB // 2, "copy_src", ref_counts)
+        self.copy_dst = _i32_out(copy_dst, NB // 2, "copy_dst", ref_counts)
+        self.counts = _i32_out(counts, 2, "counts", ref_counts)
+        self.remap = _i32_out(remap, NB, "remap", ref_counts)
+        result = (self.copy_src, self.copy_dst, self.counts, self.remap)
+        self._prepare(
+            lib.pa_compact_pages, "pa_compact_pages",
+            (_address(block_tables), block_tables.stride(0), _address(context_lens), rows,
+             _address(ref_counts), NB, block_size, *map(_address, result),
+             _address(error_flags), PA_LAUNCH_PDL if pdl else 0),
+            (block_tables, context_lens, ref_counts, *result, error_flags), result)
+
+
+def compact_pages(block_tables, context_lens, ref_counts, copy_src=None, copy_dst=None,
+                  counts=None, remap=None, error_flags=None, stream=None, pdl=False):
+    """pa_compact_pages: plan the move of the live pages to the front of the
+    pool and bring tables and counts up to date; ``copy_pages(pools, copy_src,
+    copy_dst, count=counts)`` then moves the contents.  Returns (copy_src,
+    copy_dst [NB / 2], counts [moves, live pages], remap [NB]), int32."""
+    return CompactPagesCall(block_tables, context_lens, ref_counts, copy_src, copy_dst, counts,
+                            remap, error_flags, pdl)(stream)
 
 
 def decode_merge(out, workspace, context_lens, num_splits, block_size=16, stream=None):
