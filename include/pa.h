@@ -18,7 +18,8 @@
  * FP8 (E4M3) KV cache: pa_store_kv_fp8 quantises into it, pa_decode_fp8
  * decodes over it and pa_store_decode_fp8 does both for a decode step.  A
  * second FP8 cache has scales that follow the data, one per (block, kv head):
- * pa_store_kv_fp8_block appends to it and pa_decode_fp8_block decodes over it.
+ * pa_store_kv_fp8_block appends to it, pa_decode_fp8_block and
+ * pa_prefill_fp8_block attend to it.
  * Pages of any of the caches are managed by pa_fork_pages, pa_free_pages,
  * pa_compact_pages and pa_copy_pages.
  *
@@ -799,6 +800,27 @@ PA_API pa_status pa_prefill_store_varlen(void *out, int32_t out_dtype, const voi
                                          int32_t num_kv_heads, int32_t head_dim,
                                          int32_t block_size, float scale, int32_t *error_flags,
                                          void *stream);
+
+/*
+ * pa_prefill_fp8_block -- pa_prefill_varlen over a block-scaled FP8 cache:
+ * causal varlen attention of the packed chunks over the values code *
+ * 2^(scale byte - 127).  Store the chunks with pa_store_kv_fp8_block first
+ * (their keys are read from the cache, as rounded there).  Arguments, outputs
+ * and errors as pa_prefill_varlen, plus k_scale / v_scale (uint8
+ * [num_blocks][num_kv_heads]).  Products run on the tensor cores in f16 with
+ * fp32 accumulation: codes are exact, q is rounded to f16 (exact for bf16
+ * magnitudes 2^-14 .. 65504, larger ones saturate) and the softmax weights to
+ * f16 (11 bits) after taking in the V scale of their block.  Rows past
+ * cu_seqlens[num_seqs] are neither read nor written.  A NaN code of a value
+ * reaches every row of the 64-key tile that holds it, earlier rows included.
+ */
+PA_API pa_status pa_prefill_fp8_block(
+    void *out, int32_t out_dtype, const void *q, const int32_t *cu_seqlens, int32_t num_seqs,
+    int32_t total_tokens, int32_t max_q_len, const void *k_cache, const void *v_cache,
+    const uint8_t *k_scale, const uint8_t *v_scale, int64_t num_blocks,
+    const int32_t *block_tables, int32_t block_table_stride, const int32_t *context_lens,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, float scale,
+    int32_t *error_flags, void *stream);
 
 #ifdef __cplusplus
 }

@@ -369,7 +369,11 @@ unsigned row_blocks(long long stride) {
   return (unsigned)(y < 1 ? 1 : y > 64 ? 64 : y);
 }
 
-bool misaligned4(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 3) != 0; }
+// Whether any of the int32 arrays does not start on a 4-byte boundary.
+template <typename... T>
+bool misaligned4(const T *...x) {
+  return ((reinterpret_cast<uintptr_t>(x) | ...) & 3) != 0;
+}
 
 }  // namespace
 }  // namespace pa
@@ -384,6 +388,7 @@ extern "C" pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools,
   if (flags & ~static_cast<uint32_t>(PA_LAUNCH_PDL)) return PA_ERR_INVALID_ARG;
   if (num_pools == 0 || num_pairs == 0) return PA_OK;
   if (!pools || !src || !dst) return PA_ERR_INVALID_ARG;
+  if (misaligned4(src, dst, count, error_flags)) return PA_ERR_INVALID_ARG;
   for (int i = 0; i < num_pools; ++i)
     if (!pools[i].base || pools[i].page_bytes < 1 || pools[i].page_bytes > (1ll << 31))
       return PA_ERR_INVALID_ARG;
@@ -447,7 +452,9 @@ extern "C" pa_status pa_fork_pages(int32_t *block_tables, int32_t block_table_st
   if (!block_tables || !context_lens || !parents || !children || !ref_counts || !copy_src ||
       !copy_dst || !forked || block_table_stride < 1)
     return PA_ERR_INVALID_ARG;
-  if (misaligned4(block_tables) || misaligned4(ref_counts)) return PA_ERR_INVALID_ARG;
+  if (misaligned4(block_tables, context_lens, parents, children, ref_counts, copy_src, copy_dst,
+                  forked, error_flags))
+    return PA_ERR_INVALID_ARG;
   ForkParams p{block_tables, block_table_stride, context_lens, num_rows, parents, children,
                num_forks, ref_counts, num_blocks, copy_src, copy_dst, forked, error_flags};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -472,6 +479,8 @@ extern "C" pa_status pa_free_pages(int32_t *block_tables, int32_t block_table_st
   if (num_seqs == 0) return PA_OK;
   if (!block_tables || !context_lens || !seqs || !ref_counts || block_table_stride < 1)
     return PA_ERR_INVALID_ARG;
+  if (misaligned4(block_tables, context_lens, seqs, ref_counts, error_flags))
+    return PA_ERR_INVALID_ARG;
   if (launch_kernel(free_pages_kernel, dim3((unsigned)num_seqs), dim3(256), 0,
                     static_cast<cudaStream_t>(stream), (flags & PA_LAUNCH_PDL) != 0, block_tables,
                     (long long)block_table_stride, context_lens, (int)num_rows, seqs, ref_counts,
@@ -494,6 +503,9 @@ extern "C" pa_status pa_compact_pages(int32_t *block_tables, int32_t block_table
   if (num_blocks > 0 && (!ref_counts || !remap)) return PA_ERR_INVALID_ARG;
   if (num_blocks > 1 && (!copy_src || !copy_dst)) return PA_ERR_INVALID_ARG;
   if (num_rows > 0 && (!block_tables || !context_lens || block_table_stride < 1))
+    return PA_ERR_INVALID_ARG;
+  if (misaligned4(block_tables, context_lens, ref_counts, copy_src, copy_dst, counts, remap,
+                  error_flags))
     return PA_ERR_INVALID_ARG;
   CompactParams p{block_tables, block_table_stride, context_lens, num_rows, ref_counts,
                   num_blocks, copy_src, copy_dst, counts, remap, error_flags};

@@ -37,7 +37,7 @@ EXPORTED = (
     "pa_store_decode", "pa_store_decode_fp8", "pa_prefill_store_varlen",
     "pa_rope_store_decode", "pa_get_device_error", "pa_copy", "pa_store_kv_fp8_block",
     "pa_decode_fp8_block", "pa_copy_pages", "pa_fork_pages", "pa_free_pages",
-    "pa_compact_pages",
+    "pa_compact_pages", "pa_prefill_fp8_block",
 )
 
 
@@ -95,6 +95,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_decode_fp8_block.restype = i32
     lib.pa_decode_fp8_block.argtypes = [P, i32, P, P, P, P, P, i64, P, i32, P, i32, i32, i32,
                                         i32, i32, f32, i32, P, sz, u32, P]
+    lib.pa_prefill_fp8_block.restype = i32
+    lib.pa_prefill_fp8_block.argtypes = [P, i32, P, P, i32, i32, i32, P, P, P, P, i64, P, i32, P,
+                                         i32, i32, i32, i32, f32, P, P]
     lib.pa_copy_pages.restype = i32
     lib.pa_copy_pages.argtypes = [P, i32, i64, P, P, i32, P, P, u32, P]
     lib.pa_fork_pages.restype = i32
@@ -745,6 +748,48 @@ def decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, contex
         out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     return DecodeFp8BlockCall(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                               scale, out, num_splits, workspace, pdl, early_kv)(stream)
+
+
+class PrefillFp8BlockCall(_Prepared):
+    """A prepared pa_prefill_fp8_block (arguments as
+    ``prefill_varlen_fp8_block``)."""
+
+    def __init__(self, q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tables,
+                 context_lens, scale, max_q_len, out, error_flags=None):
+        NB, bs, Hkv, D = _need_fp8_block_pools(k_cache, v_cache, k_scale, v_scale)
+        _need_contiguous(q, torch.bfloat16, "q", dims=3)
+        T, Hq, Dq = q.shape
+        if Dq != D:
+            raise PagedAttentionError("q and the pools differ in head_dim")
+        _need_contiguous(cu_seqlens, torch.int32, "cu_seqlens", dims=1)
+        B = cu_seqlens.shape[0] - 1
+        if B < 0:
+            raise PagedAttentionError("cu_seqlens needs num_seqs + 1 entries")
+        _need_tables(block_tables, context_lens, B)
+        code = _out_code(out.dtype)
+        _need_contiguous(out, out.dtype, "out", q.shape)
+        _need_error_flags(error_flags)
+        self.out = out
+        self._prepare(
+            lib.pa_prefill_fp8_block, "pa_prefill_fp8_block",
+            (_address(out), code, _address(q), _address(cu_seqlens), B, T, int(max_q_len),
+             _address(k_cache), _address(v_cache), _address(k_scale), _address(v_scale), NB,
+             _address(block_tables), block_tables.stride(0), _address(context_lens), Hq, Hkv, D,
+             bs, float(scale), _address(error_flags)),
+            (q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out,
+             error_flags), out)
+
+
+def prefill_varlen_fp8_block(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tables,
+                             context_lens, scale, max_q_len, out=None, out_dtype=torch.bfloat16,
+                             error_flags=None, stream=None):
+    """pa_prefill_fp8_block: q bf16 [T, Hq, D] packed by cu_seqlens (int32
+    [N + 1]) over block-scaled FP8 pools that hold the chunks' own keys too
+    (store_kv_fp8_block first); returns out [T, Hq, D]."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    return PrefillFp8BlockCall(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tables,
+                               context_lens, scale, max_q_len, out, error_flags)(stream)
 
 
 class _PagePool(ctypes.Structure):
