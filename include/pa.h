@@ -548,7 +548,8 @@ PA_API pa_status pa_decode_fp8(void *out, int32_t out_dtype, const void *q, cons
  *                  longer than its context or past its table row sets
  *                  PA_DEVERR_SHAPE, a table entry outside the pool sets
  *                  PA_DEVERR_BLOCK_INDEX; that sequence or block is skipped.
- *   flags          0 or PA_LAUNCH_PDL.
+ *   flags          0 or PA_LAUNCH_PDL; the kernel waits for the kernel before
+ *                  it first of all either way.
  * k_cache and v_cache must be 16-byte aligned.  A block written by two
  * sequences of one call is a caller error (fork it first: one of the results,
  * or a mix of both, ends up in it).
@@ -568,7 +569,10 @@ PA_API pa_status pa_store_kv_fp8_block(
  * tensor cores in f16 as in pa_decode_fp8 (codes exact, q rounded to f16);
  * the softmax weights are rounded to f16 (11 bits) after taking in the V
  * scale of their block, the scores, sums and outputs stay fp32.  Same
- * workspace, splits, flags and outputs as pa_decode (with
+ * workspace, flags and outputs as pa_decode, and the same splits for
+ * num_splits > 0; with num_splits = 0 the number of splits in use is
+ * min(pa_decode_default_splits, ceil(N / 10)), N being the blocks of all
+ * sequences (the workspace is that of pa_decode_default_splits).  (With
  * PA_LAUNCH_EARLY_KV the pools must not be written by the kernel before; the
  * scale arrays are read after it).  k_scale and v_scale must be 8-byte
  * aligned; NULL or unaligned: PA_ERR_INVALID_ARG.
@@ -656,7 +660,8 @@ PA_API pa_status pa_decode_noalloc(void *out, int32_t out_dtype, const void *q,
  * change the tables on the device and read nothing back; a call must not
  * overlap another that uses the same tables.  Results do not depend on the
  * order in which threads run.  Arrays are 4-byte aligned; flags: 0 or
- * PA_LAUNCH_PDL (nothing is read before the wait).
+ * PA_LAUNCH_PDL, which mean the same here: the kernels wait for the kernel
+ * before them first of all and let the one after them begin early.
  *
  * pa_copy_pages -- for every pair i < n and every pool, page dst[i] becomes a
  * copy of page src[i], n = num_pairs, or min(num_pairs, *count) where the

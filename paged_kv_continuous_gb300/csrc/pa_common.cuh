@@ -254,6 +254,13 @@ __device__ __forceinline__ long long split_begin(long long c, long long S, long 
   if (!split_light_tail(S, N)) return c * N / S;
   return N * split_weight_before(c, S) / split_weight_before(S, S);
 }
+// The splits in use of S when each is to take at least min_blocks of the N
+// blocks (0: all of them).
+__device__ __forceinline__ long long capped_splits(long long S, long long N, int min_blocks) {
+  if (min_blocks <= 0) return S;
+  const long long want = (N + min_blocks - 1) / min_blocks;
+  return want < 1 ? 1 : want < S ? want : S;
+}
 // The split holding global block x: the largest c with split_begin(c) <= x,
 // i.e. the largest c with W(c) <= floor(((x + 1) W(S) - 1) / N).
 __device__ __forceinline__ long long split_of_block(long long x, long long S, long long N) {

@@ -25,7 +25,13 @@ struct MergeParams {
   int batch;
   int num_q_heads;
   int num_splits;
+  int min_blocks = 0;  // block-scaled pools: blocks a split takes at least
 };
+
+// Blocks that a split of the block-scaled decode takes at least when the
+// caller leaves the split count to the library: fewer, and the merges of many
+// short pieces cost more than the streams they shorten.
+constexpr int kBlockScaleMinBlocks = 10;
 
 constexpr int kMergeWarps = 4;   // warps per (sequence, head) row, a quarter of its pieces each
 constexpr int kMergeChunk = 16;  // pieces whose loads are in flight together in one warp
@@ -107,7 +113,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergePara
   __shared__ float4 share_acc[kMergeWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x, h = blockIdx.y;
-  const long long S = p.num_splits;
   // N and the blocks before sequence b
   long long all = 0, before = 0;
   for (int x = tid; x < p.batch; x += 32 * kMergeWarps) {
@@ -131,6 +136,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergePara
     N += red[0][w];
     P += red[1][w];
   }
+  const long long S = capped_splits(p.num_splits, N, p.min_blocks);
   const int n = seq_blocks(p.context_lens, b);
   if (n == 0) return;
   const long long c0 = split_of_block(P, S, N), c1 = split_of_block(P + n - 1, S, N);
@@ -293,6 +299,8 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   p.k_pool8 = r.fp8 ? static_cast<uint8_t *>(const_cast<void *>(r.k_cache)) : nullptr;
   p.v_pool8 = r.fp8 ? static_cast<uint8_t *>(const_cast<void *>(r.v_cache)) : nullptr;
   p.early_kv = (r.flags & PA_LAUNCH_EARLY_KV) != 0;
+  p.wait_first = (r.flags & PA_LAUNCH_PDL) == 0;
+  p.min_blocks = r.num_splits == 0 ? kBlockScaleMinBlocks : 0;
   p.positions = r.positions;
   p.cos_table = r.cos_table;
   p.sin_table = r.sin_table;
@@ -302,7 +310,8 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
       cudaMemsetAsync(p.counters, 0, (size_t)r.splits * sizeof(int32_t), s) != cudaSuccess)
     return PA_ERR_LAUNCH;
   const int G = r.num_q_heads / r.num_kv_heads;
-  const bool pdl = (r.flags & PA_LAUNCH_PDL) != 0;
+  // (the block-scaled kernel waits first of all without the flag)
+  const bool pdl = (r.flags & PA_LAUNCH_PDL) != 0 || r.k_bscale != nullptr;
   // Few sequences over many splits (at least 8 per sequence) with 4 or 8 kv
   // heads: every cut sequence has many pieces of many query heads, and one
   // CTA merging them at the end of the decode kernel sets its end; merge
@@ -370,6 +379,7 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
     m.batch = r.batch;
     m.num_q_heads = r.num_q_heads;
     m.num_splits = r.splits;
+    if (r.k_bscale) m.min_blocks = p.min_blocks;
     if (launch_merge(m, s, true) != cudaSuccess) return PA_ERR_LAUNCH;
   }
   return PA_OK;

@@ -119,6 +119,11 @@ struct DecodeParams {
   // previous kernel in the stream completes (the caller guarantees that
   // kernel does not write the pools).
   int early_kv;
+  // BS kernels: nonzero: nothing is read before the previous kernel is over
+  // (the launch is a programmatic dependent one whatever the caller's flags)
+  int wait_first;
+  // BS kernels: blocks a split takes at least (0: as many splits as CTAs)
+  int min_blocks;
   // Rotary embedding inside the fused store (ROPE kernels): sequence b's new
   // token sits at position positions[b]; its q rows and its new K row are
   // rotated with row positions[b] of the float32 tables [max_position][64]
@@ -900,8 +905,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // is warp-uniform
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int lane = tid & 31;
-  const long long nsplit = p.num_splits;
+  long long nsplit = p.num_splits;
   const long long c = blockIdx.x;
+  if constexpr (BS) {
+    if (p.wait_first) griddep_wait();
+  }
 
   // ---- 1. block counts of all sequences: the total N, this CTA's block range
   //         [lo, hi) and the sequence that holds block lo.  One block-wide
@@ -941,6 +949,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         // last pass: N is known, and (one-pass batches) so is this
         // sequence's first block
         N = running;
+        if constexpr (BS) nsplit = capped_splits(nsplit, N, p.min_blocks);
         if (base == 0 && b < p.batch && n > 0) {
           const long long lo1 = split_begin(c, nsplit, N), hi1 = split_begin(c + 1, nsplit, N);
           const long long prefix = before + incl - n;
@@ -953,8 +962,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       __syncthreads();
     }
   }
-  const long long lo = N ? split_begin(c, nsplit, N) : 0;
-  const long long hi = N ? split_begin(c + 1, nsplit, N) : 0;
+  // (BS: no block for the CTAs past the splits in use)
+  const bool in_use = !BS || c < nsplit;
+  const long long lo = N && in_use ? split_begin(c, nsplit, N) : 0;
+  const long long hi = N && in_use ? split_begin(c + 1, nsplit, N) : 0;
   if (p.batch > (int)blockDim.x) {
     // second pass over the prefix sums (batches larger than one pass)
     long long running = 0;

@@ -5,6 +5,9 @@
 // state: a fork takes the lowest free pages, so results do not depend on the
 // order in which blocks of a launch run (the counts are integer sums).
 //
+// Every kernel here is launched as a programmatic dependent and waits for the
+// kernel before it first of all, which only moves its own set-up ahead.
+//
 // Fork and compact are planned by one block, since every pick depends on all
 // earlier ones (a scan over the counts); a second launch, spread over the
 // sequences, applies the plan.  Nothing is read back to the host: the plan's
@@ -170,6 +173,7 @@ struct ForkParams {
 // that names it until the plan is applied (a length below 1 reads as empty).
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams p) {
   griddep_wait();
+  griddep_launch_dependents();
   __shared__ int wsum[32];
   const int tid = threadIdx.x;
   volatile int32_t *ctx = p.ctx;
@@ -304,6 +308,7 @@ struct CompactParams {
 // k-th free page before L; both lists have the same length.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactParams p) {
   griddep_wait();
+  griddep_launch_dependents();
   __shared__ int wsum[32];
   const int tid = threadIdx.x;
   constexpr int kStep = kPlanThreads * kPlanPer;
@@ -396,7 +401,6 @@ extern "C" pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools,
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_DEVICE;
-  bool pdl = (flags & PA_LAUNCH_PDL) != 0;
   for (int first = 0; first < num_pools; first += kCopyPools) {
     const int n = num_pools - first < kCopyPools ? num_pools - first : kCopyPools;
     CopyPagesParams p = {};
@@ -429,9 +433,8 @@ extern "C" pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools,
     long long blocks = (units + kCopyWarps - 1) / kCopyWarps;
     if (blocks > 8ll * sms) blocks = 8ll * sms;
     if (launch_kernel(copy_pages_kernel, dim3((unsigned)blocks), dim3(32 * kCopyWarps), 0,
-                      static_cast<cudaStream_t>(stream), pdl, p) != cudaSuccess)
+                      static_cast<cudaStream_t>(stream), true, p) != cudaSuccess)
       return PA_ERR_LAUNCH;
-    pdl = true;  // the launches of one call touch different pools
   }
   return PA_OK;
 }
@@ -459,7 +462,7 @@ extern "C" pa_status pa_fork_pages(int32_t *block_tables, int32_t block_table_st
                num_forks, ref_counts, num_blocks, copy_src, copy_dst, forked, error_flags};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
-                    (flags & PA_LAUNCH_PDL) != 0, p) != cudaSuccess ||
+                    true, p) != cudaSuccess ||
       launch_kernel(fork_apply_kernel, dim3((unsigned)num_forks, row_blocks(block_table_stride)),
                     dim3(256), 0, s, true, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
@@ -482,7 +485,7 @@ extern "C" pa_status pa_free_pages(int32_t *block_tables, int32_t block_table_st
   if (misaligned4(block_tables, context_lens, seqs, ref_counts, error_flags))
     return PA_ERR_INVALID_ARG;
   if (launch_kernel(free_pages_kernel, dim3((unsigned)num_seqs), dim3(256), 0,
-                    static_cast<cudaStream_t>(stream), (flags & PA_LAUNCH_PDL) != 0, block_tables,
+                    static_cast<cudaStream_t>(stream), true, block_tables,
                     (long long)block_table_stride, context_lens, (int)num_rows, seqs, ref_counts,
                     (long long)num_blocks, error_flags) != cudaSuccess)
     return PA_ERR_LAUNCH;
@@ -511,7 +514,7 @@ extern "C" pa_status pa_compact_pages(int32_t *block_tables, int32_t block_table
                   num_blocks, copy_src, copy_dst, counts, remap, error_flags};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
-                    (flags & PA_LAUNCH_PDL) != 0, p) != cudaSuccess)
+                    true, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   if (num_rows > 0 &&
       launch_kernel(compact_apply_kernel,

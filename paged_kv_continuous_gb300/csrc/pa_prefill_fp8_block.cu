@@ -3,32 +3,42 @@
 //
 // One CTA computes a 128-row tile of one (sequence, kv head), rows being the
 // (query position, query head) pairs of 128 / G positions, over 64-key tiles:
-//   S   = Q C_k^T        f16 x f16 -> fp32 (C: codes, exact in f16)
-//   t   = c 2^ek S + ev  base-2 score plus the exponent of the key's V scale
-//   P'  = 2^(t - m)      with m the row's running reference of t
-//   O  += P' C_v         f16 x f16 -> fp32 in TMEM
-//   l  += 2^-ev P'       per 16-key page;        out = O / l.
-// Neither scale is applied to an element: K's goes into the page's constants
-// of the exponent, V's into its offset, so P' <= 256 carries weight times V
-// scale relative to the largest such product and one f16 term of it (11
-// bits) suffices for a 4-bit significand.  That halves the PV products of a
-// bf16 cache (whose weights take two bf16 terms) and its softmax's packing.
+//   S   = (Q_hi + Q_lo) C_k^T   e4m3 x e4m3 -> fp32 (C: codes)
+//   t   = c 2^(eq + ek) S + ev  base-2 score plus the exponent of V's scale
+//   P'  = 2^(t - m)             m the row's running reference of t
+//   O  += P' C_v                f16 x f16 -> fp32 in TMEM
+//   l  += 2^-ev P'              per 16-key page;        out = O / l.
+// Neither scale is applied to an element: K's goes into the page's factor of
+// the exponent, V's into its offset, so P' <= 256 carries weight times V
+// scale relative to the largest such product, and one f16 term of it (11
+// bits) suffices for a 4-bit significand.
 //
-// Codes are widened on the way into shared memory by two converter warps (K,
-// V), each with a rolling window of eight 16-byte loads per lane: a chunk is
-// requested as soon as the one eight before it is converted, so half an 8 KB
-// tile is always in flight per warp.  K pages (token-major)
-// give K-major rows of the score MMA; V pages are dim-major, [128 dims][16
-// tokens], which are K-major rows (a dim, 64 keys = 128 bytes) of the PV MMA
-// with no transpose.  Both land in the 128-byte swizzle, and the lanes are
-// laid over (row, chunk) so that a store instruction hits every bank once.
+// K codes feed the score MMA as they are: a query row times 2^-eq, its
+// largest magnitude in (224, 448], is the sum of two E4M3 terms.  A bf16 has 8
+// significant bits; the rounded first term leaves a remainder of at most 4
+// bits, which the second holds exactly wherever the element is at least
+// 2^-11 of the row's largest (below, the error is 2^-19 of the largest).  Two
+// passes at the FP8 rate cost what one f16 pass would, and K needs no
+// conversion: its pages arrive by TMA in the layout the MMA reads.
 //
-// Warps: 0 converts K, 2 converts V, 1 issues the score MMAs, 3 the PV MMAs,
-// 4 .. 7 run the softmax, a row per thread.  Two CTAs share an SM: one's
-// softmax runs while the other's MMAs use the tensor pipe.  A NaN or
-// infinite value of q or of a key reaches every row of the tiles that meet
-// it, those that do not attend to that key included (0 * NaN in the MMA).
+// V codes are widened to f16 by one warp, from a staging buffer that bulk
+// copies fill (a page of a head is 2 KB contiguous).  V pages are dim-major,
+// [128 dims][16 tokens]: K-major rows (a dim, 64 keys = 128 bytes) of the PV
+// MMA with no transpose, written in the 128-byte swizzle.  (A first form had
+// two warps widen K and V from plain loads: with half a tile in flight per
+// warp their latency set a step's time, 2.6 us.)
+//
+// Warps: 0 requests pages (K boxes, V staging) and scales, 2 widens V, 1
+// issues the score MMAs, 3 the PV MMAs, 4 .. 7 run the softmax, a row per
+// thread.  Two CTAs share an SM: one's softmax runs while the other's MMAs
+// use the tensor pipe.  A NaN code of a value reaches every row of the tiles
+// that meet it, those that do not attend to that key included (0 * NaN in the
+// MMA); a query row with a NaN or an infinity gives NaN.
 #include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include <cudaTypedefs.h>
 
 #include "pa_fp8_block.cuh"
 #include "pa_prefill_common.cuh"
@@ -39,25 +49,32 @@ namespace {
 constexpr int kQpThreads = 256;
 constexpr int kQpSoft = 128;                    // softmax threads
 constexpr int kQpPages = kPfKeys / kBlockSize;  // pages per KV tile
-constexpr int kQpKHalf = kPfKeys * 128;         // 64 keys x 64 dims, f16
-constexpr int kQpTile = 2 * kQpKHalf;           // one K or V tile, f16: 16 KB
-constexpr int kQpQHalf = kPfRows * 128;         // 128 rows x 64 dims of Q
-constexpr int kQpStages = 2;
-constexpr int kQpAhead = 8;  // chunks a converter lane requests ahead (of 16 in a tile)
-static_assert(16 % kQpAhead == 0, "a tile's chunks cycle through the window");
+constexpr int kQpCodes = kPfKeys * kHeadDim;    // one K or V tile of codes: 8 KB
+constexpr int kQpPage = kBlockSize * kHeadDim;  // one page of one head: 2 KB
+constexpr int kQpTile = 2 * kQpCodes;           // one V tile, f16: 128 dims x 64 keys
+constexpr int kQpQ = kPfRows * kHeadDim;        // one E4M3 term of Q: 128 rows x 128 bytes
+// three K stages (codes), two stages of V codes, two of widened V: 104 KB with
+// Q, under half an SM's
+constexpr int kQpKStages = 3, kQpVStages = 2;
 constexpr int kQpOffQ = 0;
-constexpr int kQpOffK = kQpOffQ + 2 * kQpQHalf;
-constexpr int kQpOffV = kQpOffK + kQpStages * kQpTile;
-constexpr int kQpOffBar = kQpOffV + kQpStages * kQpTile;
-// 8-byte slots: K full / empty, V full / empty (per stage), Q ready, two score,
-// two P and two PV barriers, four scale barriers, TMEM address, abort flag;
-// then the page scales of four tiles (K's four bytes, V's four)
-constexpr int kSlKFull = 0, kSlKEmpty = 2, kSlVFull = 4, kSlVEmpty = 6, kSlQ = 8, kSlS = 9,
-              kSlP = 11, kSlO = 13, kSlScale = 15, kSlTmem = 19, kSlAbort = 20, kSlScales = 21;
-constexpr int kQpBarBytes = 256;
-static_assert((kSlScales + 4) * 8 <= kQpBarBytes, "barrier slots do not fit");
+constexpr int kQpOffK = kQpOffQ + 2 * kQpQ;
+constexpr int kQpOffC = kQpOffK + kQpKStages * kQpCodes;  // V codes
+constexpr int kQpOffV = kQpOffC + kQpVStages * kQpCodes;
+constexpr int kQpOffBar = kQpOffV + kQpVStages * kQpTile;
+// 8-byte slots: K full / empty per stage, V codes full / empty, widened V full
+// / empty, Q ready, two score, two P and two PV barriers, eight scale
+// barriers, TMEM address, abort flag; then the page scales of eight tiles (K's
+// four bytes, V's four)
+constexpr int kSlKFull = 0, kSlKEmpty = kSlKFull + kQpKStages;
+constexpr int kSlCFull = kSlKEmpty + kQpKStages, kSlCEmpty = kSlCFull + 2;
+constexpr int kSlVFull = kSlCEmpty + 2, kSlVEmpty = kSlVFull + 2;
+constexpr int kSlQ = kSlVEmpty + 2, kSlS = kSlQ + 1, kSlP = kSlS + 2, kSlO = kSlP + 2;
+constexpr int kSlScale = kSlO + 2, kSlTmem = kSlScale + 8, kSlAbort = kSlTmem + 1;
+constexpr int kSlScales = kSlAbort + 1;
+constexpr int kQpBarBytes = 512;
+static_assert((kSlScales + 8) * 8 <= kQpBarBytes, "barrier slots do not fit");
 constexpr int kQpSmem = 1024 + kQpOffBar + kQpBarBytes;
-static_assert(kWorkOrderBytes <= kQpStages * kQpTile, "work-order scratch does not fit");
+static_assert(kWorkOrderBytes <= kQpKStages * kQpCodes, "work-order scratch does not fit");
 // TMEM (256 columns, two CTAs per SM): scores of tile j in buffer j % 2 at 0
 // and 64, P' over the scores it came from (32 columns, two keys each), O at 128
 constexpr int kQpTmemCols = 256, kQpTmemS = 64, kQpTmemO = 128;
@@ -68,7 +85,7 @@ struct PrefillQParams {
   const uint16_t *q;
   const int32_t *cu_seqlens;
   int num_seqs;
-  const uint8_t *k_cache, *v_cache;
+  const uint8_t *v_cache;
   const uint8_t *k_scale, *v_scale;
   long long num_blocks;
   const int32_t *block_tables;
@@ -80,10 +97,34 @@ struct PrefillQParams {
   int32_t *err;
 };
 
-// Instruction descriptor, kind::f16: f16 A and B (both K-major), fp32 D, M =
-// 128, N = n.
-__host__ __device__ constexpr uint32_t idesc_f16(int n) {
+// Instruction descriptor, fp32 D, M = 128, N = n, both operands K-major and of
+// format 0: f16 under kind::f16, e4m3 under kind::f8f6f4.
+__host__ __device__ constexpr uint32_t idesc_format0(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kPfRows >> 4) << 24);
+}
+
+// D (+)= A B with both operands described in shared memory, E4M3, K = 32.
+__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// bulk_load by one elected lane of a converged warp.
+__device__ __forceinline__ void bulk_load_warp(uint32_t dst, const void *src, uint32_t bytes,
+                                               uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t codes) {  // low two bytes
@@ -95,6 +136,21 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ float2 codes_to_float2(uint32_t codes) {  // low two bytes, exact
+  float lo, hi;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
+      "cvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(f16x2_of_codes(codes)));
+  return make_float2(lo, hi);
+}
+// Scale byte of a query row with largest magnitude a: as scale_for, over a
+// span wide enough for any row that matters (2^-100 .. 2^100).
+__device__ __forceinline__ int query_scale_for(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int byte = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(byte, kScaleBias - 100), kScaleBias + 100);
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                        uint32_t d) {
@@ -108,150 +164,167 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
-// A converter warp's stream of 64-key tiles of K (or V) of one (sequence, kv
-// head).  Chunk i of a tile (16 codes per lane) belongs to page i / 4 of the
-// tile; a page is four chunks: K token rows 4 (i % 4) .. + 3, or V dims
-// 32 (i % 4) .. + 31.  Pages with no key, and bad entries, read as zero codes.
-template <bool kIsV>
-__device__ __forceinline__ void convert_tiles(const PrefillQParams &p, const int32_t *row, int n,
-                                              int nkv, int g, uint32_t dst0, uint32_t b_full0,
-                                              uint32_t b_empty0, uint32_t b_scale0,
-                                              uint32_t scales0, volatile int *abort_flag) {
+// Warp 0: the pages and scales of tiles 0 .. nkv - 1 of (sequence, kv head).
+__device__ __forceinline__ void request_tiles(const PrefillQParams &p, const CUtensorMap *map,
+                                              const int32_t *row, int n, int nkv, int g,
+                                              uint32_t base, uint32_t slot0,
+                                              volatile int *abort_flag) {
   const int lane = threadIdx.x & 31;
-  // the lane's place in a chunk: K (row, 16-dim group), two rows and four
-  // groups per quarter warp; V dim row = lane
-  const int kr = ((lane >> 2) & 1) + 2 * (lane >> 4), kc = (lane & 3) + 4 * ((lane >> 3) & 1);
-  const long long row_bytes = (long long)p.hkv * kHeadDim;
-  const uint8_t *pool = kIsV ? p.v_cache + (long long)g * (kHeadDim * kBlockSize) + lane * kBlockSize
-                             : p.k_cache + (long long)g * kHeadDim + kr * row_bytes + kc * 16;
-  const long long page_bytes = row_bytes * kBlockSize;
-  const long long sub_bytes = kIsV ? 32 * kBlockSize : 4 * row_bytes;
-
-  // table entries of eight tiles (32 pages) per round of lane loads, the next
-  // round requested a tile ahead of its first use; -1: nothing to read
+  auto slot = [&](int i) { return slot0 + 8 * i; };
+  // table entries of eight tiles (32 pages) per round of lane loads; -1:
+  // nothing to read (no key, or a bad entry, which is reported)
   auto entries = [&](int j8) -> int {
     const int lb = j8 * 32 + lane;
     if (lb * kBlockSize >= n) return -1;
     const int ph = lb < p.bt_stride ? __ldg(row + lb) : -1;
     const bool ok = ph >= 0 && ph < p.num_blocks;
-    if (!ok && !kIsV) report(p.err, PA_DEVERR_BLOCK_INDEX);
+    if (!ok) report(p.err, PA_DEVERR_BLOCK_INDEX);
     return ok ? ph : -1;
   };
-  int round = entries(0);
-  uint4 buf[kQpAhead];
-  uint32_t scale = 0;  // lane pg < 4: scale byte of page pg of the tile in buf (K warp: V's << 8)
-  int now[kQpPages], next[kQpPages];  // pages of tile j and of the one after it
+  int round = -1;
+  // lane pg < 4: the scale bytes of page pg (K's, V's << 8) of the next tile
+  uint32_t next_scale = 0;
   auto load_scales = [&](int j) {
-    if constexpr (!kIsV) {
-      // both scales of the page, by the K warp (it feeds the softmax first)
-      const int ph = __shfl_sync(0xffffffffu, round, (j & 7) * kQpPages + (lane & 3));
-      scale = (uint32_t)kScaleBias * 0x101u;
-      if (lane < kQpPages && ph >= 0)
-        scale = (uint32_t)__ldg(p.k_scale + (long long)ph * p.hkv + g) |
-                ((uint32_t)__ldg(p.v_scale + (long long)ph * p.hkv + g) << 8);
-    }
+    if ((j & 7) == 0) round = entries(j >> 3);
+    const int ph = __shfl_sync(0xffffffffu, round, (j & 7) * kQpPages + (lane & 3));
+    next_scale = (uint32_t)kScaleBias * 0x101u;
+    if (lane < kQpPages && ph >= 0)
+      next_scale = (uint32_t)__ldg(p.k_scale + (long long)ph * p.hkv + g) |
+                   ((uint32_t)__ldg(p.v_scale + (long long)ph * p.hkv + g) << 8);
+    return ph;
   };
-  auto pages_of = [&](int j) {
+  int ph = load_scales(0);  // lane pg < 4: page pg of tile j
+  int k_asked = 0, c_asked = 0;  // tiles whose K, V pages were requested
+  for (int j = 0; j < nkv; ++j) {
+    const int mine = ph;
+    const uint32_t scale = next_scale;
+    if (j + 1 < nkv) ph = load_scales(j + 1);
+    const unsigned ok = __ballot_sync(0xffffffffu, lane < kQpPages && mine >= 0);
+    const uint32_t bytes = __popc(ok) * kQpPage;
+    const int ks = j % kQpKStages, vs = j & 1;
+    if (j >= kQpKStages &&
+        !__all_sync(0xffffffffu, mbar_wait(slot(kSlKEmpty + ks), (j / kQpKStages - 1) & 1,
+                                           abort_flag, p.err)))
+      break;
+    if (lane == 0) mbar_arrive_expect_tx(slot(kSlKFull + ks), bytes);
+    __syncwarp();
 #pragma unroll
     for (int pg = 0; pg < kQpPages; ++pg) {
-      now[pg] = next[pg];
-      next[pg] = __shfl_sync(0xffffffffu, round, (j & 7) * kQpPages + pg);
+      const int at = __shfl_sync(0xffffffffu, mine, pg);
+      if (at >= 0)
+        tma_load_3d(base + kQpOffK + ks * kQpCodes + pg * kQpPage, map, 0, g, at * kBlockSize,
+                    slot(kSlKFull + ks));
     }
-  };
-  // chunk i of the tile whose pages are now (i < 16) or next
-  auto load = [&](int i) {
-    const int ph = i < 16 ? now[i >> 2] : next[(i - 16) >> 2];
-    buf[i % kQpAhead] = ph >= 0 ? __ldg(reinterpret_cast<const uint4 *>(pool + ph * page_bytes +
-                                                             (i & 3) * sub_bytes))
-                     : make_uint4(0u, 0u, 0u, 0u);
-  };
+    k_asked = j + 1;
+    // the scales of tile j: slot j % 8, last read by the softmax of tile
+    // j - 8, which is over (the K stage's last reader, the score MMA of tile
+    // j - 3, waited for the PV of tile j - 5)
+    if (lane < kQpPages) {
+      const uint32_t c = clamp_scales4(scale & 0xFFFFu);
+      const uint32_t at = slot(kSlScales + (j & 7)) + lane;
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(c & 0xFFu) : "memory");
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + 4), "r"((c >> 8) & 0xFFu) : "memory");
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(slot(kSlScale + (j & 7)));
+    if (j >= kQpVStages &&
+        !__all_sync(0xffffffffu,
+                    mbar_wait(slot(kSlCEmpty + vs), ((j >> 1) - 1) & 1, abort_flag, p.err)))
+      break;
+    if (lane == 0) mbar_arrive_expect_tx(slot(kSlCFull + vs), bytes);
+    __syncwarp();
 #pragma unroll
-  for (int pg = 0; pg < kQpPages; ++pg) next[pg] = -1;
-  pages_of(0);
-  load_scales(0);
-#pragma unroll
-  for (int i = 0; i < kQpAhead; ++i) load(16 + i);
+    for (int pg = 0; pg < kQpPages; ++pg) {
+      const int at = __shfl_sync(0xffffffffu, mine, pg);
+      if (at >= 0)
+        bulk_load_warp(base + kQpOffC + vs * kQpCodes + pg * kQpPage,
+                       p.v_cache + ((long long)at * p.hkv + g) * kQpPage, kQpPage,
+                       slot(kSlCFull + vs));
+    }
+    c_asked = j + 1;
+  }
+  if (lane == 0 && *abort_flag) {
+    // copies in flight land before the CTA's shared memory is released
+    volatile int never = 0;
+    for (int i = max(k_asked - kQpKStages, 0); i < k_asked; ++i)
+      mbar_wait(slot(kSlKFull + i % kQpKStages), (i / kQpKStages) & 1, &never, nullptr);
+    for (int i = max(c_asked - kQpVStages, 0); i < c_asked; ++i)
+      mbar_wait(slot(kSlCFull + (i & 1)), (i >> 1) & 1, &never, nullptr);
+  }
+  __syncwarp();
+}
 
+// Warp 2: V codes of each tile to f16.  Chunk i (16 per lane) is page i / 4,
+// dims 32 (i % 4) .. + 31, one per lane: 16 tokens.
+__device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, int nkv,
+                                              uint32_t base, uint32_t slot0,
+                                              volatile int *abort_flag) {
+  const int lane = threadIdx.x & 31;
+  auto slot = [&](int i) { return slot0 + 8 * i; };
   for (int j = 0; j < nkv; ++j) {
     const int st = j & 1;
-    const bool more = j + 1 < nkv;
-    const uint32_t mine = scale;
-    if (more && ((j + 1) & 7) == 0) round = entries((j + 1) >> 3);
-    pages_of(j + 1);  // (past the last tile: loads nothing)
-    if (more) load_scales(j + 1);
-    if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(b_empty0 + 8 * st, ((j >> 1) - 1) & 1,
-                                                     abort_flag, p.err)))
-      return;
-    if constexpr (!kIsV) {
-      // the scales of tile j: slot j % 4, last read by the softmax of tile
-      // j - 4, which is over: the score MMA of tile j - 2 waited for its PV
-      const uint32_t c = clamp_scales4(mine & 0xFFFFu);
-      if (lane < kQpPages) {
-        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales0 + 8 * (j & 3) + lane), "r"(c & 0xFFu)
-                     : "memory");
-        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales0 + 8 * (j & 3) + 4 + lane),
-                     "r"((c >> 8) & 0xFFu)
-                     : "memory");
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_scale0 + 8 * (j & 3));
-    }
-    const uint32_t dst = dst0 + st * kQpTile;
-    const int key0 = j * kPfKeys;
+    bool ok = mbar_wait(slot(kSlCFull + st), (j >> 1) & 1, abort_flag, p.err);
+    if (ok && j >= kQpVStages)
+      ok = mbar_wait(slot(kSlVEmpty + st), ((j >> 1) - 1) & 1, abort_flag, p.err);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    const uint32_t from = base + kQpOffC + st * kQpCodes + 16 * lane;
+    const uint32_t to = base + kQpOffV + st * kQpTile + lane * 128;
+#pragma unroll 1
+    for (int pg = 0; pg < kQpPages; ++pg) {
+      uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint4 w = buf[i % kQpAhead];
-      if (i + kQpAhead < 16 || more) load(i + kQpAhead);
-      if constexpr (kIsV) {
-        // tokens past the last key weigh 0 and may hold anything: zero codes
-        const int left = n - (key0 + (i >> 2) * kBlockSize);
-        if (left < kBlockSize) {
-          uint32_t *x = &w.x;
+      for (int q = 0; q < 4; ++q) w[q] = lds128(from + pg * kQpPage + q * 512);
+      // tokens past the last key weigh 0 and may hold anything: zero codes
+      const int left = n - (j * kPfKeys + pg * kBlockSize);
+      if (left < kBlockSize) {
+        uint32_t mask[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int keep = min(max(left - 4 * q, 0), 4);
-            x[q] &= keep >= 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
-          }
+        for (int q = 0; q < 4; ++q) {
+          const int keep = min(max(left - 4 * q, 0), 4);
+          mask[q] = keep >= 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          w[q].x &= mask[0];
+          w[q].y &= mask[1];
+          w[q].z &= mask[2];
+          w[q].w &= mask[3];
         }
       }
-      const uint32_t a0 = f16x2_of_codes(w.x), a1 = f16x2_of_codes(w.x >> 16);
-      const uint32_t a2 = f16x2_of_codes(w.y), a3 = f16x2_of_codes(w.y >> 16);
-      const uint32_t b0 = f16x2_of_codes(w.z), b1 = f16x2_of_codes(w.z >> 16);
-      const uint32_t b2 = f16x2_of_codes(w.w), b3 = f16x2_of_codes(w.w >> 16);
-      uint32_t at;
-      int r, c;
-      if constexpr (kIsV) {
-        r = 32 * (i & 3) + lane;  // dim
-        c = 2 * (i >> 2);         // its 16 tokens: two 16-byte chunks
-        at = dst;
-      } else {
-        r = 16 * (i >> 2) + 4 * (i & 3) + kr;  // key
-        c = 2 * (kc & 3);
-        at = dst + (kc >> 2) * kQpKHalf;
+      // dim row 32 q + lane: chunks 2 pg and 2 pg + 1, swizzled by the row
+      const uint32_t c0 = ((2 * pg) ^ (lane & 7)) << 4, c1 = ((2 * pg + 1) ^ (lane & 7)) << 4;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sts128(to + q * 32 * 128 + c0, f16x2_of_codes(w[q].x), f16x2_of_codes(w[q].x >> 16),
+               f16x2_of_codes(w[q].y), f16x2_of_codes(w[q].y >> 16));
+        sts128(to + q * 32 * 128 + c1, f16x2_of_codes(w[q].z), f16x2_of_codes(w[q].z >> 16),
+               f16x2_of_codes(w[q].w), f16x2_of_codes(w[q].w >> 16));
       }
-      sts128(at + sw128(r, c), a0, a1, a2, a3);
-      sts128(at + sw128(r, c + 1), b0, b1, b2, b3);
     }
-    // visible to the tensor core before the tile is handed over
+    // the codes are read; the widened tile is visible to the tensor core
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_arrive(b_full0 + 8 * st);
+    mbar_arrive(slot(kSlCEmpty + st));
+    mbar_arrive(slot(kSlVFull + st));
   }
 }
 
 template <int G>
 __global__ void __launch_bounds__(kQpThreads, 2)
-    prefill_fp8_block_kernel(const __grid_constant__ PrefillQParams p) {
+    prefill_fp8_block_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                             const __grid_constant__ PrefillQParams p) {
   constexpr int PT = kPfRows / G;  // query positions per tile
+  // launched as a programmatic dependent: nothing is read or written before
+  // the kernel before it is over, and the kernel after it may be set up now
+  griddep_wait();
+  griddep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t base = smem_addr(smem);
   uint64_t *slots = reinterpret_cast<uint64_t *>(smem + kQpOffBar);
-  auto slot = [&](int i) { return smem_addr(slots + i); };
-  const uint32_t b_k_full0 = slot(kSlKFull), b_k_empty0 = slot(kSlKEmpty);
-  const uint32_t b_v_full0 = slot(kSlVFull), b_v_empty0 = slot(kSlVEmpty);
-  const uint32_t b_q = slot(kSlQ), b_s0 = slot(kSlS), b_p0 = slot(kSlP), b_o0 = slot(kSlO);
-  const uint32_t b_scale0 = slot(kSlScale), scales0 = slot(kSlScales);
+  const uint32_t slot0 = smem_addr(slots);
+  auto slot = [&](int i) { return slot0 + 8 * i; };
+  const uint32_t b_s0 = slot(kSlS), b_p0 = slot(kSlP), b_o0 = slot(kSlO);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(slots + kSlTmem);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(slots + kSlAbort);
 
@@ -288,17 +361,21 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   const int nkv = kmax / kPfKeys + 1;
 
   if (tid == 0) {
-    for (int i = 0; i < kQpStages; ++i) {
-      mbar_init(b_k_full0 + 8 * i, 32);
-      mbar_init(b_k_empty0 + 8 * i, 1);
-      mbar_init(b_v_full0 + 8 * i, 32);
-      mbar_init(b_v_empty0 + 8 * i, 1);
+    for (int i = 0; i < kQpKStages; ++i) {
+      mbar_init(slot(kSlKFull + i), 1);
+      mbar_init(slot(kSlKEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(slot(kSlCFull + i), 1);
+      mbar_init(slot(kSlCEmpty + i), 32);
+      mbar_init(slot(kSlVFull + i), 32);
+      mbar_init(slot(kSlVEmpty + i), 1);
       mbar_init(b_s0 + 8 * i, 1);
       mbar_init(b_p0 + 8 * i, kQpSoft);
       mbar_init(b_o0 + 8 * i, 1);
     }
-    mbar_init(b_q, kQpSoft);
-    for (int i = 0; i < 4; ++i) mbar_init(b_scale0 + 8 * i, 1);
+    mbar_init(slot(kSlQ), kQpSoft);
+    for (int i = 0; i < 8; ++i) mbar_init(slot(kSlScale + i), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -317,39 +394,37 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   const int32_t *row = p.block_tables + (long long)s * p.bt_stride;
 
   if (warp == 0) {
-    convert_tiles<false>(p, row, n, nkv, g, base + kQpOffK, b_k_full0, b_k_empty0, b_scale0,
-                         scales0, abort_flag);
+    request_tiles(p, &tmap_k, row, n, nkv, g, base, slot0, abort_flag);
   } else if (warp == 2) {
-    convert_tiles<true>(p, row, n, nkv, g, base + kQpOffV, b_v_full0, b_v_empty0, 0u, 0u,
-                        abort_flag);
+    widen_v_tiles(p, n, nkv, base, slot0, abort_flag);
   } else if (warp == 1 || warp == 3) {
     // ---- MMA issuers, each a whole converged warp: 1 issues S_j = Q K_j^T
     //      into buffer j & 1 once the PV of tile j - 2, which read that
     //      buffer, is done; 3 issues O += P'_j V_j ----
-    constexpr uint32_t idesc_qk = idesc_f16(kPfKeys), idesc_pv = idesc_f16(kHeadDim);
+    constexpr uint32_t idesc_qk = idesc_format0(kPfKeys), idesc_pv = idesc_format0(kHeadDim);
     constexpr unsigned kAll = 0xffffffffu;
     uint32_t last_bar = 0;  // barrier of this warp's latest commit (drained on abort)
     int last_par = 0;
     if (warp == 1) {
-      bool ok = __all_sync(kAll, mbar_wait(b_q, 0, abort_flag, p.err));
+      bool ok = __all_sync(kAll, mbar_wait(slot(kSlQ), 0, abort_flag, p.err));
       tc_fence_after();
       for (int j = 0; j < nkv && ok; ++j) {
-        const int b = j & 1, par = (j >> 1) & 1;
-        ok = __all_sync(kAll, mbar_wait(b_k_full0 + 8 * b, par, abort_flag, p.err));
+        const int b = j & 1, par = (j >> 1) & 1, ks = j % kQpKStages;
+        ok = __all_sync(kAll, mbar_wait(slot(kSlKFull + ks), (j / kQpKStages) & 1, abort_flag,
+                                        p.err));
         if (ok && j >= 2)
           ok = __all_sync(kAll, mbar_wait(b_o0 + 8 * b, par ^ 1, abort_flag, p.err));
         if (!ok) break;
         tc_fence_after();
+        // two terms of Q, 4 k-steps of 32 dims each
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_f16_ss(
-              tmem + b * kQpTmemS,
-              umma_desc(base + kQpOffQ + (ks >> 2) * kQpQHalf + (ks & 3) * 32, 16, 1024),
-              umma_desc(base + kQpOffK + b * kQpTile + (ks >> 2) * kQpKHalf + (ks & 3) * 32, 16,
-                        1024),
-              idesc_qk, ks > 0);
+        for (int i = 0; i < 8; ++i)
+          umma_f8_ss(tmem + b * kQpTmemS,
+                     umma_desc(base + kQpOffQ + (i >> 2) * kQpQ + (i & 3) * 32, 16, 1024),
+                     umma_desc(base + kQpOffK + ks * kQpCodes + (i & 3) * 32, 16, 1024),
+                     idesc_qk, i > 0);
         umma_commit(b_s0 + 8 * b);
-        umma_commit(b_k_empty0 + 8 * b);
+        umma_commit(slot(kSlKEmpty + ks));
         last_bar = b_s0 + 8 * b;
         last_par = par;
       }
@@ -357,7 +432,7 @@ __global__ void __launch_bounds__(kQpThreads, 2)
       for (int j = 0; j < nkv; ++j) {
         const int b = j & 1, par = (j >> 1) & 1;
         if (!__all_sync(kAll, mbar_wait(b_p0 + 8 * b, par, abort_flag, p.err))) break;
-        if (!__all_sync(kAll, mbar_wait(b_v_full0 + 8 * b, par, abort_flag, p.err))) break;
+        if (!__all_sync(kAll, mbar_wait(slot(kSlVFull + b), par, abort_flag, p.err))) break;
         tc_fence_after();
         // 4 k-steps of 16 keys: 32 bytes of every 128-byte dim row
 #pragma unroll
@@ -366,7 +441,7 @@ __global__ void __launch_bounds__(kQpThreads, 2)
                       umma_desc(base + kQpOffV + b * kQpTile + ks * 32, 16, 1024), idesc_pv,
                       (j > 0 || ks > 0) ? 1u : 0u);
         umma_commit(b_o0 + 8 * b);
-        umma_commit(b_v_empty0 + 8 * b);
+        umma_commit(slot(kSlVEmpty + b));
         last_bar = b_o0 + 8 * b;
         last_par = par;
       }
@@ -386,25 +461,51 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     const int limit = rvalid ? prefix + pos0 + rpos : -1;  // last key this row sees
     const uint32_t trow = (uint32_t)lb << 16;
     const long long orow = ((long long)(q0 + pos0 + rpos) * p.hq + g * G + hs) * kHeadDim;
+    float c_row, bad = 0.f;  // factor of the row's scores; NaN for a row that is not finite
     {
-      // the Q row, rounded to f16, into the K-major swizzled tile
+      // the Q row as two E4M3 terms of q 2^-eq, in the K-major swizzled tiles
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + orow);
       uint4 qv[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) qv[c] = rvalid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t top = 0;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
-        uint32_t h[4];
+        qv[c] = rvalid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t *w = &qv[c].x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 f = bf16x2_to_float2((w[i] & p.q_and) ^ p.q_xor);
-          h[i] = f16x2_of(f.x, f.y);
+          w[i] = (w[i] & p.q_and) ^ p.q_xor;
+          const uint32_t a = w[i] & 0x7FFF7FFFu;
+          top = max(top, max(a >> 16, a & 0xFFFFu));  // magnitudes order like their bits
         }
-        sts128(base + kQpOffQ + (c >> 3) * kQpQHalf + sw128(r, c & 7), h[0], h[1], h[2], h[3]);
+      }
+      if (top >= 0x7F80u) bad = __uint_as_float(0x7FC00000u);
+      const int eq = query_scale_for(__uint_as_float(top << 16));
+      const float inv = inv_scale_of(eq);
+      c_row = p.qk_scale_log2 * scale_of(eq);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {  // 16 dims
+        const uint32_t w[8] = {qv[2 * c].x,     qv[2 * c].y,     qv[2 * c].z,     qv[2 * c].w,
+                               qv[2 * c + 1].x, qv[2 * c + 1].y, qv[2 * c + 1].z, qv[2 * c + 1].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[2], r2[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 f = bf16x2_to_float2(w[2 * i + k]);
+            const float x = f.x * inv, y = f.y * inv;
+            h[k] = e4m3x2_of(x, y);
+            const float2 v = codes_to_float2(h[k]);
+            r2[k] = e4m3x2_of(x - v.x, y - v.y);
+          }
+          hi[i] = h[0] | (h[1] << 16);
+          lo[i] = r2[0] | (r2[1] << 16);
+        }
+        sts128(base + kQpOffQ + sw128(r, c), hi[0], hi[1], hi[2], hi[3]);
+        sts128(base + kQpOffQ + kQpQ + sw128(r, c), lo[0], lo[1], lo[2], lo[3]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(b_q);
+      mbar_arrive(slot(kSlQ));
     }
 
     // m: the row's reference of t; it moves only when a tile's largest t
@@ -414,13 +515,13 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     for (int j = 0; j < nkv && ok; ++j) {
       const int b = j & 1, par = (j >> 1) & 1;
       ok = __all_sync(0xffffffffu,
-                      mbar_wait(b_scale0 + 8 * (j & 3), (j >> 2) & 1, abort_flag, p.err) &&
+                      mbar_wait(slot(kSlScale + (j & 7)), (j >> 3) & 1, abort_flag, p.err) &&
                           mbar_wait(b_s0 + 8 * b, par, abort_flag, p.err));
       if (!ok) break;
       tc_fence_after();
       const uint32_t sb = tmem + b * kQpTmemS;
       const int key0 = j * kPfKeys;
-      const uint2 sc = lds64(scales0 + 8 * (j & 3));
+      const uint2 sc = lds64(slot(kSlScales + (j & 7)));
       float sv[2][32];
       tmem_ld64(sb + trow, sv);
       if (key0 + kPfKeys - 1 > prefix + pos0) {  // a row may not see every key
@@ -433,7 +534,7 @@ __global__ void __launch_bounds__(kQpThreads, 2)
 #pragma unroll
       for (int pg = 0; pg < kQpPages; ++pg) {
         // (at least the smallest normal: a masked -inf must stay -inf)
-        ck[pg] = fmaxf(p.qk_scale_log2 * scale_of((sc.x >> (8 * pg)) & 0xFF), 1.17549435e-38f);
+        ck[pg] = fmaxf(c_row * scale_of((sc.x >> (8 * pg)) & 0xFF), 1.17549435e-38f);
         ev[pg] = (float)((int)((sc.y >> (8 * pg)) & 0xFF) - kScaleBias);
         const float *x = &sv[pg >> 1][16 * (pg & 1)];
         const float a = fmax3(x[0], x[1], x[2]), c = fmax3(x[3], x[4], x[5]);
@@ -472,7 +573,7 @@ __global__ void __launch_bounds__(kQpThreads, 2)
       for (int pg = 0; pg < kQpPages; ++pg) {
         const float *x = &sv[pg >> 1][16 * (pg & 1)];
         const uint64_t c2 = pack_f32x2(ck[pg], ck[pg]);
-        const float off = ev[pg] + neg_m;
+        const float off = ev[pg] + neg_m + bad;
         const uint64_t o2 = pack_f32x2(off, off);
         uint64_t sum[2] = {0ull, 0ull};
         uint32_t h[8];
@@ -533,8 +634,32 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   }
 }
 
+// (dim 128, kv head, token slot) view of the K pool; one box = 128 dims x 1
+// head x 16 slots (one page of one head), 128-byte swizzle.
+bool k_pool_map(CUtensorMap *map, const void *pool, long long num_blocks, int hkv) {
+  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv, (cuuint64_t)num_blocks * kBlockSize};
+  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv * kHeadDim};
+  cuuint32_t box[3] = {(cuuint32_t)kHeadDim, 1, (cuuint32_t)kBlockSize};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int G>
-cudaError_t launch_prefill_q(const PrefillQParams &p, int max_q_len, cudaStream_t s, int device) {
+cudaError_t launch_prefill_q(const CUtensorMap &tk, const PrefillQParams &p, int max_q_len, cudaStream_t s, int device) {
   static std::atomic<bool> configured[64] = {};
   const cudaError_t e = set_smem_once(configured, prefill_fp8_block_kernel<G>, device, kQpSmem);
   if (e != cudaSuccess) return e;
@@ -543,7 +668,7 @@ cudaError_t launch_prefill_q(const PrefillQParams &p, int max_q_len, cudaStream_
                        100);
   constexpr int PT = kPfRows / G;
   const dim3 grid((max_q_len + PT - 1) / PT, p.hkv, p.num_seqs);
-  return launch_kernel(prefill_fp8_block_kernel<G>, grid, dim3(kQpThreads), kQpSmem, s, false, p);
+  return launch_kernel(prefill_fp8_block_kernel<G>, grid, dim3(kQpThreads), kQpSmem, s, true, tk, p);
 }
 
 }  // namespace
@@ -579,13 +704,15 @@ extern "C" pa_status pa_prefill_fp8_block(
     return PA_ERR_INVALID_ARG;
   int device = -1;
   if (cudaGetDevice(&device) != cudaSuccess) return PA_ERR_DEVICE;
+  CUtensorMap tk;
+  memset(&tk, 0, sizeof tk);
+  if (!k_pool_map(&tk, k_cache, num_blocks, num_kv_heads)) return PA_ERR_DEVICE;
   PrefillQParams p;
   p.out = out;
   p.out_f32 = out_dtype == PA_DTYPE_F32;
   p.q = static_cast<const uint16_t *>(q);
   p.cu_seqlens = cu_seqlens;
   p.num_seqs = num_seqs;
-  p.k_cache = static_cast<const uint8_t *>(k_cache);
   p.v_cache = static_cast<const uint8_t *>(v_cache);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
@@ -605,14 +732,14 @@ extern "C" pa_status pa_prefill_fp8_block(
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (num_q_heads / num_kv_heads) {
-    case 1: e = launch_prefill_q<1>(p, max_q_len, st, device); break;
-    case 2: e = launch_prefill_q<2>(p, max_q_len, st, device); break;
-    case 3: e = launch_prefill_q<3>(p, max_q_len, st, device); break;
-    case 4: e = launch_prefill_q<4>(p, max_q_len, st, device); break;
-    case 5: e = launch_prefill_q<5>(p, max_q_len, st, device); break;
-    case 6: e = launch_prefill_q<6>(p, max_q_len, st, device); break;
-    case 7: e = launch_prefill_q<7>(p, max_q_len, st, device); break;
-    default: e = launch_prefill_q<8>(p, max_q_len, st, device); break;
+    case 1: e = launch_prefill_q<1>(tk, p, max_q_len, st, device); break;
+    case 2: e = launch_prefill_q<2>(tk, p, max_q_len, st, device); break;
+    case 3: e = launch_prefill_q<3>(tk, p, max_q_len, st, device); break;
+    case 4: e = launch_prefill_q<4>(tk, p, max_q_len, st, device); break;
+    case 5: e = launch_prefill_q<5>(tk, p, max_q_len, st, device); break;
+    case 6: e = launch_prefill_q<6>(tk, p, max_q_len, st, device); break;
+    case 7: e = launch_prefill_q<7>(tk, p, max_q_len, st, device); break;
+    default: e = launch_prefill_q<8>(tk, p, max_q_len, st, device); break;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
 }

@@ -245,6 +245,6 @@ extern "C" pa_status pa_store_kv_fp8_block(
   const cudaError_t e = launch_kernel(
       vec ? store_kv_fp8_block_kernel<true> : store_kv_fp8_block_kernel<false>,
       dim3((unsigned)blocks), dim3(32 * kQsWarps), 0, static_cast<cudaStream_t>(stream),
-      (flags & PA_LAUNCH_PDL) != 0, p);
+      true, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
 }

@@ -590,6 +590,12 @@ def store_decode_fp8(q, new_k, new_v, k_cache, v_cache, k_scale, v_scale, slot_m
     return out
 
 
+# A device's current stream (as an address) and the current device, without
+# the wrapper objects that torch.cuda builds around them on every call
+_raw_stream = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None
+_current_device = torch._C._cuda_getDevice if torch.cuda.is_available() else None
+
+
 class _Prepared:
     """A prepared call: the tensors are checked once and the marshalled
     arguments kept, so each call is one foreign call.  The caller updates the
@@ -608,13 +614,11 @@ class _Prepared:
         self._args = tuple(a if t is None else t(a) for a, t in zip(args, fn.argtypes))
 
     def __call__(self, stream=None):
-        device = self._device
-        here = torch.cuda.current_device()
-        handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-        if here == device:
+        handle = _raw_stream(self._device) if stream is None else stream.cuda_stream
+        if _current_device() == self._device:
             status = self._fn(*self._args, handle)
         else:
-            with torch.cuda.device(device):
+            with torch.cuda.device(self._device):
                 status = self._fn(*self._args, handle)
         if status != PA_OK:
             _check(status, self._what)
