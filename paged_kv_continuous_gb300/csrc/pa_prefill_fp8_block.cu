@@ -24,16 +24,29 @@
 // V codes are widened to f16 by one warp, from a staging buffer that bulk
 // copies fill (a page of a head is 2 KB contiguous).  V pages are dim-major,
 // [128 dims][16 tokens]: K-major rows (a dim, 64 keys = 128 bytes) of the PV
-// MMA with no transpose, written in the 128-byte swizzle.  (A first form had
-// two warps widen K and V from plain loads: with half a tile in flight per
-// warp their latency set a step's time, 2.6 us.)
+// MMA with no transpose, written in the 128-byte swizzle.
 //
-// Warps: 0 requests pages (K boxes, V staging) and scales, 2 widens V, 1
-// issues the score MMAs, 3 the PV MMAs, 4 .. 7 run the softmax, a row per
-// thread.  Two CTAs share an SM: one's softmax runs while the other's MMAs
-// use the tensor pipe.  A NaN code of a value reaches every row of the tiles
-// that meet it, those that do not attend to that key included (0 * NaN in the
-// MMA); a query row with a NaN or an infinity gives NaN.
+// Warps: 0 requests pages (K boxes, V staging) and scales, 1 issues the score
+// MMAs, 3 the PV MMAs, 2 widens V, 4 .. 7 run the softmax, a row per thread.
+// Two CTAs share an SM: one's softmax runs while the other's MMAs use the
+// tensor pipe.
+//
+// What bounds it (two chunks of 2 k queries behind 15 k keys, Hq 32, Hkv 8:
+// 887 us, 1.10 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
+// 1700 cycles, of which the tensor pipe is busy about 1280 (the score MMAs at N
+// = 64 read their A and B tiles from shared memory at 48 cycles each, against
+// 16 of arithmetic), and the latency of the single warps' instruction streams
+// sets the rest; the last of four waves of CTAs is a sixth full.  Tried: two
+// warps widening K and V from plain loads into f16 tiles, 2068 us (the loads'
+// latency); scale bytes loaded tile by tile, 1366 us (the same, in warp 0); one
+// election per TMA or MMA and page loops, 1147 us; one issuer for both MMAs and
+// two widening warps, 1040 us; V requested by the widening warp, 1090 us, or by
+// the PV warp, 931 us; P' in a rolled loop that reads the scores twice, 1055 us;
+// the widening's loads a page ahead, 927 us.
+//
+// A NaN code of a value reaches every row of the tiles that meet it, those that
+// do not attend to that key included (0 * NaN in the MMA); a query row with a
+// NaN or an infinity gives NaN.
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -53,21 +66,21 @@ constexpr int kQpCodes = kPfKeys * kHeadDim;    // one K or V tile of codes: 8 K
 constexpr int kQpPage = kBlockSize * kHeadDim;  // one page of one head: 2 KB
 constexpr int kQpTile = 2 * kQpCodes;           // one V tile, f16: 128 dims x 64 keys
 constexpr int kQpQ = kPfRows * kHeadDim;        // one E4M3 term of Q: 128 rows x 128 bytes
-// three K stages (codes), two stages of V codes, two of widened V: 104 KB with
+// two K stages (codes), three stages of V codes, two of widened V: 104 KB with
 // Q, under half an SM's
-constexpr int kQpKStages = 3, kQpVStages = 2;
+constexpr int kQpKStages = 2, kQpCStages = 3, kQpVStages = 2;
 constexpr int kQpOffQ = 0;
 constexpr int kQpOffK = kQpOffQ + 2 * kQpQ;
 constexpr int kQpOffC = kQpOffK + kQpKStages * kQpCodes;  // V codes
-constexpr int kQpOffV = kQpOffC + kQpVStages * kQpCodes;
+constexpr int kQpOffV = kQpOffC + kQpCStages * kQpCodes;
 constexpr int kQpOffBar = kQpOffV + kQpVStages * kQpTile;
 // 8-byte slots: K full / empty per stage, V codes full / empty, widened V full
 // / empty, Q ready, two score, two P and two PV barriers, eight scale
 // barriers, TMEM address, abort flag; then the page scales of eight tiles (K's
 // four bytes, V's four)
 constexpr int kSlKFull = 0, kSlKEmpty = kSlKFull + kQpKStages;
-constexpr int kSlCFull = kSlKEmpty + kQpKStages, kSlCEmpty = kSlCFull + 2;
-constexpr int kSlVFull = kSlCEmpty + 2, kSlVEmpty = kSlVFull + 2;
+constexpr int kSlCFull = kSlKEmpty + kQpKStages, kSlCEmpty = kSlCFull + kQpCStages;
+constexpr int kSlVFull = kSlCEmpty + kQpCStages, kSlVEmpty = kSlVFull + 2;
 constexpr int kSlQ = kSlVEmpty + 2, kSlS = kSlQ + 1, kSlP = kSlS + 2, kSlO = kSlP + 2;
 constexpr int kSlScale = kSlO + 2, kSlTmem = kSlScale + 8, kSlAbort = kSlTmem + 1;
 constexpr int kSlScales = kSlAbort + 1;
@@ -103,29 +116,101 @@ __host__ __device__ constexpr uint32_t idesc_format0(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kPfRows >> 4) << 24);
 }
 
-// D (+)= A B with both operands described in shared memory, E4M3, K = 32.
-__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b,
-                                           uint32_t idesc, uint32_t accumulate) {
+// The helpers below are executed by a whole converged warp; each issues a run
+// of asynchronous instructions from one elected lane under a single election
+// (an election per instruction made up most of the issuing warp's time).
+//
+// S = (Q_hi + Q_lo) K^T: two terms of A (kQpQ bytes apart) and one B, E4M3,
+// four k-steps of 32 dims (32 bytes of each 128-byte row) each; then commits
+// to two barriers.  `a` and `b` are descriptors of the first k-step.
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                             uint32_t idesc, uint32_t bar0, uint32_t bar1) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred e, n, y;\n\t.reg .b64 a1, a2, a3, b1, b2, b3, c0, c1, c2, c3;\n\t"
+      "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "add.u64 c0, %1, %6;\n\tadd.u64 c1, a1, %6;\n\tadd.u64 c2, a2, %6;\n\t"
+      "add.u64 c3, a3, %6;\n\t"
+      "setp.ne.b32 n, 0, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, n;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c0, %2, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c1, b1, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c2, b2, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], c3, b3, %3, y;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(
+          d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(bar0), "r"(bar1), "n"(kQpQ >> 4)
       : "memory");
 }
 
-// bulk_load by one elected lane of a converged warp.
-__device__ __forceinline__ void bulk_load_warp(uint32_t dst, const void *src, uint32_t bytes,
-                                               uint32_t bar) {
+// O (+)= P' V: A in TMEM (8 columns per k-step of 16 keys), B of f16 rows of
+// 64 keys, four k-steps; then commits to two barriers.
+__device__ __forceinline__ void issue_values(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                             uint32_t idesc, uint32_t accumulate, uint32_t bar0,
+                                             uint32_t bar1) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\t"
+      "{\n\t.reg .pred e, n, y;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "setp.ne.b32 n, %4, 0;\n\tsetp.eq.b32 y, 0, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-      "[%3];\n\t}" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, n;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, y;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, y;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(bar0), "r"(bar1)
       : "memory");
 }
+
+// Four K pages (boxes at token slots z) to dst, kQpPage bytes apart.
+__device__ __forceinline__ void load_k_pages(uint32_t dst, const CUtensorMap *map, int g,
+                                             const int (&z)[4], uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 d1, d2, d3;\n\t"
+      "add.u32 d1, %0, 2048;\n\tadd.u32 d2, %0, 4096;\n\tadd.u32 d3, %0, 6144;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%7], 8192;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {0, %2, %3}], [%7];\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [d1], [%1, {0, %2, %4}], [%7];\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [d2], [%1, {0, %2, %5}], [%7];\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [d3], [%1, {0, %2, %6}], [%7];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(g), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]),
+      "r"(bar)
+      : "memory");
+}
+
+// Four V pages (2 KB each) to dst, kQpPage bytes apart.
+__device__ __forceinline__ void load_v_pages(uint32_t dst, const uint8_t *const (&v)[4],
+                                             uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 d1, d2, d3;\n\t"
+      "add.u32 d1, %0, 2048;\n\tadd.u32 d2, %0, 4096;\n\tadd.u32 d3, %0, 6144;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], 8192;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 2048, "
+      "[%5];\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [d1], [%2], 2048, "
+      "[%5];\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [d2], [%3], 2048, "
+      "[%5];\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [d3], [%4], 2048, "
+      "[%5];\n\t}" ::"r"(dst),
+      "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]), "r"(bar)
+      : "memory");
+}
+static_assert(kQpPage == 2048 && kQpCodes == 8192 && kQpPages == 4, "page loads");
 
 __device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t codes) {  // low two bytes
   uint32_t r;
@@ -164,111 +249,113 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
-// Warp 0: the pages and scales of tiles 0 .. nkv - 1 of (sequence, kv head).
+// Warp 0: the K pages (TMA boxes), the V pages (bulk copies: a page of a head
+// is contiguous) and the scales of tiles 0 .. nkv - 1 of (sequence, kv head
+// g).  The latency of this warp's own instructions can set the pace of the
+// whole tile loop, so a tile is one shape: four pages, always.  A page with no
+// key is page 0 in its place (nothing of it is used), and so is a bad entry,
+// which is reported (its rows are unspecified).  Table entries come eight
+// tiles (32 pages, one per lane) at a time, eight tiles ahead, and their
+// scales four tiles ahead.
 __device__ __forceinline__ void request_tiles(const PrefillQParams &p, const CUtensorMap *map,
                                               const int32_t *row, int n, int nkv, int g,
                                               uint32_t base, uint32_t slot0,
                                               volatile int *abort_flag) {
   const int lane = threadIdx.x & 31;
   auto slot = [&](int i) { return slot0 + 8 * i; };
-  // table entries of eight tiles (32 pages) per round of lane loads; -1:
-  // nothing to read (no key, or a bad entry, which is reported)
   auto entries = [&](int j8) -> int {
     const int lb = j8 * 32 + lane;
-    if (lb * kBlockSize >= n) return -1;
-    const int ph = lb < p.bt_stride ? __ldg(row + lb) : -1;
-    const bool ok = ph >= 0 && ph < p.num_blocks;
+    if (lb * kBlockSize >= n) return 0;
+    const int x = lb < p.bt_stride ? __ldg(row + lb) : -1;
+    const bool ok = x >= 0 && x < p.num_blocks;
     if (!ok) report(p.err, PA_DEVERR_BLOCK_INDEX);
-    return ok ? ph : -1;
+    return ok ? x : 0;
   };
-  int round = -1;
-  // lane pg < 4: the scale bytes of page pg (K's, V's << 8) of the next tile
-  uint32_t next_scale = 0;
-  auto load_scales = [&](int j) {
-    if ((j & 7) == 0) round = entries(j >> 3);
-    const int ph = __shfl_sync(0xffffffffu, round, (j & 7) * kQpPages + (lane & 3));
-    next_scale = (uint32_t)kScaleBias * 0x101u;
-    if (lane < kQpPages && ph >= 0)
-      next_scale = (uint32_t)__ldg(p.k_scale + (long long)ph * p.hkv + g) |
-                   ((uint32_t)__ldg(p.v_scale + (long long)ph * p.hkv + g) << 8);
-    return ph;
+  auto scales_of = [&](int x) -> uint32_t {  // K's byte, V's << 8
+    const long long at = (long long)x * p.hkv + g;
+    return (uint32_t)__ldg(p.k_scale + at) | ((uint32_t)__ldg(p.v_scale + at) << 8);
   };
-  int ph = load_scales(0);  // lane pg < 4: page pg of tile j
+  const uint8_t *v_head = p.v_cache + (long long)g * kQpPage;
+  const long long v_page = (long long)p.hkv * kQpPage;
+  int next = entries(0), ph = 0;
+  uint32_t next_sc = scales_of(next), sc = 0;
   int k_asked = 0, c_asked = 0;  // tiles whose K, V pages were requested
+  int st = 0, round = 0;         // stage of tile j's K pages, and its use
+  int cs = 0, cround = 0;        // the same of its V codes
   for (int j = 0; j < nkv; ++j) {
-    const int mine = ph;
-    const uint32_t scale = next_scale;
-    if (j + 1 < nkv) ph = load_scales(j + 1);
-    const unsigned ok = __ballot_sync(0xffffffffu, lane < kQpPages && mine >= 0);
-    const uint32_t bytes = __popc(ok) * kQpPage;
-    const int ks = j % kQpKStages, vs = j & 1;
-    if (j >= kQpKStages &&
-        !__all_sync(0xffffffffu, mbar_wait(slot(kSlKEmpty + ks), (j / kQpKStages - 1) & 1,
-                                           abort_flag, p.err)))
-      break;
-    if (lane == 0) mbar_arrive_expect_tx(slot(kSlKFull + ks), bytes);
-    __syncwarp();
+    if ((j & 7) == 0) {
+      ph = next;
+      sc = clamp_scales4(next_sc);
+      next = j + 8 < nkv ? entries((j >> 3) + 1) : 0;
+    } else if ((j & 7) == 4) {
+      next_sc = scales_of(next);
+    }
+    int z[4];
+    const uint8_t *v[4];
 #pragma unroll
     for (int pg = 0; pg < kQpPages; ++pg) {
-      const int at = __shfl_sync(0xffffffffu, mine, pg);
-      if (at >= 0)
-        tma_load_3d(base + kQpOffK + ks * kQpCodes + pg * kQpPage, map, 0, g, at * kBlockSize,
-                    slot(kSlKFull + ks));
+      const int x = __shfl_sync(0xffffffffu, ph, (j & 7) * kQpPages + pg);
+      z[pg] = x * kBlockSize;
+      v[pg] = v_head + x * v_page;
     }
+    if (round > 0 && !__all_sync(0xffffffffu, mbar_wait_soon(slot(kSlKEmpty + st),
+                                                             (round - 1) & 1, abort_flag, p.err)))
+      break;
+    load_k_pages(base + kQpOffK + st * kQpCodes, map, g, z, slot(kSlKFull + st));
     k_asked = j + 1;
+    if (++st == kQpKStages) {
+      st = 0;
+      ++round;
+    }
     // the scales of tile j: slot j % 8, last read by the softmax of tile
-    // j - 8, which is over (the K stage's last reader, the score MMA of tile
-    // j - 3, waited for the PV of tile j - 5)
-    if (lane < kQpPages) {
-      const uint32_t c = clamp_scales4(scale & 0xFFFFu);
-      const uint32_t at = slot(kSlScales + (j & 7)) + lane;
-      asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(c & 0xFFu) : "memory");
-      asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + 4), "r"((c >> 8) & 0xFFu) : "memory");
+    // j - 8, which is over (the K stage is free: the score MMA of tile j - 2
+    // waited for the PV of tile j - 4)
+    if ((lane >> 2) == (j & 7)) {
+      const uint32_t at = slot(kSlScales + (j & 7)) + (lane & 3);
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(sc & 0xFFu) : "memory");
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + 4), "r"((sc >> 8) & 0xFFu) : "memory");
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(slot(kSlScale + (j & 7)));
-    if (j >= kQpVStages &&
-        !__all_sync(0xffffffffu,
-                    mbar_wait(slot(kSlCEmpty + vs), ((j >> 1) - 1) & 1, abort_flag, p.err)))
-      break;
-    if (lane == 0) mbar_arrive_expect_tx(slot(kSlCFull + vs), bytes);
     __syncwarp();
-#pragma unroll
-    for (int pg = 0; pg < kQpPages; ++pg) {
-      const int at = __shfl_sync(0xffffffffu, mine, pg);
-      if (at >= 0)
-        bulk_load_warp(base + kQpOffC + vs * kQpCodes + pg * kQpPage,
-                       p.v_cache + ((long long)at * p.hkv + g) * kQpPage, kQpPage,
-                       slot(kSlCFull + vs));
-    }
+    if (cround > 0 &&
+        !__all_sync(0xffffffffu, mbar_wait_soon(slot(kSlCEmpty + cs), (cround - 1) & 1,
+                                                abort_flag, p.err)))
+      break;
+    load_v_pages(base + kQpOffC + cs * kQpCodes, v, slot(kSlCFull + cs));
     c_asked = j + 1;
+    if (++cs == kQpCStages) {
+      cs = 0;
+      ++cround;
+    }
   }
   if (lane == 0 && *abort_flag) {
     // copies in flight land before the CTA's shared memory is released
     volatile int never = 0;
     for (int i = max(k_asked - kQpKStages, 0); i < k_asked; ++i)
       mbar_wait(slot(kSlKFull + i % kQpKStages), (i / kQpKStages) & 1, &never, nullptr);
-    for (int i = max(c_asked - kQpVStages, 0); i < c_asked; ++i)
-      mbar_wait(slot(kSlCFull + (i & 1)), (i >> 1) & 1, &never, nullptr);
+    for (int i = max(c_asked - kQpCStages, 0); i < c_asked; ++i)
+      mbar_wait(slot(kSlCFull + i % kQpCStages), (i / kQpCStages) & 1, &never, nullptr);
   }
   __syncwarp();
 }
 
-// Warp 2: V codes of each tile to f16.  Chunk i (16 per lane) is page i / 4,
-// dims 32 (i % 4) .. + 31, one per lane: 16 tokens.
+// Warp 2: the V codes of each tile to f16.
 __device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, int nkv,
                                               uint32_t base, uint32_t slot0,
                                               volatile int *abort_flag) {
   const int lane = threadIdx.x & 31;
   auto slot = [&](int i) { return slot0 + 8 * i; };
+  int cs = 0, cround = 0;  // stage of the codes of tile j, and its use
   for (int j = 0; j < nkv; ++j) {
     const int st = j & 1;
-    bool ok = mbar_wait(slot(kSlCFull + st), (j >> 1) & 1, abort_flag, p.err);
-    if (ok && j >= kQpVStages)
-      ok = mbar_wait(slot(kSlVEmpty + st), ((j >> 1) - 1) & 1, abort_flag, p.err);
+    bool ok = mbar_wait_soon(slot(kSlCFull + cs), cround & 1, abort_flag, p.err);
+    if (ok && j >= 2)
+      ok = mbar_wait_soon(slot(kSlVEmpty + st), ((j >> 1) - 1) & 1, abort_flag, p.err);
     if (!__all_sync(0xffffffffu, ok)) return;
-    const uint32_t from = base + kQpOffC + st * kQpCodes + 16 * lane;
+    const uint32_t from = base + kQpOffC + cs * kQpCodes + 16 * lane;
     const uint32_t to = base + kQpOffV + st * kQpTile + lane * 128;
+    // chunk q of a page: dims 32 q .. + 31, one per lane, 16 tokens
 #pragma unroll 1
     for (int pg = 0; pg < kQpPages; ++pg) {
       uint4 w[4];
@@ -292,7 +379,7 @@ __device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, in
         }
       }
       // dim row 32 q + lane: chunks 2 pg and 2 pg + 1, swizzled by the row
-      const uint32_t c0 = ((2 * pg) ^ (lane & 7)) << 4, c1 = ((2 * pg + 1) ^ (lane & 7)) << 4;
+      const uint32_t c0 = ((2 * pg) ^ (lane & 7)) << 4, c1 = c0 ^ 16;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         sts128(to + q * 32 * 128 + c0, f16x2_of_codes(w[q].x), f16x2_of_codes(w[q].x >> 16),
@@ -303,8 +390,15 @@ __device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, in
     }
     // the codes are read; the widened tile is visible to the tensor core
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_arrive(slot(kSlCEmpty + st));
-    mbar_arrive(slot(kSlVFull + st));
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(slot(kSlVFull + st));
+      mbar_arrive(slot(kSlCEmpty + cs));
+    }
+    if (++cs == kQpCStages) {
+      cs = 0;
+      ++cround;
+    }
   }
 }
 
@@ -365,13 +459,15 @@ __global__ void __launch_bounds__(kQpThreads, 2)
       mbar_init(slot(kSlKFull + i), 1);
       mbar_init(slot(kSlKEmpty + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kQpCStages; ++i) {
       mbar_init(slot(kSlCFull + i), 1);
-      mbar_init(slot(kSlCEmpty + i), 32);
-      mbar_init(slot(kSlVFull + i), 32);
+      mbar_init(slot(kSlCEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(slot(kSlVFull + i), 1);
       mbar_init(slot(kSlVEmpty + i), 1);
       mbar_init(b_s0 + 8 * i, 1);
-      mbar_init(b_p0 + 8 * i, kQpSoft);
+      mbar_init(b_p0 + 8 * i, kQpSoft / 32);
       mbar_init(b_o0 + 8 * i, 1);
     }
     mbar_init(slot(kSlQ), kQpSoft);
@@ -406,42 +502,33 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     uint32_t last_bar = 0;  // barrier of this warp's latest commit (drained on abort)
     int last_par = 0;
     if (warp == 1) {
-      bool ok = __all_sync(kAll, mbar_wait(slot(kSlQ), 0, abort_flag, p.err));
+      bool ok = __all_sync(kAll, mbar_wait_soon(slot(kSlQ), 0, abort_flag, p.err));
       tc_fence_after();
       for (int j = 0; j < nkv && ok; ++j) {
         const int b = j & 1, par = (j >> 1) & 1, ks = j % kQpKStages;
-        ok = __all_sync(kAll, mbar_wait(slot(kSlKFull + ks), (j / kQpKStages) & 1, abort_flag,
-                                        p.err));
+        ok = __all_sync(kAll, mbar_wait_soon(slot(kSlKFull + ks), (j / kQpKStages) & 1,
+                                             abort_flag, p.err));
         if (ok && j >= 2)
-          ok = __all_sync(kAll, mbar_wait(b_o0 + 8 * b, par ^ 1, abort_flag, p.err));
+          ok = __all_sync(kAll, mbar_wait_soon(b_o0 + 8 * b, par ^ 1, abort_flag, p.err));
         if (!ok) break;
         tc_fence_after();
-        // two terms of Q, 4 k-steps of 32 dims each
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          umma_f8_ss(tmem + b * kQpTmemS,
-                     umma_desc(base + kQpOffQ + (i >> 2) * kQpQ + (i & 3) * 32, 16, 1024),
-                     umma_desc(base + kQpOffK + ks * kQpCodes + (i & 3) * 32, 16, 1024),
-                     idesc_qk, i > 0);
-        umma_commit(b_s0 + 8 * b);
-        umma_commit(slot(kSlKEmpty + ks));
+        issue_scores(tmem + b * kQpTmemS, umma_desc(base + kQpOffQ, 16, 1024),
+                     umma_desc(base + kQpOffK + ks * kQpCodes, 16, 1024), idesc_qk, b_s0 + 8 * b,
+                     slot(kSlKEmpty + ks));
         last_bar = b_s0 + 8 * b;
         last_par = par;
       }
     } else {
       for (int j = 0; j < nkv; ++j) {
         const int b = j & 1, par = (j >> 1) & 1;
-        if (!__all_sync(kAll, mbar_wait(b_p0 + 8 * b, par, abort_flag, p.err))) break;
-        if (!__all_sync(kAll, mbar_wait(slot(kSlVFull + b), par, abort_flag, p.err))) break;
+        // (V first: it is there long before P', whose wait is the step's end)
+        if (!__all_sync(kAll, mbar_wait_soon(slot(kSlVFull + b), par, abort_flag, p.err) &&
+                                  mbar_wait_soon(b_p0 + 8 * b, par, abort_flag, p.err)))
+          break;
         tc_fence_after();
-        // 4 k-steps of 16 keys: 32 bytes of every 128-byte dim row
-#pragma unroll
-        for (int ks = 0; ks < kPfKeys / 16; ++ks)
-          umma_f16_ta(tmem_o, tmem + b * kQpTmemS + ks * 8,
-                      umma_desc(base + kQpOffV + b * kQpTile + ks * 32, 16, 1024), idesc_pv,
-                      (j > 0 || ks > 0) ? 1u : 0u);
-        umma_commit(b_o0 + 8 * b);
-        umma_commit(slot(kSlVEmpty + b));
+        issue_values(tmem_o, tmem + b * kQpTmemS,
+                     umma_desc(base + kQpOffV + b * kQpTile, 16, 1024), idesc_pv, j > 0,
+                     b_o0 + 8 * b, slot(kSlVEmpty + b));
         last_bar = b_o0 + 8 * b;
         last_par = par;
       }
@@ -514,14 +601,15 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     bool ok = true;
     for (int j = 0; j < nkv && ok; ++j) {
       const int b = j & 1, par = (j >> 1) & 1;
+      // (the scales are there long before the scores)
       ok = __all_sync(0xffffffffu,
-                      mbar_wait(slot(kSlScale + (j & 7)), (j >> 3) & 1, abort_flag, p.err) &&
-                          mbar_wait(b_s0 + 8 * b, par, abort_flag, p.err));
+                      mbar_wait_soon(slot(kSlScale + (j & 7)), (j >> 3) & 1, abort_flag, p.err));
+      const uint2 sc = lds64(slot(kSlScales + (j & 7)));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(b_s0 + 8 * b, par, abort_flag, p.err));
       if (!ok) break;
       tc_fence_after();
       const uint32_t sb = tmem + b * kQpTmemS;
       const int key0 = j * kPfKeys;
-      const uint2 sc = lds64(slot(kSlScales + (j & 7)));
       float sv[2][32];
       tmem_ld64(sb + trow, sv);
       if (key0 + kPfKeys - 1 > prefix + pos0) {  // a row may not see every key
@@ -551,7 +639,7 @@ __global__ void __launch_bounds__(kQpThreads, 2)
       // done and before that of tile j (tcgen05.ld / st are warp-collective)
       if (__any_sync(0xffffffffu, alpha != 1.f)) {
         if (j >= 1) {
-          ok = __all_sync(0xffffffffu, mbar_wait(b_o0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1,
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(b_o0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1,
                                                 abort_flag, p.err));
           if (!ok) break;
           tc_fence_after();
@@ -592,11 +680,12 @@ __global__ void __launch_bounds__(kQpThreads, 2)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(b_p0 + 8 * b);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_p0 + 8 * b);
     }
     // out = O / l
     if (ok && nkv > 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(b_o0 + 8 * ((nkv - 1) & 1), ((nkv - 1) >> 1) & 1,
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(b_o0 + 8 * ((nkv - 1) & 1), ((nkv - 1) >> 1) & 1,
                                             abort_flag, p.err));
     tc_fence_after();
     if (ok) {
