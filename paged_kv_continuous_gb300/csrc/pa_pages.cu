@@ -111,6 +111,9 @@ __global__ void __launch_bounds__(32 * kCopyWarps) copy_pages_kernel(
 // ---- plans: one block -----------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = 8;  // pages a thread looks at in one step
+// A fork of at most this many table entries (rows at their full width) is
+// applied by the plan's own block, a launch less; beyond, spread over the SMs.
+constexpr long long kInlineEntries = 4096;
 
 // Exclusive sum over the block's threads of v, and the total.
 __device__ __forceinline__ int plan_scan(int v, int *wsum, int &total) {
@@ -164,7 +167,27 @@ struct ForkParams {
   long long num_blocks;
   int32_t *src, *dst, *forked;
   int32_t *err;
+  int apply;  // the plan's block applies it too
 };
+
+// Fork i's table row: the child's entries j0, j0 + step, ...
+__device__ __forceinline__ void apply_fork(const ForkParams &p, int i, int j0, int step) {
+  const int n = p.forked[i];
+  if (n < 0) return;
+  const int k = ceil_div_blocks(n);
+  const int last = p.src[i] >= 0 ? k - 1 : -1;
+  const int32_t *from = p.tables + (long long)p.parents[i] * p.stride;
+  int32_t *to = p.tables + (long long)p.children[i] * p.stride;
+  for (int j = j0; j < k; j += step) {
+    const int page = j == last ? p.dst[i] : from[j];
+    to[j] = page;
+    if (page >= 0 && page < p.num_blocks)
+      atomicAdd(p.refs + page, 1);
+    else
+      report(p.err, PA_DEVERR_BLOCK_INDEX);
+  }
+  if (j0 == 0) p.ctx[p.children[i]] = n;
+}
 
 // Fork i is refused when its parent or child is no row, they are the same,
 // the child holds pages or is an earlier fork's child, or the parent's
@@ -237,28 +260,17 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
     if (p.forked[i] < 0 && c >= 0 && c < p.rows && ctx[c] == INT_MIN + i) p.ctx[c] = 0;
     p.src[i] = s;
   }
+  if (!p.apply) return;
+  __syncthreads();
+  // 5. few entries: a warp per fork applies it here
+  for (int i = tid >> 5; i < p.n; i += kPlanThreads / 32) apply_fork(p, i, tid & 31, 32);
 }
 
 // Block (i, y): entries of fork i's table row.
 __global__ void __launch_bounds__(256) fork_apply_kernel(const ForkParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int i = blockIdx.x;
-  const int n = p.forked[i];
-  if (n < 0) return;
-  const int k = ceil_div_blocks(n);
-  const int last = p.src[i] >= 0 ? k - 1 : -1;
-  const int32_t *from = p.tables + (long long)p.parents[i] * p.stride;
-  int32_t *to = p.tables + (long long)p.children[i] * p.stride;
-  for (int j = blockIdx.y * 256 + threadIdx.x; j < k; j += gridDim.y * 256) {
-    const int page = j == last ? p.dst[i] : from[j];
-    to[j] = page;
-    if (page >= 0 && page < p.num_blocks)
-      atomicAdd(p.refs + page, 1);
-    else
-      report(p.err, PA_DEVERR_BLOCK_INDEX);
-  }
-  if (blockIdx.y == 0 && threadIdx.x == 0) p.ctx[p.children[i]] = n;
+  apply_fork(p, blockIdx.x, blockIdx.y * 256 + threadIdx.x, gridDim.y * 256);
 }
 
 // ---- free: one block per row ------------------------------------------------------
@@ -459,10 +471,13 @@ extern "C" pa_status pa_fork_pages(int32_t *block_tables, int32_t block_table_st
                   forked, error_flags))
     return PA_ERR_INVALID_ARG;
   ForkParams p{block_tables, block_table_stride, context_lens, num_rows, parents, children,
-               num_forks, ref_counts, num_blocks, copy_src, copy_dst, forked, error_flags};
+               num_forks, ref_counts, num_blocks, copy_src, copy_dst, forked, error_flags,
+               (long long)num_forks * block_table_stride <= kInlineEntries};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
-                    true, p) != cudaSuccess ||
+                    true, p) != cudaSuccess)
+    return PA_ERR_LAUNCH;
+  if (!p.apply &&
       launch_kernel(fork_apply_kernel, dim3((unsigned)num_forks, row_blocks(block_table_stride)),
                     dim3(256), 0, s, true, p) != cudaSuccess)
     return PA_ERR_LAUNCH;

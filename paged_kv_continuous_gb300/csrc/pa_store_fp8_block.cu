@@ -20,6 +20,15 @@
 // so unit u = floor(cu_seqlens[s] / 16) + 2 s + i names the i-th page of
 // sequence s without overlap, the host sizes the grid from total_tokens and
 // num_seqs alone, and a warp finds its s by a 32-way search.
+//
+// Measured: 5 x 5-8 k tokens at 8 kv heads (204 MB) 34.1 us, 6.0 TB/s, 88 % of
+// the measured copy bandwidth; 32 k tokens at 2 kv heads (49 MB) 9.8 us; the 64
+// tokens of a decode step 3.6 us (launch and four dependent loads).  It was
+// bound by its instructions, not by memory: pages that are all new take a path
+// without row masks, two bf16 per maximum and byte transposes of two rounds of
+// permutes (about 280 instructions a warp, from 700), 45.3 -> 34.1 us.  A warp
+// that fetches its next page's rows while it codes one (half the warps fit) was
+// slower, 51.6 us.
 #include "pa_fp8_block.cuh"
 
 namespace pa {
@@ -66,8 +75,111 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int num_seqs, long lo
   return lo;
 }
 
+// One warp's share of a page: rows r0 .. r1 - 1 of one head of K (dst = row 0 of
+// the head) or V (dst = the lane's first dim row).
+struct Share {
+  const uint16_t *src;  // row 0 of the page in k / v, the lane's dims
+  long long tok;        // stride of a token in elements
+  uint8_t *dst, *scale;
+  long long k_row;      // bytes from one K row of the head to the next
+  int r0, r1;
+};
+
+// kFull: all 16 rows are new, and nothing the page holds matters.
+template <bool kFull, bool kIsV>
+__device__ __forceinline__ void store_share(const Share &t, const uint2 (&row)[kBlockSize]) {
+  const int r0 = kFull ? 0 : t.r0, r1 = kFull ? kBlockSize : t.r1;
+  const int old =
+      !kFull && r0 > 0 ? min(max((int)*t.scale, kScaleMin), kScaleMax) : 0;
+  uint4 vold[4];
+  if (kIsV && !kFull) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) vold[d] = *reinterpret_cast<const uint4 *>(t.dst + d * kBlockSize);
+  }
+
+  // ---- the page's scale ------------------------------------------------------
+  // |x| of bf16 orders like its bits (two elements per maximum).  Infinities
+  // and NaN (exponent all ones) do not count -- an infinity saturates, a NaN
+  // keeps its code -- so where the warp met one it looks again, without them.
+  uint32_t top2 = 0;
+#pragma unroll
+  for (int r = 0; r < kBlockSize; ++r)
+    top2 = __vmaxu2(top2, __vmaxu2(row[r].x & 0x7FFF7FFFu, row[r].y & 0x7FFF7FFFu));
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 >> 16, top2 & 0xFFFFu));
+  if (top >= 0x7F80u) {
+    top = 0;
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+      const uint16_t *q = t.src + (long long)r * t.tok;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t a = __ldg(q + k) & 0x7FFFu;
+        top = max(top, a < 0x7F80u ? a : 0u);
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  const int e = max(scale_for(__uint_as_float(top << 16)), old);
+  const float inv = inv_scale_of(e);
+  const bool grew = !kFull && r0 > 0 && e > old;
+  const float down = grew ? __uint_as_float((uint32_t)(old - e + kScaleBias) << 23) : 1.f;
+
+  // ---- the codes ---------------------------------------------------------------
+  uint32_t code[kBlockSize];
+#pragma unroll
+  for (int r = 0; r < kBlockSize; ++r) {
+    const float2 a = bf16x2_to_float2(row[r].x), b = bf16x2_to_float2(row[r].y);
+    code[r] = e4m3x2_of(a.x * inv, a.y * inv) | (e4m3x2_of(b.x * inv, b.y * inv) << 16);
+  }
+  if (!kIsV) {
+#pragma unroll
+    for (int r = 0; r < kBlockSize; ++r) {
+      uint32_t *q = reinterpret_cast<uint32_t *>(t.dst + r * t.k_row);
+      if (kFull || (r >= r0 && r < r1))
+        *q = code[r];
+      else if (grew && r < r0)
+        *q = recode4(*q, down);
+    }
+  } else {
+    // rows to columns: the 16-byte dim row d holds byte d of every token's
+    // codes; 4 x 4 bytes at a time, two rounds of byte permutes
+    uint32_t o[4][4];  // [dim][tokens 4 q .. 4 q + 3]
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t a = code[4 * q], b = code[4 * q + 1], c = code[4 * q + 2], d = code[4 * q + 3];
+      const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+      const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+      o[0][q] = __byte_perm(ab0, cd0, 0x5410);
+      o[1][q] = __byte_perm(ab0, cd0, 0x7632);
+      o[2][q] = __byte_perm(ab1, cd1, 0x5410);
+      o[3][q] = __byte_perm(ab1, cd1, 0x7632);
+    }
+    if (!kFull) {
+      // tokens past the chunk keep their bytes, earlier ones their values
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // bytes [r0, r1) of the page that fall in this word
+        const int b0 = min(max(r0 - 4 * q, 0), 4), b1 = min(max(r1 - 4 * q, 0), 4);
+        const uint32_t below = b0 >= 4 ? 0xFFFFFFFFu : (1u << (8 * b0)) - 1u;
+        const uint32_t upto = b1 >= 4 ? 0xFFFFFFFFu : (1u << (8 * b1)) - 1u;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          uint32_t kept = q == 0 ? vold[d].x : q == 1 ? vold[d].y : q == 2 ? vold[d].z : vold[d].w;
+          if (grew) kept = (recode4(kept, down) & below) | (kept & ~below);
+          o[d][q] = (o[d][q] & upto & ~below) | (kept & ~(upto & ~below));
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      *reinterpret_cast<uint4 *>(t.dst + d * kBlockSize) =
+          make_uint4(o[d][0], o[d][1], o[d][2], o[d][3]);
+  }
+  if ((threadIdx.x & 31) == 0) *t.scale = (uint8_t)e;
+}
+
 template <bool kVec>
-__global__ void __launch_bounds__(32 * kQsWarps) store_kv_fp8_block_kernel(QuantStoreParams p) {
+__global__ void __launch_bounds__(32 * kQsWarps, 8)
+    store_kv_fp8_block_kernel(const QuantStoreParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -78,9 +190,23 @@ __global__ void __launch_bounds__(32 * kQsWarps) store_kv_fp8_block_kernel(Quant
   if (u >= p.units) return;
   const int x = (int)(w % per), is_v = x & 1, h = x >> 1;
 
-  const int s = find_seq(p.cu_seqlens, p.num_seqs, u, lane);
-  const int c0 = __ldg(p.cu_seqlens + s), c1 = __ldg(p.cu_seqlens + s + 1);
-  const int n = __ldg(p.context_lens + s);
+  int s, c0, c1, n;
+  if (p.num_seqs <= 32) {
+    // one round of loads: a sequence per lane
+    const int mine = min(lane, p.num_seqs - 1);
+    const int a = __ldg(p.cu_seqlens + mine), b = __ldg(p.cu_seqlens + mine + 1);
+    const int c = __ldg(p.context_lens + mine);
+    const unsigned m = __ballot_sync(0xffffffffu, (long long)(a >> 4) + 2ll * mine <= u);
+    s = m ? min(31 - __clz(m), p.num_seqs - 1) : 0;
+    c0 = __shfl_sync(0xffffffffu, a, s);
+    c1 = __shfl_sync(0xffffffffu, b, s);
+    n = __shfl_sync(0xffffffffu, c, s);
+  } else {
+    s = find_seq(p.cu_seqlens, p.num_seqs, u, lane);
+    c0 = __ldg(p.cu_seqlens + s);
+    c1 = __ldg(p.cu_seqlens + s + 1);
+    n = __ldg(p.context_lens + s);
+  }
   const long long i = u - (((long long)(c0 >> 4)) + 2ll * s);  // page of the chunk
   if (c0 < 0 || c1 < c0 || c1 > p.total_tokens || n < c1 - c0) {
     if (i == 0 && x == 0 && lane == 0) report(p.err, PA_DEVERR_SHAPE);
@@ -93,102 +219,49 @@ __global__ void __launch_bounds__(32 * kQsWarps) store_kv_fp8_block_kernel(Quant
     if (x == 0 && lane == 0) report(p.err, PA_DEVERR_SHAPE);
     return;
   }
+  // (requested before the rows and looked at after: one round of loads)
   const long long page = __ldg(p.block_tables + (long long)s * p.bt_stride + j);
-  if (page < 0 || page >= p.num_blocks) {
-    if (x == 0 && lane == 0) report(p.err, PA_DEVERR_BLOCK_INDEX);
-    return;
-  }
   const int base = (int)(j * kBlockSize);
-  const int r0 = max(0, first - base), r1 = min(kBlockSize, n - base);
-
-  // ---- the new rows, the scale so far and the codes that may change ---------
-  const uint16_t *src = p.rows[is_v] + (long long)(c0 + base - first) * p.tok[is_v] +
-                        (long long)h * p.head[is_v] + 4 * lane;
+  Share t;
+  t.tok = p.tok[is_v];
+  t.r0 = max(0, first - base);
+  t.r1 = min(kBlockSize, n - base);
+  t.src = p.rows[is_v] + (long long)(c0 + base - first) * t.tok + (long long)h * p.head[is_v] +
+          4 * lane;
   uint2 row[kBlockSize];
 #pragma unroll
   for (int r = 0; r < kBlockSize; ++r) {
     row[r] = make_uint2(0u, 0u);
-    if (r >= r0 && r < r1) {
-      const uint16_t *q = src + (long long)r * p.tok[is_v];
+    if (r >= t.r0 && r < t.r1) {
+      const uint16_t *q = t.src + (long long)r * t.tok;
       if (kVec) {
-        row[r] = __ldg(reinterpret_cast<const uint2 *>(q));
+        row[r] = __ldcs(reinterpret_cast<const uint2 *>(q));  // read once
       } else {
         row[r].x = (uint32_t)__ldg(q) | ((uint32_t)__ldg(q + 1) << 16);
         row[r].y = (uint32_t)__ldg(q + 2) | ((uint32_t)__ldg(q + 3) << 16);
       }
     }
   }
-  uint8_t *scale = p.scale[is_v] + page * p.hkv + h;
-  const int old = r0 > 0 ? min(max((int)*scale, kScaleMin), kScaleMax) : 0;
-  // V: the page of this head, 128 dims x 16 tokens; K: row 0 of this head
-  uint8_t *dst = is_v ? p.cache[1] + ((page * p.hkv + h) * kHeadDim + 4 * lane) * kBlockSize
-                      : p.cache[0] + (page * kBlockSize * p.hkv + h) * kHeadDim + 4 * lane;
-  const long long k_row = (long long)p.hkv * kHeadDim;
-  uint4 vold[4];
+  if (page < 0 || page >= p.num_blocks) {
+    if (x == 0 && lane == 0) report(p.err, PA_DEVERR_BLOCK_INDEX);
+    return;
+  }
+  t.scale = p.scale[is_v] + page * p.hkv + h;
+  t.k_row = (long long)p.hkv * kHeadDim;
+  t.dst = is_v ? p.cache[1] + ((page * p.hkv + h) * kHeadDim + 4 * lane) * kBlockSize
+               : p.cache[0] + (page * kBlockSize * p.hkv + h) * kHeadDim + 4 * lane;
+  const bool full = t.r0 == 0 && t.r1 == kBlockSize;
   if (is_v) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-      vold[d] = r0 > 0 || r1 < kBlockSize ? *reinterpret_cast<const uint4 *>(dst + d * kBlockSize)
-                                          : make_uint4(0u, 0u, 0u, 0u);
-  }
-
-  // ---- the page's scale ------------------------------------------------------
-  // |x| of bf16 orders like its bits; infinities and NaN (exponent all ones)
-  // do not count: an infinity saturates, a NaN keeps its code
-  uint32_t top = 0;
-#pragma unroll
-  for (int r = 0; r < kBlockSize; ++r) {
-    const uint32_t a = row[r].x & 0x7FFF7FFFu, b = row[r].y & 0x7FFF7FFFu;
-    const uint32_t v[4] = {a & 0xFFFFu, a >> 16, b & 0xFFFFu, b >> 16};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top = max(top, v[k] < 0x7F80u ? v[k] : 0u);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  const int e = max(scale_for(__uint_as_float(top << 16)), old);
-  const float inv = inv_scale_of(e);
-  const bool grew = r0 > 0 && e > old;
-  const float down = grew ? __uint_as_float((uint32_t)(old - e + kScaleBias) << 23) : 1.f;
-
-  // ---- the codes ---------------------------------------------------------------
-  uint32_t code[kBlockSize];
-#pragma unroll
-  for (int r = 0; r < kBlockSize; ++r) {
-    const float2 a = bf16x2_to_float2(row[r].x), b = bf16x2_to_float2(row[r].y);
-    code[r] = e4m3x2_of(a.x * inv, a.y * inv) | (e4m3x2_of(b.x * inv, b.y * inv) << 16);
-  }
-  if (!is_v) {
-#pragma unroll
-    for (int r = 0; r < kBlockSize; ++r) {
-      uint32_t *q = reinterpret_cast<uint32_t *>(dst + r * k_row);
-      if (r >= r0 && r < r1)
-        *q = code[r];
-      else if (grew && r < r0)
-        *q = recode4(*q, down);
-    }
+    if (full)
+      store_share<true, true>(t, row);
+    else
+      store_share<false, true>(t, row);
   } else {
-    // rows to columns: 16-byte dim row d holds byte d of every token's codes;
-    // tokens past the chunk keep their bytes
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      uint32_t o[4] = {vold[d].x, vold[d].y, vold[d].z, vold[d].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // byte d of tokens 4q .. 4q + 3
-        const uint32_t lo = __byte_perm(code[4 * q], code[4 * q + 1], d | ((4 + d) << 4));
-        const uint32_t hi = __byte_perm(code[4 * q + 2], code[4 * q + 3], d | ((4 + d) << 4));
-        const uint32_t fresh = __byte_perm(lo, hi, 0x5410);
-        // bytes [r0, r1) of the page that fall in this word
-        const int b0 = min(max(r0 - 4 * q, 0), 4), b1 = min(max(r1 - 4 * q, 0), 4);
-        const uint32_t below = b0 >= 4 ? 0xFFFFFFFFu : (1u << (8 * b0)) - 1u;
-        const uint32_t upto = b1 >= 4 ? 0xFFFFFFFFu : (1u << (8 * b1)) - 1u;
-        uint32_t kept = o[q];
-        if (grew) kept = (recode4(kept, down) & below) | (kept & ~below);
-        o[q] = (fresh & upto & ~below) | (kept & ~(upto & ~below));
-      }
-      *reinterpret_cast<uint4 *>(dst + d * kBlockSize) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    if (full)
+      store_share<true, false>(t, row);
+    else
+      store_share<false, false>(t, row);
   }
-  if (lane == 0) *scale = (uint8_t)e;
 }
 
 }  // namespace
