@@ -119,9 +119,6 @@ struct DecodeParams {
   // previous kernel in the stream completes (the caller guarantees that
   // kernel does not write the pools).
   int early_kv;
-  // BS kernels: nonzero: nothing is read before the previous kernel is over
-  // (the launch is a programmatic dependent one whatever the caller's flags)
-  int wait_first;
   // BS kernels: blocks a split takes at least (0: as many splits as CTAs)
   int min_blocks;
   // Rotary embedding inside the fused store (ROPE kernels): sequence b's new
@@ -468,19 +465,20 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 }
 
 // The HKV scale bytes of a block (1, 2, 4 or 8, at a multiple of HKV bytes
-// from a base aligned to 8).
+// from a base aligned to 8).  Plain loads: the kernel before, which a
+// programmatic launch overlaps, may have written them.
 template <int HKV>
 __device__ __forceinline__ void load_scale_bytes(const uint8_t *src, uint32_t (&w)[2]) {
   if constexpr (HKV == 8) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+    const uint2 x = *reinterpret_cast<const uint2 *>(src);
     w[0] = x.x;
     w[1] = x.y;
   } else if constexpr (HKV == 4) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+    w[0] = *reinterpret_cast<const uint32_t *>(src);
   } else if constexpr (HKV == 2) {
-    w[0] = __ldg(reinterpret_cast<const uint16_t *>(src));
+    w[0] = *reinterpret_cast<const uint16_t *>(src);
   } else {
-    w[0] = __ldg(src);
+    w[0] = *src;
   }
 }
 
@@ -907,9 +905,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   const int lane = tid & 31;
   long long nsplit = p.num_splits;
   const long long c = blockIdx.x;
-  if constexpr (BS) {
-    if (p.wait_first) griddep_wait();
-  }
 
   // ---- 1. block counts of all sequences: the total N, this CTA's block range
   //         [lo, hi) and the sequence that holds block lo.  One block-wide

@@ -5,9 +5,6 @@
 // state: a fork takes the lowest free pages, so results do not depend on the
 // order in which blocks of a launch run (the counts are integer sums).
 //
-// Every kernel here is launched as a programmatic dependent and waits for the
-// kernel before it first of all, which only moves its own set-up ahead.
-//
 // Fork and compact are planned by one block, since every pick depends on all
 // earlier ones (a scan over the counts); a second launch, spread over the
 // sequences, applies the plan.  Nothing is read back to the host: the plan's
@@ -51,7 +48,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps) copy_pages_kernel(
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   int pairs = p.num_pairs;
-  if (p.count) pairs = min(pairs, max(__ldg(p.count), 0));
+  if (p.count) pairs = min(pairs, max(*p.count, 0));
   const int per = p.num_big ? p.chunk_end[p.num_big - 1] : 0;
   const long long big = (long long)pairs * per, tiny = (long long)pairs * p.num_tiny;
   const long long units = big + (tiny + 31) / 32;
@@ -62,7 +59,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps) copy_pages_kernel(
       const long long t = (u - big) * 32 + lane;
       if (t >= tiny) continue;
       const int i = (int)(t / p.num_tiny), q = p.num_big + (int)(t % p.num_tiny);
-      const long long s = __ldg(p.src + i), d = __ldg(p.dst + i);
+      const long long s = p.src[i], d = p.dst[i];
       if (s < 0) continue;
       if (s >= p.num_blocks || d < 0 || d >= p.num_blocks) {
         report(p.err, PA_DEVERR_BLOCK_INDEX);
@@ -75,7 +72,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps) copy_pages_kernel(
       continue;
     }
     const int i = (int)(u / per), c = (int)(u % per);
-    const long long s = __ldg(p.src + i), d = __ldg(p.dst + i);
+    const long long s = p.src[i], d = p.dst[i];
     if (s < 0) continue;
     if (s >= p.num_blocks || d < 0 || d >= p.num_blocks) {
       if (c == 0 && lane == 0) report(p.err, PA_DEVERR_BLOCK_INDEX);
@@ -170,23 +167,29 @@ struct ForkParams {
   int apply;  // the plan's block applies it too
 };
 
-// Fork i's table row: the child's entries j0, j0 + step, ...
-__device__ __forceinline__ void apply_fork(const ForkParams &p, int i, int j0, int step) {
-  const int n = p.forked[i];
+// A fork's plan: rows, the child's length (-1: refused), the page to copy
+// (-1: none) and its copy.
+struct Fork {
+  int parent, child, n, src, dst;
+};
+
+// The fork's table row: the child's entries j0, j0 + step, ...
+__device__ __forceinline__ void apply_fork(const ForkParams &p, const Fork &f, int j0, int step) {
+  const int n = f.n;
   if (n < 0) return;
   const int k = ceil_div_blocks(n);
-  const int last = p.src[i] >= 0 ? k - 1 : -1;
-  const int32_t *from = p.tables + (long long)p.parents[i] * p.stride;
-  int32_t *to = p.tables + (long long)p.children[i] * p.stride;
+  const int last = f.src >= 0 ? k - 1 : -1;
+  const int32_t *from = p.tables + (long long)f.parent * p.stride;
+  int32_t *to = p.tables + (long long)f.child * p.stride;
   for (int j = j0; j < k; j += step) {
-    const int page = j == last ? p.dst[i] : from[j];
+    const int page = j == last ? f.dst : from[j];
     to[j] = page;
     if (page >= 0 && page < p.num_blocks)
       atomicAdd(p.refs + page, 1);
     else
       report(p.err, PA_DEVERR_BLOCK_INDEX);
   }
-  if (j0 == 0) p.ctx[p.children[i]] = n;
+  if (j0 == 0) p.ctx[f.child] = n;
 }
 
 // Fork i is refused when its parent or child is no row, they are the same,
@@ -194,14 +197,31 @@ __device__ __forceinline__ void apply_fork(const ForkParams &p, int i, int j0, i
 // context does not fit its table row.  The children claim their rows: the
 // context length of an empty child row takes INT_MIN + i of the lowest fork i
 // that names it until the plan is applied (a length below 1 reads as empty).
+//
+// The plan is a chain of dependent loads by one block (about 4 us), so up to
+// 1024 forks keep their rows and plan in shared memory between its steps.
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams p) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ int wsum[32];
+  __shared__ int kept[5][kPlanThreads];
   const int tid = threadIdx.x;
   volatile int32_t *ctx = p.ctx;
+  const bool small = p.n <= kPlanThreads;
+  const int32_t *parents = small ? kept[0] : p.parents, *children = small ? kept[1] : p.children;
+  int32_t *src = small ? kept[2] : p.src, *dst = small ? kept[3] : p.dst;
+  int32_t *forked = small ? kept[4] : p.forked;
+  if (small && tid < p.n) {
+    kept[0][tid] = p.parents[tid];
+    kept[1][tid] = p.children[tid];
+  }
+  // the first pages' counts, for step 3
+  unsigned first_mask = 0;
+  if ((long long)tid * kPlanPer < p.num_blocks)
+    first_mask = free_mask(p.refs, (long long)tid * kPlanPer, p.num_blocks);
+  __syncthreads();
   auto length = [&](int i) {  // the parent's context length; -1: refused
-    const int a = p.parents[i], c = p.children[i];
+    const int a = parents[i], c = children[i];
     if (a < 0 || a >= p.rows || c < 0 || c >= p.rows || a == c) return -1;
     const int n = ctx[a];
     if (n > 0 && (long long)(n - 1) / kBlockSize >= p.stride) return -1;
@@ -209,8 +229,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
   };
   // 1. claims
   for (int i = tid; i < p.n; i += kPlanThreads) {
-    const int c = p.children[i];
-    if (length(i) >= 0 && ctx[c] <= 0) atomicMin(p.ctx + c, INT_MIN + i);
+    const int n = length(i);
+    if (n >= 0 && ctx[children[i]] <= 0) atomicMin(p.ctx + children[i], INT_MIN + i);
   }
   __syncthreads();
   // 2. ranks of the forks that need a page of their own; src[r] = fork of rank r
@@ -220,15 +240,15 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
     int want = 0;
     if (i < p.n) {
       const int n = length(i);
-      const bool ok = n >= 0 && ctx[p.children[i]] == INT_MIN + i;
-      p.forked[i] = ok ? n : -1;
-      p.dst[i] = -1;
-      if (n < 0 || !ok) report(p.err, PA_DEVERR_SHAPE);
+      const bool ok = n >= 0 && ctx[children[i]] == INT_MIN + i;
+      forked[i] = ok ? n : -1;
+      dst[i] = -1;
+      if (!ok) report(p.err, PA_DEVERR_SHAPE);
       want = ok && n % kBlockSize != 0;
     }
     int total;
     const int r = need + plan_scan(want, wsum, total);
-    if (want) p.src[r] = i;
+    if (want) src[r] = i;
     need += total;
   }
   __syncthreads();
@@ -236,41 +256,49 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
   int found = 0;
   for (long long b = 0; b < p.num_blocks && found < need; b += kPlanThreads * kPlanPer) {
     const long long first = b + (long long)tid * kPlanPer;
-    unsigned m = first < p.num_blocks ? free_mask(p.refs, first, p.num_blocks) : 0u;
+    unsigned m = b == 0 ? first_mask
+                        : first < p.num_blocks ? free_mask(p.refs, first, p.num_blocks) : 0u;
     int total;
     int r = found + plan_scan(__popc(m), wsum, total);
-    for (; m && r < need; m &= m - 1, ++r) p.dst[p.src[r]] = (int)(first + __ffs(m) - 1);
+    for (; m && r < need; m &= m - 1, ++r) dst[src[r]] = (int)(first + __ffs(m) - 1);
     found += total;
   }
   __syncthreads();
   // 4. the pairs
   for (int i = tid; i < p.n; i += kPlanThreads) {
-    const int n = p.forked[i];
+    const int n = forked[i], c = children[i];
     int s = -1;
     if (n > 0 && n % kBlockSize != 0) {
-      if (p.dst[i] >= 0) {
-        s = p.tables[(long long)p.parents[i] * p.stride + n / kBlockSize];
+      if (dst[i] >= 0) {
+        s = p.tables[(long long)parents[i] * p.stride + n / kBlockSize];
       } else {
-        p.forked[i] = -1;  // no page left
+        forked[i] = -1;  // no page left
         report(p.err, PA_DEVERR_PAGES);
       }
     }
     // a claim that comes to nothing is given back
-    const int c = p.children[i];
-    if (p.forked[i] < 0 && c >= 0 && c < p.rows && ctx[c] == INT_MIN + i) p.ctx[c] = 0;
-    p.src[i] = s;
+    if (forked[i] < 0 && c >= 0 && c < p.rows && ctx[c] == INT_MIN + i) p.ctx[c] = 0;
+    src[i] = s;
+    if (small) {
+      p.src[i] = s;
+      p.dst[i] = dst[i];
+      p.forked[i] = forked[i];
+    }
   }
   if (!p.apply) return;
   __syncthreads();
   // 5. few entries: a warp per fork applies it here
-  for (int i = tid >> 5; i < p.n; i += kPlanThreads / 32) apply_fork(p, i, tid & 31, 32);
+  for (int i = tid >> 5; i < p.n; i += kPlanThreads / 32)
+    apply_fork(p, Fork{parents[i], children[i], forked[i], src[i], dst[i]}, tid & 31, 32);
 }
 
 // Block (i, y): entries of fork i's table row.
 __global__ void __launch_bounds__(256) fork_apply_kernel(const ForkParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  apply_fork(p, blockIdx.x, blockIdx.y * 256 + threadIdx.x, gridDim.y * 256);
+  const int i = blockIdx.x;
+  apply_fork(p, Fork{p.parents[i], p.children[i], p.forked[i], p.src[i], p.dst[i]},
+             blockIdx.y * 256 + threadIdx.x, gridDim.y * 256);
 }
 
 // ---- free: one block per row ------------------------------------------------------
@@ -316,62 +344,118 @@ struct CompactParams {
   int32_t *err;
 };
 
+// Exclusive sums, in place, of the 256 ints of `a` by one warp; returns the total.
+__device__ __forceinline__ int scan256(int *a, int lane) {
+  int v[8], sum = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = a[8 * lane + k];
+    sum += v[k];
+  }
+  int x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  int at = x - sum;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    a[8 * lane + k] = at;
+    at += v[k];
+  }
+  return __shfl_sync(0xffffffffu, x, 31);
+}
+
 // With L live pages, the k-th live page at or past L (ascending) moves to the
-// k-th free page before L; both lists have the same length.
+// k-th free page before L; both lists have the same length.  Every hole comes
+// before every mover in page order, so one ascending walk can pair them: a
+// step (8192 pages, eight per thread, 1024 apart so that all its accesses are
+// contiguous) writes its holes, and behind a barrier every hole that its
+// movers need stands in dst.  Ranks are ballots within a warp over a scan of
+// the step's 256 warp counts.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int wsum[32];
-  const int tid = threadIdx.x;
-  constexpr int kStep = kPlanThreads * kPlanPer;
+  static_assert(kPlanThreads == 1024 && kPlanPer == 8, "256 warp counts a step");
+  __shared__ int wsum[32], hole_at[256], mover_at[256], totals[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned before = (1u << lane) - 1u;
   int mine = 0;
-  for (long long b = (long long)tid * kPlanPer; b < p.num_blocks; b += kStep)
-    mine += __popc(free_mask(p.refs, b, p.num_blocks));
-  int free_total;
-  plan_scan(mine, wsum, free_total);
-  const long long live = p.num_blocks - free_total;
+#pragma unroll 8
+  for (long long page = tid; page < p.num_blocks; page += kPlanThreads) mine += p.refs[page] > 0;
+  int live;
+  plan_scan(mine, wsum, live);
   int holes = 0, movers = 0;
-  for (long long b = 0; b < p.num_blocks; b += kStep) {
-    const long long first = b + (long long)tid * kPlanPer;
-    const int in = (int)max(0ll, min((long long)kPlanPer, p.num_blocks - first));
-    const unsigned all = (1u << in) - 1u;
-    const unsigned free = in ? free_mask(p.refs, first, p.num_blocks) : 0u;
-    const int below = (int)max(0ll, min((long long)in, live - first));  // pages before L
-    const unsigned low = (1u << below) - 1u;
-    unsigned hole = free & low, mover = ~free & all & ~low;
-    int th, tm;
-    int rh = holes + plan_scan(__popc(hole), wsum, th);
-    int rm = movers + plan_scan(__popc(mover), wsum, tm);
-    for (; hole; hole &= hole - 1) p.dst[rh++] = (int)(first + __ffs(hole) - 1);
-    for (; mover; mover &= mover - 1) p.src[rm++] = (int)(first + __ffs(mover) - 1);
-    for (int k = 0; k < in; ++k) p.remap[first + k] = (int)(first + k);
-    holes += th;
-    movers += tm;
+  for (long long b = 0; b < p.num_blocks; b += kPlanThreads * kPlanPer) {
+    int ref[kPlanPer];
+    unsigned hole[kPlanPer], mover[kPlanPer];
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      const long long page = b + k * kPlanThreads + tid;
+      ref[k] = page < p.num_blocks ? p.refs[page] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      const long long page = b + k * kPlanThreads + tid;
+      hole[k] = __ballot_sync(0xffffffffu, ref[k] <= 0 && page < live);
+      mover[k] = __ballot_sync(0xffffffffu, ref[k] > 0 && page >= live);
+      if (lane == k) {
+        hole_at[k * 32 + warp] = __popc(hole[k]);
+        mover_at[k * 32 + warp] = __popc(mover[k]);
+      }
+    }
+    __syncthreads();
+    if (warp < 2) {
+      const int total = scan256(warp ? mover_at : hole_at, lane);
+      if (lane == 0) totals[warp] = total;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k)
+      if ((hole[k] >> lane) & 1u)
+        p.dst[holes + hole_at[k * 32 + warp] + __popc(hole[k] & before)] =
+            (int)(b + k * kPlanThreads + tid);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+      const long long page = b + k * kPlanThreads + tid;
+      if (page >= p.num_blocks) continue;
+      int to = (int)page;
+      if ((mover[k] >> lane) & 1u) {
+        const int r = movers + mover_at[k * 32 + warp] + __popc(mover[k] & before);
+        to = p.dst[r];
+        p.src[r] = (int)page;
+        p.refs[to] = ref[k];
+        p.refs[page] = 0;
+      }
+      p.remap[page] = to;
+    }
+    holes += totals[0];
+    movers += totals[1];
+    __syncthreads();  // the counts are the next step's
   }
-  __syncthreads();
-  for (int k = tid; k < movers; k += kPlanThreads) {
-    const int s = p.src[k], d = p.dst[k];
-    p.remap[s] = d;
-    p.refs[d] = p.refs[s];
-    p.refs[s] = 0;
-  }
-  for (long long k = movers + tid; k < p.num_blocks / 2; k += kPlanThreads) p.src[k] = p.dst[k] = -1;
   if (tid == 0) {
     p.counts[0] = movers;
-    p.counts[1] = (int)live;
+    p.counts[1] = live;
   }
 }
 
-__global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams p) {
+// Blocks along the table rows, which also fill the lists past the moves.
+__global__ void __launch_bounds__(256) compact_apply_kernel(const CompactParams p, int per_row) {
   griddep_wait();
   griddep_launch_dependents();
-  const int row = blockIdx.x;
+  const long long total = (long long)gridDim.x * 256;
+  for (long long k = p.counts[0] + (long long)blockIdx.x * 256 + threadIdx.x;
+       k < p.num_blocks / 2; k += total)
+    p.src[k] = p.dst[k] = -1;
+  const int row = blockIdx.x / per_row, y = blockIdx.x % per_row;
+  if (row >= p.rows) return;
   const int n = p.ctx[row];
   if (n <= 0) return;
   const long long k = min((long long)ceil_div_blocks(n), p.stride);
-  if (threadIdx.x == 0 && blockIdx.y == 0 && ceil_div_blocks(n) > p.stride)
-    report(p.err, PA_DEVERR_SHAPE);
-  for (long long j = blockIdx.y * 256 + threadIdx.x; j < k; j += gridDim.y * 256) {
+  if (threadIdx.x == 0 && y == 0 && ceil_div_blocks(n) > p.stride) report(p.err, PA_DEVERR_SHAPE);
+  for (long long j = y * 256 + threadIdx.x; j < k; j += per_row * 256) {
     const int page = p.tables[row * p.stride + j];
     if (page >= 0 && page < p.num_blocks)
       p.tables[row * p.stride + j] = p.remap[page];
@@ -413,6 +497,7 @@ extern "C" pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools,
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_DEVICE;
+  bool pdl = (flags & PA_LAUNCH_PDL) != 0;
   for (int first = 0; first < num_pools; first += kCopyPools) {
     const int n = num_pools - first < kCopyPools ? num_pools - first : kCopyPools;
     CopyPagesParams p = {};
@@ -445,8 +530,9 @@ extern "C" pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools,
     long long blocks = (units + kCopyWarps - 1) / kCopyWarps;
     if (blocks > 8ll * sms) blocks = 8ll * sms;
     if (launch_kernel(copy_pages_kernel, dim3((unsigned)blocks), dim3(32 * kCopyWarps), 0,
-                      static_cast<cudaStream_t>(stream), true, p) != cudaSuccess)
+                      static_cast<cudaStream_t>(stream), pdl, p) != cudaSuccess)
       return PA_ERR_LAUNCH;
+    pdl = true;  // a later launch waits for the one before it first of all
   }
   return PA_OK;
 }
@@ -475,7 +561,7 @@ extern "C" pa_status pa_fork_pages(int32_t *block_tables, int32_t block_table_st
                (long long)num_forks * block_table_stride <= kInlineEntries};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
-                    true, p) != cudaSuccess)
+                    (flags & PA_LAUNCH_PDL) != 0, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   if (!p.apply &&
       launch_kernel(fork_apply_kernel, dim3((unsigned)num_forks, row_blocks(block_table_stride)),
@@ -500,7 +586,7 @@ extern "C" pa_status pa_free_pages(int32_t *block_tables, int32_t block_table_st
   if (misaligned4(block_tables, context_lens, seqs, ref_counts, error_flags))
     return PA_ERR_INVALID_ARG;
   if (launch_kernel(free_pages_kernel, dim3((unsigned)num_seqs), dim3(256), 0,
-                    static_cast<cudaStream_t>(stream), true, block_tables,
+                    static_cast<cudaStream_t>(stream), (flags & PA_LAUNCH_PDL) != 0, block_tables,
                     (long long)block_table_stride, context_lens, (int)num_rows, seqs, ref_counts,
                     (long long)num_blocks, error_flags) != cudaSuccess)
     return PA_ERR_LAUNCH;
@@ -529,12 +615,12 @@ extern "C" pa_status pa_compact_pages(int32_t *block_tables, int32_t block_table
                   num_blocks, copy_src, copy_dst, counts, remap, error_flags};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
-                    true, p) != cudaSuccess)
+                    (flags & PA_LAUNCH_PDL) != 0, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
-  if (num_rows > 0 &&
-      launch_kernel(compact_apply_kernel,
-                    dim3((unsigned)num_rows, row_blocks(block_table_stride)), dim3(256), 0, s,
-                    true, p) != cudaSuccess)
+  const int per_row = (int)row_blocks(block_table_stride);
+  const long long blocks = num_rows > 0 ? (long long)num_rows * per_row : 1;
+  if (launch_kernel(compact_apply_kernel, dim3((unsigned)blocks), dim3(256), 0, s, true, p,
+                    per_row) != cudaSuccess)
     return PA_ERR_LAUNCH;
   return PA_OK;
 }

@@ -32,7 +32,7 @@
 // tensor pipe.
 //
 // What bounds it (two chunks of 2 k queries behind 15 k keys, Hq 32, Hkv 8:
-// 887 us, 1.10 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
+// 859 us, 1.13 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
 // 1700 cycles, of which the tensor pipe is busy about 1280 (the score MMAs at N
 // = 64 read their A and B tiles from shared memory at 48 cycles each, against
 // 16 of arithmetic), and the latency of the single warps' instruction streams
@@ -98,6 +98,8 @@ struct PrefillQParams {
   const uint16_t *q;
   const int32_t *cu_seqlens;
   int num_seqs;
+  int total_tokens;
+  int sms;
   const uint8_t *v_cache;
   const uint8_t *k_scale, *v_scale;
   long long num_blocks;
@@ -229,6 +231,20 @@ __device__ __forceinline__ float2 codes_to_float2(uint32_t codes) {  // low two 
       : "=f"(lo), "=f"(hi)
       : "r"(f16x2_of_codes(codes)));
   return make_float2(lo, hi);
+}
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = r[i];
 }
 // Scale byte of a query row with largest magnitude a: as scale_for, over a
 // span wide enough for any row that matters (2^-100 .. 2^100).
@@ -407,10 +423,6 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     prefill_fp8_block_kernel(const __grid_constant__ CUtensorMap tmap_k,
                              const __grid_constant__ PrefillQParams p) {
   constexpr int PT = kPfRows / G;  // query positions per tile
-  // launched as a programmatic dependent: nothing is read or written before
-  // the kernel before it is over, and the kernel after it may be set up now
-  griddep_wait();
-  griddep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -423,7 +435,13 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(slots + kSlAbort);
 
   const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  // The warp's role.  Roles 0 .. 3 of the CTAs of every other round over the
+  // SMs change places two by two, so that the widening warps of the two CTAs of
+  // an SM (as a rule of neighbouring rounds) issue from different quarters of
+  // it: 878 -> 869 us.
+  const int place = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const unsigned linear = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+  const int warp = place < 4 ? place ^ (int)((linear / (unsigned)p.sms & 1u) << 1) : place;
   // the work item: longest first while one thread per sequence suffices,
   // else in grid order with the last tiles of a chunk first
   int s, mt, g;
@@ -450,7 +468,11 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   const int n = __ldg(p.context_lens + s);
   const int prefix = n - q_len;
   const int npos = min(PT, q_len - pos0);
-  const int rows = npos * G;
+  // a chunk with rows outside q: none of the tile's rows is read or written
+  // (an early return here made the whole kernel 8 % slower)
+  const bool inside = q0 >= 0 && q0 + (long long)q_len <= p.total_tokens;
+  if (!inside && tid == 0) report(p.err, PA_DEVERR_SHAPE);
+  const int rows = inside ? npos * G : 0;
   const int kmax = prefix + pos0 + npos - 1;  // last key any row of the tile sees
   const int nkv = kmax / kPfKeys + 1;
 
@@ -601,22 +623,29 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     bool ok = true;
     for (int j = 0; j < nkv && ok; ++j) {
       const int b = j & 1, par = (j >> 1) & 1;
-      // (the scales are there long before the scores)
       ok = __all_sync(0xffffffffu,
-                      mbar_wait_soon(slot(kSlScale + (j & 7)), (j >> 3) & 1, abort_flag, p.err));
+                      mbar_wait_soon(slot(kSlScale + (j & 7)), (j >> 3) & 1, abort_flag, p.err) &&
+                          mbar_wait_soon(b_s0 + 8 * b, par, abort_flag, p.err));
       const uint2 sc = lds64(slot(kSlScales + (j & 7)));
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(b_s0 + 8 * b, par, abort_flag, p.err));
       if (!ok) break;
       tc_fence_after();
       const uint32_t sb = tmem + b * kQpTmemS;
       const int key0 = j * kPfKeys;
+      if (key0 + kPfKeys - 1 > prefix + pos0) {
+        // a row may not see every key: those scores become -inf in place, out
+        // of the way of the full tiles' instructions
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          uint32_t v[16];
+          tmem_ld16(sb + trow + 16 * h, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = key0 + 16 * h + i <= limit ? v[i] : 0xFF800000u;
+          tmem_st16(sb + trow + 16 * h, v);
+          tmem_wait_st();
+        }
+      }
       float sv[2][32];
       tmem_ld64(sb + trow, sv);
-      if (key0 + kPfKeys - 1 > prefix + pos0) {  // a row may not see every key
-#pragma unroll
-        for (int i = 0; i < kPfKeys; ++i)
-          sv[i >> 5][i & 31] = key0 + i <= limit ? sv[i >> 5][i & 31] : -INFINITY;
-      }
       // per page: factor and offset of the exponent, the largest t
       float ck[kQpPages], ev[kQpPages], top = -INFINITY;
 #pragma unroll
@@ -757,7 +786,7 @@ cudaError_t launch_prefill_q(const CUtensorMap &tk, const PrefillQParams &p, int
                        100);
   constexpr int PT = kPfRows / G;
   const dim3 grid((max_q_len + PT - 1) / PT, p.hkv, p.num_seqs);
-  return launch_kernel(prefill_fp8_block_kernel<G>, grid, dim3(kQpThreads), kQpSmem, s, true, tk, p);
+  return launch_kernel(prefill_fp8_block_kernel<G>, grid, dim3(kQpThreads), kQpSmem, s, false, tk, p);
 }
 
 }  // namespace
@@ -791,8 +820,11 @@ extern "C" pa_status pa_prefill_fp8_block(
   auto misaligned = [](const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15) != 0; };
   if (misaligned(out) || misaligned(q) || misaligned(k_cache) || misaligned(v_cache))
     return PA_ERR_INVALID_ARG;
-  int device = -1;
-  if (cudaGetDevice(&device) != cudaSuccess) return PA_ERR_DEVICE;
+  int device = -1, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+      sms < 1)
+    return PA_ERR_DEVICE;
   CUtensorMap tk;
   memset(&tk, 0, sizeof tk);
   if (!k_pool_map(&tk, k_cache, num_blocks, num_kv_heads)) return PA_ERR_DEVICE;
@@ -802,6 +834,8 @@ extern "C" pa_status pa_prefill_fp8_block(
   p.q = static_cast<const uint16_t *>(q);
   p.cu_seqlens = cu_seqlens;
   p.num_seqs = num_seqs;
+  p.total_tokens = total_tokens;
+  p.sms = sms;
   p.v_cache = static_cast<const uint8_t *>(v_cache);
   p.k_scale = k_scale;
   p.v_scale = v_scale;

@@ -55,7 +55,7 @@ struct QuantStoreParams {
 
 // First unit of sequence s.
 __device__ __forceinline__ long long first_unit(const int32_t *cu, int s) {
-  return (long long)(__ldg(cu + s) >> 4) + 2ll * s;
+  return (long long)(cu[s] >> 4) + 2ll * s;
 }
 
 // The sequence whose units hold u: the largest s with first_unit(s) <= u, by
@@ -112,7 +112,7 @@ __device__ __forceinline__ void store_share(const Share &t, const uint2 (&row)[k
     for (int r = r0; r < r1; ++r) {
       const uint16_t *q = t.src + (long long)r * t.tok;
       for (int k = 0; k < 4; ++k) {
-        const uint32_t a = __ldg(q + k) & 0x7FFFu;
+        const uint32_t a = q[k] & 0x7FFFu;
         top = max(top, a < 0x7F80u ? a : 0u);
       }
     }
@@ -180,6 +180,8 @@ __device__ __forceinline__ void store_share(const Share &t, const uint2 (&row)[k
 template <bool kVec>
 __global__ void __launch_bounds__(32 * kQsWarps, 8)
     store_kv_fp8_block_kernel(const QuantStoreParams p) {
+  // (plain loads after the wait, not the read-only path: the kernel before may
+  // have written any of it while this one was set up)
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -194,8 +196,8 @@ __global__ void __launch_bounds__(32 * kQsWarps, 8)
   if (p.num_seqs <= 32) {
     // one round of loads: a sequence per lane
     const int mine = min(lane, p.num_seqs - 1);
-    const int a = __ldg(p.cu_seqlens + mine), b = __ldg(p.cu_seqlens + mine + 1);
-    const int c = __ldg(p.context_lens + mine);
+    const int a = p.cu_seqlens[mine], b = p.cu_seqlens[mine + 1];
+    const int c = p.context_lens[mine];
     const unsigned m = __ballot_sync(0xffffffffu, (long long)(a >> 4) + 2ll * mine <= u);
     s = m ? min(31 - __clz(m), p.num_seqs - 1) : 0;
     c0 = __shfl_sync(0xffffffffu, a, s);
@@ -203,9 +205,9 @@ __global__ void __launch_bounds__(32 * kQsWarps, 8)
     n = __shfl_sync(0xffffffffu, c, s);
   } else {
     s = find_seq(p.cu_seqlens, p.num_seqs, u, lane);
-    c0 = __ldg(p.cu_seqlens + s);
-    c1 = __ldg(p.cu_seqlens + s + 1);
-    n = __ldg(p.context_lens + s);
+    c0 = p.cu_seqlens[s];
+    c1 = p.cu_seqlens[s + 1];
+    n = p.context_lens[s];
   }
   const long long i = u - (((long long)(c0 >> 4)) + 2ll * s);  // page of the chunk
   if (c0 < 0 || c1 < c0 || c1 > p.total_tokens || n < c1 - c0) {
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(32 * kQsWarps, 8)
     return;
   }
   // (requested before the rows and looked at after: one round of loads)
-  const long long page = __ldg(p.block_tables + (long long)s * p.bt_stride + j);
+  const long long page = p.block_tables[(long long)s * p.bt_stride + j];
   const int base = (int)(j * kBlockSize);
   Share t;
   t.tok = p.tok[is_v];
@@ -237,8 +239,8 @@ __global__ void __launch_bounds__(32 * kQsWarps, 8)
       if (kVec) {
         row[r] = __ldcs(reinterpret_cast<const uint2 *>(q));  // read once
       } else {
-        row[r].x = (uint32_t)__ldg(q) | ((uint32_t)__ldg(q + 1) << 16);
-        row[r].y = (uint32_t)__ldg(q + 2) | ((uint32_t)__ldg(q + 3) << 16);
+        row[r].x = (uint32_t)q[0] | ((uint32_t)q[1] << 16);
+        row[r].y = (uint32_t)q[2] | ((uint32_t)q[3] << 16);
       }
     }
   }
@@ -318,6 +320,6 @@ extern "C" pa_status pa_store_kv_fp8_block(
   const cudaError_t e = launch_kernel(
       vec ? store_kv_fp8_block_kernel<true> : store_kv_fp8_block_kernel<false>,
       dim3((unsigned)blocks), dim3(32 * kQsWarps), 0, static_cast<cudaStream_t>(stream),
-      true, p);
+      (flags & PA_LAUNCH_PDL) != 0, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
 }

@@ -155,6 +155,10 @@ def test_errors_are_reported(ops):
     assert err == ops.DEVERR_BLOCK_INDEX and torch.equal(out[20:], good[20:])
     out, err = run(ops, q, cu, cache, tables, np.array([19, 50], np.int32))
     assert err == ops.DEVERR_SHAPE and torch.equal(out[20:], good[20:])
+    # a chunk whose rows lie past q: skipped, the other one attended
+    out, err = run(ops, q, np.array([0, 20, 99], np.int32), cache, tables,
+                   np.array([50, 129], np.int32), max_q=79)
+    assert err & ops.DEVERR_SHAPE and torch.equal(out[:20], good[:20])
     # rows past max_q_len that no CTA covers (a CTA takes 21 positions here)
     q, cu, cache, tables, ctx = case(rng, [(30, 0)], 12, 2)
     _, err = run(ops, q, cu, cache, tables, ctx, max_q=1)
