@@ -548,8 +548,9 @@ PA_API pa_status pa_decode_fp8(void *out, int32_t out_dtype, const void *q, cons
  *                  longer than its context or past its table row sets
  *                  PA_DEVERR_SHAPE, a table entry outside the pool sets
  *                  PA_DEVERR_BLOCK_INDEX; that sequence or block is skipped.
- *   flags          0 or PA_LAUNCH_PDL (nothing is read before the wait for
- *                  the kernel before).
+ *   flags          0 or PA_LAUNCH_PDL, which mean the same here: nothing is
+ *                  read or written before the kernel before is over, and the
+ *                  kernel after may be set up early.
  * k_cache and v_cache must be 16-byte aligned.  A block written by two
  * sequences of one call is a caller error (fork it first: one of the results,
  * or a mix of both, ends up in it).
@@ -660,7 +661,8 @@ PA_API pa_status pa_decode_noalloc(void *out, int32_t out_dtype, const void *q,
  * change the tables on the device and read nothing back; a call must not
  * overlap another that uses the same tables.  Results do not depend on the
  * order in which threads run.  Arrays are 4-byte aligned; flags: 0 or
- * PA_LAUNCH_PDL (nothing is read before the wait for the kernel before).
+ * PA_LAUNCH_PDL, which mean the same here: nothing is read or written before
+ * the kernel before is over, and the kernel after may be set up early.
  *
  * pa_copy_pages -- for every pair i < n and every pool, page dst[i] becomes a
  * copy of page src[i], n = num_pairs, or min(num_pairs, *count) where the

@@ -31,6 +31,16 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// An index or length: by the read-only path, or by a plain load where the
+// kernel before, which a programmatic launch overlaps, may have written it.
+template <bool kPlain>
+__device__ __forceinline__ int32_t ld_index(const int32_t *p) {
+  if constexpr (kPlain)
+    return *p;
+  else
+    return __ldg(p);
+}
+
 // Launches `kernel`, with programmatic dependent launch when `pdl` is set.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,

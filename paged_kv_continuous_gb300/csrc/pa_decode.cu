@@ -299,6 +299,7 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   p.k_pool8 = r.fp8 ? static_cast<uint8_t *>(const_cast<void *>(r.k_cache)) : nullptr;
   p.v_pool8 = r.fp8 ? static_cast<uint8_t *>(const_cast<void *>(r.v_cache)) : nullptr;
   p.early_kv = (r.flags & PA_LAUNCH_EARLY_KV) != 0;
+  p.wait_first = (r.flags & PA_LAUNCH_PDL) == 0;
   p.min_blocks = r.num_splits == 0 ? kBlockScaleMinBlocks : 0;
   p.positions = r.positions;
   p.cos_table = r.cos_table;
@@ -309,7 +310,7 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
       cudaMemsetAsync(p.counters, 0, (size_t)r.splits * sizeof(int32_t), s) != cudaSuccess)
     return PA_ERR_LAUNCH;
   const int G = r.num_q_heads / r.num_kv_heads;
-  const bool pdl = (r.flags & PA_LAUNCH_PDL) != 0;
+  const bool pdl = (r.flags & PA_LAUNCH_PDL) != 0 || r.k_bscale != nullptr;  // (wait_first)
   // Few sequences over many splits (at least 8 per sequence) with 4 or 8 kv
   // heads: every cut sequence has many pieces of many query heads, and one
   // CTA merging them at the end of the decode kernel sets its end; merge

@@ -119,6 +119,10 @@ struct DecodeParams {
   // previous kernel in the stream completes (the caller guarantees that
   // kernel does not write the pools).
   int early_kv;
+  // BS kernels: nonzero: nothing at all is read before the previous kernel is
+  // over.  So they always launch as programmatic dependents: without the
+  // caller's flag the wait just comes first, and only their set-up moves ahead.
+  int wait_first;
   // BS kernels: blocks a split takes at least (0: as many splits as CTAs)
   int min_blocks;
   // Rotary embedding inside the fused store (ROPE kernels): sequence b's new
@@ -286,8 +290,9 @@ struct DecodeCtl {
 };
 static_assert(sizeof(DecodeCtl) <= 512, "control words do not fit their 512 bytes");
 
+template <bool kPlain = false>
 __device__ __forceinline__ int seq_blocks(const int32_t *ctx, int b) {
-  const int n = __ldg(ctx + b);
+  const int n = ld_index<kPlain>(ctx + b);
   return n > 0 ? ceil_div_blocks(n) : 0;
 }
 
@@ -299,13 +304,14 @@ __device__ __forceinline__ int seq_blocks(const int32_t *ctx, int b) {
 // and placed with a warp scan, so a chunk costs one round of loads however
 // many sequences it crosses.  The position then moves past the chunk.  All
 // 32 lanes must call it with the same position (the result is uniform).
+template <bool kPlain>
 __device__ __forceinline__ int walk_chunk(const int32_t *ctx_arr, int batch, int &b, int &ctx,
                                           int &j, long long remaining, int lane, int &lb,
                                           int &lj, int &lctx) {
   while (j >= (ctx > 0 ? ceil_div_blocks(ctx) : 0)) {  // leave finished / empty sequences
     if (b + 1 >= batch) return 0;  // inconsistent with the block count: stop the walk
     ++b;
-    ctx = __ldg(ctx_arr + b);
+    ctx = ld_index<kPlain>(ctx_arr + b);
     j = 0;
   }
   const int rem = ceil_div_blocks(ctx) - j;  // blocks left in b (>= 1)
@@ -313,7 +319,7 @@ __device__ __forceinline__ int walk_chunk(const int32_t *ctx_arr, int batch, int
   int nctx = 0, nn = 0;
   if (rem < count) {
     const int bb = b + 1 + lane;
-    nctx = bb < batch ? __ldg(ctx_arr + bb) : 0;
+    nctx = bb < batch ? ld_index<kPlain>(ctx_arr + bb) : 0;
     nn = nctx > 0 ? ceil_div_blocks(nctx) : 0;
   }
   int incl = nn;
@@ -905,6 +911,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   const int lane = tid & 31;
   long long nsplit = p.num_splits;
   const long long c = blockIdx.x;
+  if constexpr (BS) {
+    if (p.wait_first) griddep_wait();
+  }
 
   // ---- 1. block counts of all sequences: the total N, this CTA's block range
   //         [lo, hi) and the sequence that holds block lo.  One block-wide
@@ -924,7 +933,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     long long running = 0;
     for (int base = 0; base < p.batch; base += blockDim.x) {
       const int b = base + tid;
-      const int n = b < p.batch ? seq_blocks(p.context_lens, b) : 0;
+      const int n = b < p.batch ? seq_blocks<BS>(p.context_lens, b) : 0;
       long long incl = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -966,7 +975,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     long long running = 0;
     for (int base = 0; base < p.batch; base += blockDim.x) {
       const int b = base + tid;
-      const int n = b < p.batch ? seq_blocks(p.context_lens, b) : 0;
+      const int n = b < p.batch ? seq_blocks<BS>(p.context_lens, b) : 0;
       long long incl = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -1002,7 +1011,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // t0, t0 + nt, ...
   auto zero_empty_rows = [&](int t0, int nt) {
     for (long long b = c; b < p.batch; b += nsplit)
-      if (__ldg(p.context_lens + b) <= 0)
+      if (ld_index<BS>(p.context_lens + b) <= 0)
         for (int i = 2 * t0; i < S::HQ * kHeadDim; i += 2 * nt)
           store_out2(p.out, p.out_f32, b * S::HQ * kHeadDim + i, 0.f, 0.f);
   };
@@ -1095,14 +1104,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
     };
     int b = first_b;
-    int ctx = __ldg(p.context_lens + b);
+    int ctx = ld_index<BS>(p.context_lens + b);
     int j = (int)(lo - first_prefix);
     long long gb = lo, issued = 0;
     bool stop = false;
     bool waited = false;
     while (gb < hi && !stop) {
       int lb, lj, lctx;
-      const int count = walk_chunk(p.context_lens, p.batch, b, ctx, j, hi - gb, lane, lb, lj, lctx);
+      const int count = walk_chunk<BS>(p.context_lens, p.batch, b, ctx, j, hi - gb, lane, lb, lj, lctx);
       if (count == 0) {
         wait_prev_then_release();
         if (lane == 0) report(p.err, PA_DEVERR_SHAPE);
@@ -1110,7 +1119,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       // all block-table entries of the chunk in one round of loads
       const bool in_row = lane < count && lj < p.bt_stride;
-      const long long phys = in_row ? __ldg(p.block_tables + (long long)lb * p.bt_stride + lj) : -1;
+      const long long phys = in_row ? ld_index<BS>(p.block_tables + (long long)lb * p.bt_stride + lj) : -1;
       int n_early = 0;  // stages of this chunk whose K/V pages went out before the wait
       if (!waited) {
         // the first chunk's descriptors are ready.  With p.early_kv the K/V
@@ -1434,7 +1443,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // and the first stage.  (The rows of empty sequences are the epilogue
   // warp's.)
   int wb = first_b;
-  int wctx = __ldg(p.context_lens + wb);
+  int wctx = ld_index<BS>(p.context_lens + wb);
   int wj = (int)(lo - first_prefix);
   bool cons_waited = false;
   const int g = cw % HKV;     // kv head of this warp
@@ -1509,7 +1518,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // the next (up to) 32 blocks: lane L describes block gb0 + L
     int lb = 0, lj = 0, lctx = 0;
     const int count =
-        walk_chunk(p.context_lens, p.batch, wb, wctx, wj, hi - gb0, lane, lb, lj, lctx);
+        walk_chunk<BS>(p.context_lens, p.batch, wb, wctx, wj, hi - gb0, lane, lb, lj, lctx);
     if (!cons_waited) {
       // the first chunk is walked: now wait for the previous kernel, then
       // read the FP8 scales

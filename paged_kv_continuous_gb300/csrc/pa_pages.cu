@@ -5,6 +5,11 @@
 // state: a fork takes the lowest free pages, so results do not depend on the
 // order in which blocks of a launch run (the counts are integer sums).
 //
+// Every kernel here is launched as a programmatic dependent, waits for the
+// kernel before it first of all and reads with plain loads (that kernel may
+// have written anything while this one was set up), so that only its set-up
+// moves ahead, about 2 us of a call behind another.
+//
 // Fork and compact are planned by one block, since every pick depends on all
 // earlier ones (a scan over the counts); a second launch, spread over the
 // sequences, applies the plan.  Nothing is read back to the host: the plan's
@@ -497,7 +502,6 @@ extern "C" pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools,
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_DEVICE;
-  bool pdl = (flags & PA_LAUNCH_PDL) != 0;
   for (int first = 0; first < num_pools; first += kCopyPools) {
     const int n = num_pools - first < kCopyPools ? num_pools - first : kCopyPools;
     CopyPagesParams p = {};
@@ -530,9 +534,8 @@ extern "C" pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools,
     long long blocks = (units + kCopyWarps - 1) / kCopyWarps;
     if (blocks > 8ll * sms) blocks = 8ll * sms;
     if (launch_kernel(copy_pages_kernel, dim3((unsigned)blocks), dim3(32 * kCopyWarps), 0,
-                      static_cast<cudaStream_t>(stream), pdl, p) != cudaSuccess)
+                      static_cast<cudaStream_t>(stream), true, p) != cudaSuccess)
       return PA_ERR_LAUNCH;
-    pdl = true;  // a later launch waits for the one before it first of all
   }
   return PA_OK;
 }
@@ -561,7 +564,7 @@ extern "C" pa_status pa_fork_pages(int32_t *block_tables, int32_t block_table_st
                (long long)num_forks * block_table_stride <= kInlineEntries};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
-                    (flags & PA_LAUNCH_PDL) != 0, p) != cudaSuccess)
+                    true, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   if (!p.apply &&
       launch_kernel(fork_apply_kernel, dim3((unsigned)num_forks, row_blocks(block_table_stride)),
@@ -586,7 +589,7 @@ extern "C" pa_status pa_free_pages(int32_t *block_tables, int32_t block_table_st
   if (misaligned4(block_tables, context_lens, seqs, ref_counts, error_flags))
     return PA_ERR_INVALID_ARG;
   if (launch_kernel(free_pages_kernel, dim3((unsigned)num_seqs), dim3(256), 0,
-                    static_cast<cudaStream_t>(stream), (flags & PA_LAUNCH_PDL) != 0, block_tables,
+                    static_cast<cudaStream_t>(stream), true, block_tables,
                     (long long)block_table_stride, context_lens, (int)num_rows, seqs, ref_counts,
                     (long long)num_blocks, error_flags) != cudaSuccess)
     return PA_ERR_LAUNCH;
@@ -615,7 +618,7 @@ extern "C" pa_status pa_compact_pages(int32_t *block_tables, int32_t block_table
                   num_blocks, copy_src, copy_dst, counts, remap, error_flags};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s,
-                    (flags & PA_LAUNCH_PDL) != 0, p) != cudaSuccess)
+                    true, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   const int per_row = (int)row_blocks(block_table_stride);
   const long long blocks = num_rows > 0 ? (long long)num_rows * per_row : 1;

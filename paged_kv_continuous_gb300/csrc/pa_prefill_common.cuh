@@ -279,7 +279,7 @@ __device__ __forceinline__ int block_excl_scan(int v, int *wsum, int &total) {
   __syncthreads();  // wsum is reused by the next scan
   return before + x - v;
 }
-template <int PT, int NT, typename Params>
+template <int PT, int NT, bool kPlain = false, typename Params>
 __device__ bool pick_work_item(const Params &p, int gx, int *sc, int &s_out, int &mt_out,
                                int &g_out) {
   int *hist = sc;                     // [kLptBins] items per step count
@@ -295,9 +295,9 @@ __device__ bool pick_work_item(const Params &p, int gx, int *sc, int &s_out, int
   const int s0 = min(ns, tid * spt), s1 = min(ns, s0 + spt);
   // pass 1: the histogram (runs of equal counts added at once)
   for (int s = s0; s < s1; ++s) {
-    const int q_len = __ldg(p.cu_seqlens + s + 1) - __ldg(p.cu_seqlens + s);
+    const int q_len = ld_index<kPlain>(p.cu_seqlens + s + 1) - ld_index<kPlain>(p.cu_seqlens + s);
     if (q_len <= 0) continue;
-    const int prefix = __ldg(p.context_lens + s) - q_len;
+    const int prefix = ld_index<kPlain>(p.context_lens + s) - q_len;
     if (prefix < 0) {
       report(p.err, PA_DEVERR_SHAPE);
       continue;
@@ -350,8 +350,8 @@ __device__ bool pick_work_item(const Params &p, int gx, int *sc, int &s_out, int
   // pass 3: the j-th item of bin vb in (s, mt, g) order
   int cnt = 0;
   for (int s = s0; s < s1; ++s) {
-    const int q_len = __ldg(p.cu_seqlens + s + 1) - __ldg(p.cu_seqlens + s);
-    const int prefix = __ldg(p.context_lens + s) - q_len;
+    const int q_len = ld_index<kPlain>(p.cu_seqlens + s + 1) - ld_index<kPlain>(p.cu_seqlens + s);
+    const int prefix = ld_index<kPlain>(p.context_lens + s) - q_len;
     if (q_len <= 0 || prefix < 0) continue;
     const int T = min((q_len + PT - 1) / PT, gx);
     for (int mt = 0; mt < T; ++mt) cnt += lpt_bin(prefix, q_len, mt, PT) == vb ? hkv : 0;
@@ -361,8 +361,8 @@ __device__ bool pick_work_item(const Params &p, int gx, int *sc, int &s_out, int
   if (j >= before && j < before + cnt) {
     int k = j - before;
     for (int s = s0; s < s1 && k >= 0; ++s) {
-      const int q_len = __ldg(p.cu_seqlens + s + 1) - __ldg(p.cu_seqlens + s);
-      const int prefix = __ldg(p.context_lens + s) - q_len;
+      const int q_len = ld_index<kPlain>(p.cu_seqlens + s + 1) - ld_index<kPlain>(p.cu_seqlens + s);
+      const int prefix = ld_index<kPlain>(p.context_lens + s) - q_len;
       if (q_len <= 0 || prefix < 0) continue;
       const int T = min((q_len + PT - 1) / PT, gx);
       for (int mt = 0; mt < T; ++mt) {

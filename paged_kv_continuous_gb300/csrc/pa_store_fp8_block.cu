@@ -180,8 +180,9 @@ __device__ __forceinline__ void store_share(const Share &t, const uint2 (&row)[k
 template <bool kVec>
 __global__ void __launch_bounds__(32 * kQsWarps, 8)
     store_kv_fp8_block_kernel(const QuantStoreParams p) {
-  // (plain loads after the wait, not the read-only path: the kernel before may
-  // have written any of it while this one was set up)
+  // Always a programmatic dependent: it waits for the kernel before first of
+  // all, so only its set-up moves ahead.  Plain loads, not the read-only path:
+  // that kernel may have written any of it while this one was set up.
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -320,6 +321,6 @@ extern "C" pa_status pa_store_kv_fp8_block(
   const cudaError_t e = launch_kernel(
       vec ? store_kv_fp8_block_kernel<true> : store_kv_fp8_block_kernel<false>,
       dim3((unsigned)blocks), dim3(32 * kQsWarps), 0, static_cast<cudaStream_t>(stream),
-      (flags & PA_LAUNCH_PDL) != 0, p);
+      true, p);
   return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
 }
