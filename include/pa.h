@@ -571,9 +571,9 @@ PA_API pa_status pa_store_kv_fp8_block(
  * the softmax weights are rounded to f16 (11 bits) after taking in the V
  * scale of their block, the scores, sums and outputs stay fp32.  Same
  * workspace, flags and outputs as pa_decode, and the same splits for
- * num_splits > 0; with num_splits = 0 the number of splits in use is
- * min(pa_decode_default_splits, ceil(N / 10)), N being the blocks of all
- * sequences (the workspace is that of pa_decode_default_splits).  (With
+ * num_splits > 0; with num_splits = 0 the kernel uses as many of the
+ * pa_decode_default_splits as suit the blocks it finds (about sqrt(blocks *
+ * batch); the workspace is that of pa_decode_default_splits).  (With
  * PA_LAUNCH_EARLY_KV the pools must not be written by the kernel before; the
  * scale arrays are read after it).  k_scale and v_scale must be 8-byte
  * aligned; NULL or unaligned: PA_ERR_INVALID_ARG.

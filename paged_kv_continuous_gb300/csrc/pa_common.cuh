@@ -264,12 +264,20 @@ __device__ __forceinline__ long long split_begin(long long c, long long S, long 
   if (!split_light_tail(S, N)) return c * N / S;
   return N * split_weight_before(c, S) / split_weight_before(S, S);
 }
-// The splits in use of S when each is to take at least min_blocks of the N
-// blocks (0: all of them).
-__device__ __forceinline__ long long capped_splits(long long S, long long N, int min_blocks) {
-  if (min_blocks <= 0) return S;
-  const long long want = (N + min_blocks - 1) / min_blocks;
-  return want < 1 ? 1 : want < S ? want : S;
+// The splits in use of S, for N blocks of `batch` sequences, where the caller
+// leaves the count to the block-scaled decode.  kSplitsAll: S.  kSplitsRoot
+// (sequences merged inside the decode kernel): a split's stream costs in
+// proportion to N / splits and a sequence's merge to its pieces, splits / batch,
+// so the best count goes as sqrt(N batch).  kSplitsHalf (the merge kernel, which
+// merges all pieces at once): at least two blocks a split and one split a
+// sequence.  Never more than N: splits without a block make merges slow.
+constexpr int kSplitsAll = 0, kSplitsRoot = 1, kSplitsHalf = 2;
+__device__ __forceinline__ long long splits_in_use(long long S, long long N, int batch, int rule) {
+  if (rule == kSplitsAll) return S;
+  const long long want = rule == kSplitsRoot
+                             ? (long long)(__fsqrt_rn((float)N * (float)batch) + 0.5f)
+                             : max((N + 1) / 2, (long long)batch);
+  return max(1ll, min(S, min(want, N)));
 }
 // The split holding global block x: the largest c with split_begin(c) <= x,
 // i.e. the largest c with W(c) <= floor(((x + 1) W(S) - 1) / N).

@@ -25,13 +25,8 @@ struct MergeParams {
   int batch;
   int num_q_heads;
   int num_splits;
-  int min_blocks = 0;  // block-scaled pools: blocks a split takes at least
+  int split_rule = kSplitsAll;  // block-scaled pools: the splits in use
 };
-
-// Blocks that a split of the block-scaled decode takes at least when the
-// caller leaves the split count to the library: fewer, and the merges of many
-// short pieces cost more than the streams they shorten.
-constexpr int kBlockScaleMinBlocks = 10;
 
 constexpr int kMergeWarps = 4;   // warps per (sequence, head) row, a quarter of its pieces each
 constexpr int kMergeChunk = 16;  // pieces whose loads are in flight together in one warp
@@ -136,7 +131,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergePara
     N += red[0][w];
     P += red[1][w];
   }
-  const long long S = capped_splits(p.num_splits, N, p.min_blocks);
+  const long long S = splits_in_use(p.num_splits, N, p.batch, p.split_rule);
   const int n = seq_blocks(p.context_lens, b);
   if (n == 0) return;
   const long long c0 = split_of_block(P, S, N), c1 = split_of_block(P + n - 1, S, N);
@@ -300,7 +295,6 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   p.v_pool8 = r.fp8 ? static_cast<uint8_t *>(const_cast<void *>(r.v_cache)) : nullptr;
   p.early_kv = (r.flags & PA_LAUNCH_EARLY_KV) != 0;
   p.wait_first = (r.flags & PA_LAUNCH_PDL) == 0;
-  p.min_blocks = r.num_splits == 0 ? kBlockScaleMinBlocks : 0;
   p.positions = r.positions;
   p.cos_table = r.cos_table;
   p.sin_table = r.sin_table;
@@ -317,6 +311,11 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   // them in merge_kernel instead, spread over all splits and heads.
   const bool split_merge = !r.positions && r.num_kv_heads >= 4 &&
                            (long long)r.splits >= 8LL * r.batch;
+  // (explicit counts are kept: their partition is documented).  Measured against
+  // all 152 splits: 8 sequences of 55 blocks 15.4 against 21.8 us, one of 250
+  // 15.6 / 35.4, 96 of one block 7.4 / 7.7, and with the merge kernel 4 of 44
+  // blocks 13.4 / 12.7, one of 250 14.7 / 17.9.
+  p.split_rule = r.num_splits != 0 ? kSplitsAll : split_merge ? kSplitsHalf : kSplitsRoot;
   cudaError_t e;
   if (r.k_bscale) {
     switch (r.num_kv_heads) {
@@ -378,7 +377,7 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
     m.batch = r.batch;
     m.num_q_heads = r.num_q_heads;
     m.num_splits = r.splits;
-    if (r.k_bscale) m.min_blocks = p.min_blocks;
+    if (r.k_bscale) m.split_rule = p.split_rule;
     if (launch_merge(m, s, true) != cudaSuccess) return PA_ERR_LAUNCH;
   }
   return PA_OK;

@@ -123,8 +123,8 @@ struct DecodeParams {
   // over.  So they always launch as programmatic dependents: without the
   // caller's flag the wait just comes first, and only their set-up moves ahead.
   int wait_first;
-  // BS kernels: blocks a split takes at least (0: as many splits as CTAs)
-  int min_blocks;
+  // BS kernels: how many of the splits are used (kSplits*)
+  int split_rule;
   // Rotary embedding inside the fused store (ROPE kernels): sequence b's new
   // token sits at position positions[b]; its q rows and its new K row are
   // rotated with row positions[b] of the float32 tables [max_position][64]
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         // last pass: N is known, and (one-pass batches) so is this
         // sequence's first block
         N = running;
-        if constexpr (BS) nsplit = capped_splits(nsplit, N, p.min_blocks);
+        if constexpr (BS) nsplit = splits_in_use(nsplit, N, p.batch, p.split_rule);
         if (base == 0 && b < p.batch && n > 0) {
           const long long lo1 = split_begin(c, nsplit, N), hi1 = split_begin(c + 1, nsplit, N);
           const long long prefix = before + incl - n;
