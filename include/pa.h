@@ -813,11 +813,14 @@ PA_API pa_status pa_prefill_store_varlen(void *out, int32_t out_dtype, const voi
  * 2^(scale byte - 127).  Store the chunks with pa_store_kv_fp8_block first
  * (their keys are read from the cache, as rounded there).  Arguments, outputs
  * and errors as pa_prefill_varlen, plus k_scale / v_scale (uint8
- * [num_blocks][num_kv_heads]).  Products run on the tensor cores in f16 with
- * fp32 accumulation: codes are exact, q is rounded to f16 (exact for bf16
- * magnitudes 2^-14 .. 65504, larger ones saturate) and the softmax weights to
- * f16 (11 bits) after taking in the V scale of their block.  Rows past
- * cu_seqlens[num_seqs] are neither read nor written.  A NaN code of a value
+ * [num_blocks][num_kv_heads]).  Products run on the tensor cores with fp32
+ * accumulation.  A query row times a power of two enters as the sum of two
+ * E4M3 terms, exact for elements down to 2^-10 of the row's largest and within
+ * 2^-17 of that largest below; the codes are exact; the softmax weights are
+ * rounded to f16 (11 bits) after taking in the V scale of their block.  A
+ * query row with a NaN or an infinity gives NaN.  Rows past
+ * cu_seqlens[num_seqs] are neither read nor written; a chunk with rows outside
+ * [0, total_tokens) sets PA_DEVERR_SHAPE and is skipped.  A NaN code of a value
  * reaches every row of the 64-key tile that holds it, earlier rows included.
  */
 PA_API pa_status pa_prefill_fp8_block(

@@ -17,7 +17,8 @@
 // largest magnitude in (224, 448], is the sum of two E4M3 terms.  A bf16 has 8
 // significant bits; the rounded first term leaves a remainder of at most 4
 // bits, which the second holds exactly wherever the element is at least
-// 2^-11 of the row's largest (below, the error is 2^-19 of the largest).  Two
+// 2^-10 of the row's largest (below, the error is under 2^-17 of the largest).
+// Two
 // passes at the FP8 rate cost what one f16 pass would, and K needs no
 // conversion: its pages arrive by TMA in the layout the MMA reads.
 //
@@ -32,10 +33,10 @@
 // tensor pipe.
 //
 // What bounds it (two chunks of 2 k queries behind 15 k keys, Hq 32, Hkv 8:
-// 859 us, 1.13 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
+// 851 us, 1.14 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
 // 1700 cycles, of which the tensor pipe is busy about 1280 (the score MMAs at N
 // = 64 read their A and B tiles from shared memory at 48 cycles each, against
-// 16 of arithmetic), and the latency of the single warps' instruction streams
+// 32 of arithmetic), and the latency of the single warps' instruction streams
 // sets the rest; the last of four waves of CTAs is a sixth full.  Tried: two
 // warps widening K and V from plain loads into f16 tiles, 2068 us (the loads'
 // latency); scale bytes loaded tile by tile, 1366 us (the same, in warp 0); one

@@ -644,14 +644,25 @@ def _need_error_flags(t):
             raise PagedAttentionError("error_flags must hold an int32 word")
 
 
-def _need_tables(block_tables, context_lens, batch):
+def _need_table_rows(block_tables):
+    """Contiguous rows that do not overlap, the last one with room for a whole
+    row stride (the kernels know a row by its stride)."""
     _need(block_tables, torch.int32, "block_tables", 2)
+    rows, width = block_tables.shape
+    if not rows:
+        return
+    step = block_tables.stride(0)
+    if width < 1 or (width > 1 and block_tables.stride(1) != 1) or step < width:
+        raise PagedAttentionError("block_tables rows must be contiguous and apart")
+    if 4 * (block_tables.storage_offset() + rows * step) > block_tables.untyped_storage().nbytes():
+        raise PagedAttentionError("block_tables needs room for its last row's whole stride")
+
+
+def _need_tables(block_tables, context_lens, batch):
+    _need_table_rows(block_tables)
     _need_contiguous(context_lens, torch.int32, "context_lens", (batch,))
     if block_tables.shape[0] < batch:
         raise PagedAttentionError("block_tables needs one row per sequence")
-    if batch and (block_tables.shape[1] < 1 or block_tables.stride(1) != 1 or
-                  block_tables.stride(0) < block_tables.shape[1]):
-        raise PagedAttentionError("block_tables rows must be contiguous and apart")
 
 
 def fp8_block_pools(num_blocks, num_kv_heads, head_dim=128, block_size=16, device=None):
@@ -850,11 +861,11 @@ def copy_pages(pools, src, dst, count=None, error_flags=None, stream=None, pdl=F
 
 
 def _need_rows(block_tables, context_lens, ref_counts, error_flags):
-    _need(block_tables, torch.int32, "block_tables", 2)
+    _need_table_rows(block_tables)
     rows = block_tables.shape[0]
-    if rows and (block_tables.shape[1] < 1 or block_tables.stride(1) != 1 or
-                 (rows > 1 and block_tables.stride(0) < block_tables.shape[1])):
-        raise PagedAttentionError("block_tables rows must be contiguous and apart")
+    if rows and block_tables.stride(0) != block_tables.shape[1]:
+        # a row is written up to its stride
+        raise PagedAttentionError("block_tables must be contiguous")
     _need_contiguous(context_lens, torch.int32, "context_lens", (rows,))
     _need_contiguous(ref_counts, torch.int32, "ref_counts", dims=1)
     _need_error_flags(error_flags)

@@ -326,6 +326,90 @@ def test_decode_bad_table_entry_is_reported(ops):
     assert np.all(err <= ref.tolerance(want, mag, tiny))
 
 
+def test_decode_many_sequences(ops):
+    """More sequences than a CTA has threads, one to three blocks each."""
+    rng = np.random.default_rng(503)
+    ctx = rng.integers(0, 41, 400).astype(np.int32)
+    tables = random_tables(rng, np.maximum(ctx, 1), 1300)
+    for Hq, Hkv in ((2, 1), (8, 4)):
+        check_decode(ops, normal_bits(rng, (400, Hq, 128)), ref.random_cache(rng, 1300, Hkv),
+                     tables, ctx, SCALE)
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 4, 8])
+def test_decode_default_splits_over_batches(ops, Hkv):
+    """The splits in use with the default count, from one block to thousands,
+    alone and beside others."""
+    rng = np.random.default_rng(504 + Hkv)
+    for lens in ([1], [20], [300], [5000], [17, 16, 4], [900] * 5, [60, 2000, 1, 0, 0, 33] * 4,
+                 [16] * 21):
+        ctx = np.array(lens, np.int32)
+        NB = int(((ctx + 15) // 16).sum()) + 2
+        tables = random_tables(rng, np.maximum(ctx, 1), NB + len(lens))
+        check_decode(ops, normal_bits(rng, (len(lens), 4 * Hkv, 128)),
+                     ref.random_cache(rng, NB + len(lens), Hkv), tables, ctx, SCALE)
+
+
+def test_pools_past_four_gigabytes(ops):
+    """Pages at the far end of pools of 5 GB each: offsets need 64 bits in the
+    store, the decode and the prefill."""
+    rng = np.random.default_rng(505)
+    NB, Hkv, Hq = 1_250_000, 2, 12
+    spec = [(40, 0), (17, 30)]
+    cu, ctx, tables, k, v = chunks(rng, spec, 10, Hkv)
+    cache = ref.random_cache(rng, 10, Hkv)
+    pools = ops.fp8_block_pools(NB, Hkv, device="cuda")
+    far = NB - 10
+    for pool, small in zip(pools, dev_cache(cache)):
+        pool[far:] = small
+    td = to_dev_i32(np.where(tables >= 0, tables + far, tables))
+    args = [to_dev_i32(cu), td, to_dev_i32(ctx)]
+    ops.store_kv_fp8_block(to_dev_bf16(k), to_dev_bf16(v), *pools, *args)
+    want = [a.copy() for a in cache]
+    ref.store(k, v, *want, cu, tables, ctx)
+    same_bytes([p[far:] for p in pools], want)
+    q = normal_bits(rng, (2, Hq, 128))
+    out = ops.decode_fp8_block(to_dev_bf16(q), *pools, td, args[2], SCALE,
+                               out_dtype=torch.float32)
+    w, mag, tiny = ref.attention(q, *want, tables, ctx, SCALE)
+    assert np.all(np.abs(out.double().cpu().numpy() - w) <= ref.tolerance(w, mag, tiny))
+    q = normal_bits(rng, (int(cu[-1]), Hq, 128))
+    out = ops.prefill_varlen_fp8_block(to_dev_bf16(q), args[0], *pools, td, args[2], SCALE, 40,
+                                       out_dtype=torch.float32)
+    w, mag, tiny = ref.attention(q, *want, tables, ctx, SCALE, cu)
+    assert np.all(np.abs(out.double().cpu().numpy() - w) <= ref.tolerance(w, mag, tiny))
+
+
+def test_store_many_heads(ops):
+    rng = np.random.default_rng(506)
+    cu, ctx, tables, k, v = chunks(rng, SPECS["ragged"], 30, 64)
+    cache = ref.random_cache(rng, 30, 64)
+    got, err = run_store(ops, k, v, cache, cu, tables, ctx)
+    want = [a.copy() for a in cache]
+    ref.store(k, v, *want, cu, tables, ctx)
+    assert err == 0
+    same_bytes(got, want)
+
+
+def test_strided_tables(ops):
+    """Tables as columns of a wider buffer; a view whose last row has no room
+    for its stride is refused."""
+    rng = np.random.default_rng(507)
+    ctx = np.array([40, 17], np.int32)
+    tables = random_tables(rng, ctx, 12)
+    cache = ref.random_cache(rng, 12, 2)
+    q = normal_bits(rng, (2, 12, 128))
+    wide = torch.full((2, 9), 2 ** 30, dtype=torch.int32, device="cuda")
+    wide[:, :3] = to_dev_i32(tables)
+    out = ops.decode_fp8_block(to_dev_bf16(q), *dev_cache(cache), wide[:, :3], to_dev_i32(ctx),
+                               SCALE, out_dtype=torch.float32)
+    w, mag, tiny = ref.attention(q, *cache, tables, ctx, SCALE)
+    assert np.all(np.abs(out.double().cpu().numpy() - w) <= ref.tolerance(w, mag, tiny))
+    with pytest.raises(ops.PagedAttentionError, match="whole stride"):
+        ops.decode_fp8_block(to_dev_bf16(q), *dev_cache(cache), wide[:, 6:], to_dev_i32(ctx),
+                             SCALE)
+
+
 # ---- together ---------------------------------------------------------------
 
 def test_steps_of_store_and_decode(ops):
@@ -415,3 +499,28 @@ def test_calls_on_another_stream(ops):
     same_bytes(d, want)
     w, mag, tiny = ref.attention(q, *want, tables, ctx, SCALE)
     assert np.all(np.abs(out.double().cpu().numpy() - w) <= ref.tolerance(w, mag, tiny))
+
+
+def test_two_calls_at_once(ops):
+    """Two decode calls in flight on two streams, each with its own workspace
+    and output, give what each gives alone."""
+    rng = np.random.default_rng(602)
+    sets = []
+    for n in (9000, 5):
+        ctx = rng.integers(1, n, 6).astype(np.int32)
+        tables = random_tables(rng, ctx, 3500)
+        cache = dev_cache(ref.random_cache(rng, 3500, 2))
+        out = torch.empty((6, 12, 128), dtype=torch.float32, device="cuda")
+        call = ops.DecodeFp8BlockCall(to_dev_bf16(normal_bits(rng, (6, 12, 128))), *cache,
+                                      to_dev_i32(tables), to_dev_i32(ctx), SCALE, out)
+        alone = call().clone()
+        sets.append((call, alone))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for (call, _), s in zip(sets, streams):
+            call(s)
+    torch.cuda.synchronize()
+    for call, alone in sets:
+        assert torch.equal(call.out, alone)
+        assert ops.read_error_word(call.workspace) == 0

@@ -275,6 +275,16 @@ def test_compact_full_and_empty_pool(ops):
         assert counts.cpu().tolist() == [0, L]
 
 
+def test_tables_must_be_contiguous(ops):
+    wide = torch.zeros((4, 9), dtype=torch.int32, device="cuda")
+    c, r, one = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (4, 20, 1))
+    for fn in (lambda: ops.fork_pages(wide[:, :5], c, one, one, r),
+               lambda: ops.free_pages(wide[:, :5], c, one, r),
+               lambda: ops.compact_pages(wide[:, :5], c, r)):
+        with pytest.raises(ops.PagedAttentionError, match="contiguous"):
+            fn()
+
+
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
 def test_serving_loop(ops, kind):
     """Prompts, a fork into beams, steps that store and decode, beams freed

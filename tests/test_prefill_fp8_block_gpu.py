@@ -94,6 +94,49 @@ def test_scales_far_apart(ops, spread):
     assert np.all(e <= mag * (2.0 ** -11 + 8 * 185 * 2.0 ** -24 + 2.0 ** -16))
 
 
+def test_query_rows_of_any_size(ops):
+    """Rows whose magnitudes lie far apart and far from 1 (each takes its own
+    scale), elements of one row far apart: an element below 2^-11 of the row's
+    largest may be off by 2^-10 where the largest is 224 or more, so by at most
+    2^-17 of it, which moves a score by at most that times the sum of the key's
+    magnitudes, and a weight by that in base e."""
+    rng = np.random.default_rng(10)
+    q, cu, cache, tables, ctx = case(rng, [(40, 60)], 4, 1)
+    kk = np.abs(ref.widen(*cache)[0]).sum(-1).max()
+    f = ref.bf16_to_f64(q)
+    rows = 2.0 ** rng.integers(-60, 60, (40, 4, 1))
+    for spread in (0, 16):
+        x = f * 2.0 ** rng.integers(-spread, 1, f.shape)
+        for scale, y in ((SCALE, x), (SCALE * 2.0 ** -60, x * 2.0 ** 60), (2.0 ** -40, x * rows)):
+            bits = bf16_bits(y.astype(np.float32))
+            out, err = run(ops, bits, cu, cache, tables, ctx, scale)
+            assert err == 0
+            want, mag, tiny = ref.attention(bits, *cache, tables, ctx, scale, cu)
+            top = np.abs(ref.bf16_to_f64(bits)).max(-1, keepdims=True)
+            move = scale * top * 2.0 ** -17 * kk
+            # only rows whose scores stay where a rounding of fp32 is small
+            fine = (scale * top * kk < 2000).squeeze(-1)
+            bound = ref.tolerance(want, mag, tiny, score=3000.0) + 2 * np.expm1(np.minimum(move, 1.0)) * mag
+            e = np.abs(out.double().cpu().numpy() - want)
+            assert fine.any() and np.all(e[fine] <= bound[fine])
+
+
+def test_query_rows_that_are_not_finite(ops):
+    """A NaN or an infinity in a query row makes that row NaN and no other."""
+    rng = np.random.default_rng(11)
+    q, cu, cache, tables, ctx = case(rng, [(30, 40)], 4, 1)
+    good, _ = run(ops, q, cu, cache, tables, ctx)
+    q[3, 1, 7] = 0x7FC0
+    q[9, 0, 0] = 0x7F80
+    q[20, 3, 127] = 0xFF80
+    out, err = run(ops, q, cu, cache, tables, ctx)
+    bad = torch.zeros(30, 4, dtype=torch.bool, device="cuda")
+    for i, h in ((3, 1), (9, 0), (20, 3)):
+        bad[i, h] = True
+    assert err == 0
+    assert torch.all(torch.isnan(out[bad])) and torch.equal(out[~bad], good[~bad])
+
+
 def test_ignores_what_no_key_holds(ops):
     """Stale NaN codes past the last key, unused blocks and table entries."""
     rng = np.random.default_rng(4)
