@@ -88,7 +88,6 @@ constexpr int kSlScales = kSlAbort + 1;
 constexpr int kQpBarBytes = 512;
 static_assert((kSlScales + 8) * 8 <= kQpBarBytes, "barrier slots do not fit");
 constexpr int kQpSmem = 1024 + kQpOffBar + kQpBarBytes;
-static_assert(kWorkOrderBytes <= kQpKStages * kQpCodes, "work-order scratch does not fit");
 // TMEM (256 columns, two CTAs per SM): scores of tile j in buffer j % 2 at 0
 // and 64, P' over the scores it came from (32 columns, two keys each), O at 128
 constexpr int kQpTmemCols = 256, kQpTmemS = 64, kQpTmemO = 128;
@@ -419,6 +418,101 @@ __device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, in
   }
 }
 
+// The work order.  Work items are (sequence s, query tile mt of PT positions,
+// kv head g), an item's length the number of 64-key tiles it attends, and the
+// CTA of linear index r takes the item of rank r, longest first (ties by s, mt,
+// g), so that long items do not start at the end of the grid.  Lengths grow
+// with mt, so the tiles of a sequence that are at least v long are a closed
+// form; every warp finds the length of rank r by bisection over such counts and
+// the item by one scan, a sequence per lane (kSeqsPerLane of them at most), with
+// no barrier.  (A histogram over all items took 8 to 16 thousand cycles, a
+// tenth of a CTA's life; this takes about 2 thousand.)
+constexpr int kSeqsPerLane = 8;
+struct WorkItem {
+  int s, mt, g;  // s < 0: none
+};
+template <int PT>
+__device__ __forceinline__ WorkItem pick_item(const PrefillQParams &p, int gx, int r) {
+  const int lane = threadIdx.x & 31;
+  const int per = (p.num_seqs + 31) / 32;
+  int prefix[kSeqsPerLane], q_len[kSeqsPerLane];
+  int longest = 0;
+#pragma unroll
+  for (int k = 0; k < kSeqsPerLane; ++k) {
+    prefix[k] = q_len[k] = 0;
+    const int s = lane * per + k;
+    if (k < per && s < p.num_seqs) {
+      const int q = p.cu_seqlens[s + 1] - p.cu_seqlens[s];
+      const int pre = p.context_lens[s] - q;
+      // (reported once, by the CTA of rank 0)
+      if (r == 0 && threadIdx.x < 32 && q > 0 && (pre < 0 || q > (long long)gx * PT))
+        report(p.err, PA_DEVERR_SHAPE);
+      if (q > 0 && pre >= 0) {
+        prefix[k] = pre;
+        q_len[k] = q;
+        longest = max(longest, (pre + min(q, gx * PT) - 1) / kPfKeys + 1);
+      }
+    }
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  // tiles of the lane's k-th sequence in the grid, and those shorter than v
+  auto tiles = [&](int k) { return min((q_len[k] + PT - 1) / PT, gx); };
+  auto shorter = [&](int k, int v) -> int {
+    const int need = (v - 1) * kPfKeys - prefix[k] + 1;  // positions up to the tile's end
+    if (need > q_len[k]) return tiles(k);
+    return min(need > 0 ? (need + PT - 1) / PT - 1 : 0, tiles(k));
+  };
+  auto count = [&](int v) -> int {  // all tiles at least v long
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < kSeqsPerLane; ++k)
+      if (k < per) c += tiles(k) - shorter(k, v);
+    return __reduce_add_sync(0xffffffffu, c);
+  };
+  WorkItem item{-1, 0, 0};
+  const int rank = r / p.hkv;
+  if (rank >= count(1)) return item;
+  int lo = 1, hi = longest + 1;  // count(lo) > rank >= count(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (count(mid) > rank)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  // the item is among the tiles of length lo: its place there, (s, mt, g) order
+  int mine = 0;
+#pragma unroll
+  for (int k = 0; k < kSeqsPerLane; ++k)
+    if (k < per) mine += shorter(k, lo + 1) - shorter(k, lo);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int at = r - p.hkv * count(lo + 1);
+  int j = at / p.hkv - (incl - mine);  // among the lane's own tiles
+  const bool here = j >= 0 && j < mine;
+  int s = 0, mt = 0;
+#pragma unroll
+  for (int k = 0; k < kSeqsPerLane; ++k)
+    if (k < per && here && j >= 0) {
+      const int first = shorter(k, lo), n = shorter(k, lo + 1) - first;
+      if (j < n) {
+        s = lane * per + k;
+        mt = first + j;
+      }
+      j -= n;
+    }
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  item.s = __shfl_sync(0xffffffffu, s, src & 31);
+  item.mt = __shfl_sync(0xffffffffu, mt, src & 31);
+  item.g = at % p.hkv;
+  if (src < 0) item.s = -1;
+  return item;
+}
+
 template <int G>
 __global__ void __launch_bounds__(kQpThreads, 2)
     prefill_fp8_block_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -448,13 +542,15 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   const int place = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const unsigned linear = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
   const int warp = place < 4 ? place ^ (int)((linear / (unsigned)p.sms & 1u) << 1) : place;
-  // the work item: longest first while one thread per sequence suffices,
-  // else in grid order with the last tiles of a chunk first
+  // the work item: longest first while a warp's lanes hold the sequences, else
+  // in grid order with the last tiles of a chunk first
   int s, mt, g;
-  if (p.num_seqs <= kQpThreads) {
-    if (!pick_work_item<PT, kQpThreads, true>(p, (int)gridDim.x,
-                                        reinterpret_cast<int *>(smem + kQpOffK), s, mt, g))
-      return;
+  if (p.num_seqs <= 32 * kSeqsPerLane) {
+    const WorkItem item = pick_item<PT>(p, (int)gridDim.x, (int)linear);
+    if (item.s < 0) return;
+    s = item.s;
+    mt = item.mt;
+    g = item.g;
   } else {
     mt = (int)gridDim.x - 1 - (int)blockIdx.x;
     g = blockIdx.y;
