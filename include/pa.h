@@ -573,7 +573,8 @@ PA_API pa_status pa_store_kv_fp8_block(
  * workspace, flags and outputs as pa_decode, and the same splits for
  * num_splits > 0; with num_splits = 0 the kernel uses as many of the
  * pa_decode_default_splits as suit the blocks it finds (about sqrt(blocks *
- * batch); the workspace is that of pa_decode_default_splits).  (With
+ * batch); the workspace is that of pa_decode_default_splits) and may count
+ * the end of a sequence like some blocks when it divides them.  (With
  * PA_LAUNCH_EARLY_KV the pools must not be written by the kernel before; the
  * scale arrays are read after it).  k_scale and v_scale must be 8-byte
  * aligned; NULL or unaligned: PA_ERR_INVALID_ARG.

@@ -158,6 +158,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// mbar_wait where the phase is most likely over, or soon to be: the first try,
+// which the hardware suspends for a while, stands alone in the instruction
+// stream and the rest out of its way.
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, volatile int *abort,
+                                               int32_t *err) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  return mbar_wait(bar, parity, abort, err);
+}
+
 // ---- bulk copies (TMA, non-tensor) ---------------------------------------
 
 // Global -> shared bulk copy completing on an mbarrier.  dst, src and bytes

@@ -316,6 +316,11 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   // 15.6 / 35.4, 96 of one block 7.4 / 7.7, and with the merge kernel 4 of 44
   // blocks 13.4 / 12.7, one of 250 14.7 / 17.9.
   p.split_rule = r.num_splits != 0 ? kSplitsAll : split_merge ? kSplitsHalf : kSplitsRoot;
+  // (units of a piece's end: 2 / 4 / 6 / 8 / 12 took 22.8 / 22.0 / 20.1 / 20.2 /
+  // 20.5 us for 64 log-uniform sequences at 2 kv heads, 28.6 / 27.7 / 28.1 /
+  // 28.3 / 28.8 at 4, 47.0 / 44.6 / 45.5 / 46.2 / 47.5 at 8, where a block takes
+  // longer; for equal ones 6 costs 0.3 us at 2 heads)
+  p.piece_units = p.split_rule != kSplitsRoot ? 0 : r.num_kv_heads <= 2 ? 6 : 4;
   cudaError_t e;
   if (r.k_bscale) {
     switch (r.num_kv_heads) {

@@ -8,6 +8,8 @@
 // N blocks; CTA c of S takes blocks [floor(cN/S), floor((c+1)N/S)).  Every
 // CTA moves the same number of bytes however skewed the lengths are, and
 // consecutive sequences flow through one CTA's pipeline without draining it.
+// (Block scales, default split count: a sequence counts some units beside its
+// blocks, see kWeighted.)
 // A "piece" is the run of one sequence's blocks inside one CTA.  A piece
 // that is the whole sequence writes the output rows.  A cut piece writes a
 // partial (o normalised over its keys, natural-log sum-exp) to the
@@ -125,6 +127,9 @@ struct DecodeParams {
   int wait_first;
   // BS kernels: how many of the splits are used (kSplits*)
   int split_rule;
+  // BS kernels that merge in place: units that a sequence counts beside its
+  // blocks when the work is divided among the splits
+  int piece_units;
   // Rotary embedding inside the fused store (ROPE kernels): sequence b's new
   // token sits at position positions[b]; its q rows and its new K row are
   // rotated with row positions[b] of the float32 tables [max_position][64]
@@ -211,7 +216,8 @@ struct DecodeShape {
   static constexpr int NST_FIT =
       (kDecodeSmemBudget - 1024 - RED_BYTES - MERGE_BYTES - CTL_BYTES - EWW_BYTES - SC_BYTES) /
       (STAGE_BYTES + 16);
-  static constexpr int NST_CAP = NST_FIT > 12 ? 12 : NST_FIT;
+  static constexpr int NST_MAX = BS ? 16 : 12;
+  static constexpr int NST_CAP = NST_FIT > NST_MAX ? NST_MAX : NST_FIT;
   // The ring is a multiple of 2 (each slot is always filled by the same one
   // of the two producer warps) and of NPH (each slot always holds stages of
   // the same phase, so the Hkv consumer warps of that phase wait on every
@@ -277,6 +283,9 @@ struct DecodeCtl {
   int owed_now;  // an owed merge runs beside the final one (consumer thread 0 decides)
   long long first_prefix;    // global index of block 0 of first_b
   int first_b;               // sequence holding this CTA's first block
+  int first_k, weight;       // non-empty sequences before first_b, units each adds
+  long long lo, hi;          // the CTA's blocks (weighted splits; < 0: N)
+  long long units, splits;   // what the splits divide, the splits in use
   int abort;                 // set by a wait that gave up
   int last;                  // this CTA merges the current cut sequence
   // the current piece's sequence: splits pc_cs0..pc_cs1 hold its blocks, in
@@ -316,6 +325,15 @@ __device__ __forceinline__ int walk_chunk(const int32_t *ctx_arr, int batch, int
   }
   const int rem = ceil_div_blocks(ctx) - j;  // blocks left in b (>= 1)
   int count = remaining < 32 ? (int)remaining : 32;
+  if constexpr (kPlain) {
+    if (rem >= count) {  // no sequence ends before the chunk does
+      lb = b;
+      lj = j + lane;
+      lctx = ctx;
+      j += count;
+      return count;
+    }
+  }
   int nctx = 0, nn = 0;
   if (rem < count) {
     const int bb = b + 1 + lane;
@@ -383,6 +401,43 @@ __device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void *src, u
       " [%0], [%1], %2, [%3], %4;\n\t}" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar), "l"(policy)
       : "memory");
+}
+
+// One block of FP8 pools into a ring slot: the K boxes of NPAIR head groups and
+// V's contiguous page, with their bytes added to the slot's barrier, all by one
+// elected lane of a converged warp.
+template <int NPAIR, int HB, int KV_BYTES>
+__device__ __forceinline__ void load_block(uint32_t dst, const CUtensorMap *map, int z,
+                                           const void *v, uint32_t bar, uint64_t policy) {
+  static_assert(NPAIR == 1 || NPAIR == 2 || NPAIR == 4, "head groups");
+#define PA_K_BOX(D, Y)                                                                      \
+  "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"   \
+  ".L2::cache_hint [" D "], [%1, {zero, " Y ", %2}], [%4], %5;\n\t"
+#define PA_BLOCK_HEAD                                                                      \
+  "{\n\t.reg .pred e;\n\t.reg .b32 zero, d1, d2, d3, dv;\n\tmov.u32 zero, 0;\n\t"        \
+  "add.u32 d1, %0, %7;\n\tadd.u32 d2, d1, %7;\n\tadd.u32 d3, d2, %7;\n\t"                 \
+  "add.u32 dv, %0, %6;\n\telect.sync _|e, 0xffffffff;\n\t"                               \
+  "@e mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%4], %8;\n\t"
+#define PA_BLOCK_TAIL                                                                      \
+  "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "   \
+  "[dv], [%3], %6, [%4], %5;\n\t}"
+#define PA_BLOCK_ARGS                                                                      \
+  "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(z), "l"(v), "r"(bar), "l"(policy),   \
+      "n"(KV_BYTES), "n"(HB * kTileBytes), "n"(2 * KV_BYTES)
+  if constexpr (NPAIR == 1)
+    asm volatile(PA_BLOCK_HEAD PA_K_BOX("%0", "0") PA_BLOCK_TAIL ::PA_BLOCK_ARGS : "memory");
+  else if constexpr (NPAIR == 2)
+    asm volatile(PA_BLOCK_HEAD PA_K_BOX("%0", "0") PA_K_BOX("d1", "2") PA_BLOCK_TAIL
+                 ::PA_BLOCK_ARGS
+                 : "memory");
+  else
+    asm volatile(PA_BLOCK_HEAD PA_K_BOX("%0", "0") PA_K_BOX("d1", "2") PA_K_BOX("d2", "4")
+                     PA_K_BOX("d3", "6") PA_BLOCK_TAIL ::PA_BLOCK_ARGS
+                 : "memory");
+#undef PA_K_BOX
+#undef PA_BLOCK_HEAD
+#undef PA_BLOCK_TAIL
+#undef PA_BLOCK_ARGS
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2,
@@ -921,9 +976,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   //         pass (one round of context-length loads, two barriers); larger
   //         batches take a pass for N, then a pass for the search.
   __shared__ long long warp_tot[kDecodeWarps];
+  // BS: with a batch of one pass the splits divide units, of which a sequence
+  // has its blocks and piece_units more behind them (no one's work): the end
+  // of a piece costs a CTA as much as several blocks, and short sequences side
+  // by side would leave one CTA with most of the ends.  64 sequences of 1 to
+  // 8192 keys (12/2 heads): 30.7 -> 20.1 us, 78 -> 20.3 sorted by length.  N counts units from then on, and the
+  // blocks of a sequence are consecutive units, so every split between its
+  // first and its last still holds some of them.
+  constexpr bool kWeighted = BS && !SPLIT_MERGE;
+  constexpr long long kOne = 1ll << 40;  // a non-empty sequence, above the block count
+  int W = kWeighted && p.batch <= (int)blockDim.x ? p.piece_units : 0;
+  long long all_blocks = 0;
+  long long my_first = 0;  // this thread's sequence: global index of its block 0,
+  int my_n = 0, my_k = 0;  // blocks, non-empty sequences before it
   if (tid == 0) {
     ctl->first_b = -1;
     ctl->first_prefix = 0;
+    if constexpr (kWeighted) {
+      ctl->first_k = 0;
+      ctl->lo = ctl->hi = -1;
+    }
     ctl->abort = 0;
     ctl->last = 0;
   }
@@ -935,6 +1007,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const int b = base + tid;
       const int n = b < p.batch ? seq_blocks<BS>(p.context_lens, b) : 0;
       long long incl = n;
+      if constexpr (kWeighted) incl += n > 0 ? kOne : 0;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, incl, off);
@@ -953,8 +1026,28 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         // last pass: N is known, and (one-pass batches) so is this
         // sequence's first block
         N = running;
+        if constexpr (kWeighted) all_blocks = N &= kOne - 1;
         if constexpr (BS) nsplit = splits_in_use(nsplit, N, p.batch, p.split_rule);
-        if (base == 0 && b < p.batch && n > 0) {
+        if constexpr (kWeighted) {
+          if (N <= nsplit) W = 0;  // no split has two blocks
+          N += W * (running / kOne);
+          if (tid == 0) {
+            ctl->weight = W;
+            ctl->units = N;
+            ctl->splits = nsplit;
+          }
+          if (base == 0 && n > 0) {
+            const long long excl = before + incl - n - kOne;
+            my_first = excl & (kOne - 1);
+            my_k = (int)(excl / kOne);
+            my_n = n;
+            const long long v = my_first + (long long)W * my_k;  // unit of its block 0
+            const long long lo1 = split_begin(c, nsplit, N) - v;
+            const long long hi1 = split_begin(c + 1, nsplit, N) - v;
+            if (lo1 >= 0 && lo1 < n + W) ctl->lo = my_first + min(lo1, (long long)n);
+            if (hi1 >= 0 && hi1 < n + W) ctl->hi = my_first + min(hi1, (long long)n);
+          }
+        } else if (base == 0 && b < p.batch && n > 0) {
           const long long lo1 = split_begin(c, nsplit, N), hi1 = split_begin(c + 1, nsplit, N);
           const long long prefix = before + incl - n;
           if (prefix <= lo1 && lo1 < prefix + n && lo1 < hi1) {
@@ -968,8 +1061,22 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   }
   // (BS: no block for the CTAs past the splits in use)
   const bool in_use = !BS || c < nsplit;
-  const long long lo = N && in_use ? split_begin(c, nsplit, N) : 0;
-  const long long hi = N && in_use ? split_begin(c + 1, nsplit, N) : 0;
+  long long lo = N && in_use ? split_begin(c, nsplit, N) : 0;
+  long long hi = N && in_use ? split_begin(c + 1, nsplit, N) : 0;
+  if (kWeighted && p.batch <= (int)blockDim.x) {
+    // (a bound that no sequence holds is the end of all blocks)
+    if (in_use && N) {
+      lo = ctl->lo;
+      hi = ctl->hi;
+      if (hi < 0) hi = all_blocks;
+      if (my_n > 0 && my_first <= lo && lo < my_first + my_n && lo < hi) {
+        ctl->first_b = tid;
+        ctl->first_prefix = my_first;
+        ctl->first_k = my_k;
+      }
+    }
+    __syncthreads();
+  }
   if (p.batch > (int)blockDim.x) {
     // second pass over the prefix sums (batches larger than one pass)
     long long running = 0;
@@ -1109,7 +1216,116 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     long long gb = lo, issued = 0;
     bool stop = false;
     bool waited = false;
-    while (gb < hi && !stop) {
+    if constexpr (BS) {
+      // The chunk's table entries and scale bytes are loaded while the chunk
+      // before it is issued, and a stage is one request and one arrival by the
+      // lane that holds its scales: with the loads at the chunk's head and a
+      // value at a time shuffled, the producers set the pace below 4 kv heads:
+      // 0.33 us a block and CTA at 2 heads, 0.20 so (155 -> 101 us for
+      // 8 x 131072 keys, 5.3 TB/s).
+      struct Chunk {
+        int count, lb, x;    // lane L: sequence and table entry of block L
+        unsigned with_q;     // blocks whose stage carries the q rows
+        bool in_row;
+        uint32_t sk[2], sv[2];
+      };
+      bool broken = false;
+      auto fetch = [&]() -> Chunk {
+        Chunk k;
+        int lj = 0, lctx = 0;
+        k.lb = 0;
+        k.count = gb < hi ? walk_chunk<BS>(p.context_lens, p.batch, b, ctx, j, hi - gb, lane,
+                                           k.lb, lj, lctx)
+                          : 0;
+        broken |= gb < hi && k.count == 0;  // inconsistent with the block count
+        k.in_row = lane < k.count && lj < p.bt_stride;
+        k.x = k.in_row ? ld_index<BS>(p.block_tables + (long long)k.lb * p.bt_stride + lj) : -1;
+        // the q rows go with the first NPH stages of every piece
+        k.with_q = __ballot_sync(0xffffffffu, lane < k.count && min(gb + lane - lo, (long long)lj) <
+                                                                   S::NPH);
+        gb += k.count;
+        return k;
+      };
+      // the entries are here: their scale bytes; a bad one is reported, not read
+      auto settle = [&](Chunk &k) {
+        const bool ok = k.in_row && k.x >= 0 && k.x < p.num_blocks;
+        if (lane < k.count && !ok)
+          report(p.err, k.in_row ? PA_DEVERR_BLOCK_INDEX : PA_DEVERR_SHAPE);
+        if (!ok) k.x = -1;
+        k.sk[0] = k.sk[1] = k.sv[0] = k.sv[1] = 0u;
+        if (ok) {
+          load_scale_bytes<HKV>(p.k_bscale + (long long)k.x * HKV, k.sk);
+          load_scale_bytes<HKV>(p.v_bscale + (long long)k.x * HKV, k.sv);
+        }
+      };
+      // (one copy of each step's code: a second one costs instruction misses
+      // at the start of every call, about 1 us)
+      Chunk cur;
+      cur.count = 0;
+      int early = 0;           // stages requested before the wait
+      int st = pw, round = 0;  // ring slot of this warp's next stage, and its use
+      while (!stop) {
+        Chunk next = fetch();
+        if (!waited) {
+          if (p.early_kv) {
+            early = min(next.count, min(S::NST, kDecodeEarlyStages));
+            for (int i = pw; i < early; i += kDecodeProducerWarps)
+              issue_kv_stage(i, __shfl_sync(0xffffffffu, next.x, i), true);
+          }
+          wait_prev_then_release();
+          waited = true;
+        }
+        int i = (int)(issued ^ pw) & 1;
+#pragma unroll 1
+        for (int half = 16; half <= 32 && !stop; half += 16) {
+          const int end = min(cur.count, half);
+#pragma unroll 1
+          for (; i < end; i += kDecodeProducerWarps) {
+            const uint32_t dst = stage0 + st * S::STAGE_BYTES;
+            const uint32_t bar = full0 + 8 * st;
+            if (round > 0 &&
+                !__all_sync(0xffffffffu, mbar_wait_soon(empty0 + 8 * st, (round - 1) & 1,
+                                                        abort_flag, p.err))) {
+              stop = true;
+              break;
+            }
+            const int x = __shfl_sync(0xffffffffu, cur.x, i);
+            if (x >= 0 && (issued + i >= early))
+              load_block<S::NPAIR, S::HB, S::KV_BYTES>(dst, &tmap_k, x * kBlockSize,
+                                                       p.v_pool + (long long)x * S::KV_BYTES,
+                                                       bar, pol_kv);
+            if ((cur.with_q >> i) & 1u) {
+              const int b_i = __shfl_sync(0xffffffffu, cur.lb, i);
+              if (lane == 0) mbar_expect_tx(bar, S::Q_BYTES);
+              __syncwarp();
+              bulk_load_elect(dst + 2 * S::KV_BYTES, q_base + (long long)b_i * S::HQ * kHeadDim,
+                              S::Q_BYTES, bar, pol_q);
+            }
+            __syncwarp();  // every expected byte is counted before the arrival
+            if (lane == i) {
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(scale0 + 16 * st),
+                           "r"(clamp_scales4(cur.sk[0])), "r"(clamp_scales4(cur.sk[1])),
+                           "r"(clamp_scales4(cur.sv[0])), "r"(clamp_scales4(cur.sv[1]))
+                           : "memory");
+              mbar_arrive(bar);
+            }
+            __syncwarp();
+            st += kDecodeProducerWarps;
+            if (st >= S::NST) {
+              st -= S::NST;
+              ++round;
+            }
+          }
+          if (half == 16) settle(next);
+        }
+        // (after a stop: this warp's stages below i are the ones in flight)
+        issued += stop ? i : cur.count;
+        if (next.count == 0) break;
+        cur = next;
+      }
+      if (broken && lane == 0) report(p.err, PA_DEVERR_SHAPE);
+    }
+    while (!BS && gb < hi && !stop) {
       int lb, lj, lctx;
       const int count = walk_chunk<BS>(p.context_lens, p.batch, b, ctx, j, hi - gb, lane, lb, lj, lctx);
       if (count == 0) {
@@ -1137,15 +1353,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         wait_prev_then_release();
         waited = true;
       }
-      // BS: lane L loads the scale bytes of block L (K's Hkv bytes in sk, V's
-      // in sv); they are needed only when a stage is armed, behind its copies
-      uint32_t sk[2] = {0u, 0u}, sv[2] = {0u, 0u};
-      if constexpr (BS) {
-        if (phys >= 0 && phys < p.num_blocks) {
-          load_scale_bytes<HKV>(p.k_bscale + phys * HKV, sk);
-          load_scale_bytes<HKV>(p.v_bscale + phys * HKV, sv);
-        }
-      }
       // the q rows go with the first NPH stages of every piece: each consumer
       // warp reads them from its own first stage of the piece
       const bool with_q = min(gb + lane - lo, (long long)lj) < S::NPH;
@@ -1169,32 +1376,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const uint32_t dst = stage0 + st * S::STAGE_BYTES;
         const uint32_t bar = full0 + 8 * st;
         const bool pre = i < n_early;  // K/V already requested and counted
-        if constexpr (BS) {
-          // raise the expected bytes, issue the copies, then write the scales
-          // and arrive: the loads of the scales and the copies overlap
-          if (lane == 0 && q_i) mbar_expect_tx(bar, S::Q_BYTES);
-          __syncwarp();
-          if (!pre) issue_kv_stage(st, ph_i, true);
-          if (q_i)
-            bulk_load_elect(dst + 2 * S::KV_BYTES, q_base + (long long)b_i * S::HQ * kHeadDim,
-                            S::Q_BYTES, bar, pol_q);
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            w[x] = __shfl_sync(0xffffffffu, sk[x], i);
-            w[2 + x] = __shfl_sync(0xffffffffu, sv[x], i);
-          }
-          if (lane == 0) {
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(scale0 + 16 * st),
-                         "r"(clamp_scales4(w[0])), "r"(clamp_scales4(w[1])),
-                         "r"(clamp_scales4(w[2])), "r"(clamp_scales4(w[3]))
-                         : "memory");
-            mbar_arrive(bar);
-            if (!ok) report(p.err, row_i ? PA_DEVERR_BLOCK_INDEX : PA_DEVERR_SHAPE);
-          }
-          __syncwarp();
-          continue;
-        }
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, (ok && !pre ? 2u * S::KV_BYTES : 0u) +
                                          (q_i ? S::Q_BYTES + S::ROPE_BYTES : 0u));
@@ -1442,6 +1623,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // walk's loads would otherwise be dependent round trips between the wait
   // and the first stage.  (The rows of empty sequences are the epilogue
   // warp's.)
+  // (kWeighted: read again where a piece ends, not kept in registers)
+  auto units = [&]() -> long long {
+    if constexpr (kWeighted) return *reinterpret_cast<volatile long long *>(&ctl->units);
+    return N;
+  };
+  auto splits = [&]() -> long long {
+    if constexpr (kWeighted) return *reinterpret_cast<volatile long long *>(&ctl->splits);
+    return nsplit;
+  };
   int wb = first_b;
   int wctx = ld_index<BS>(p.context_lens + wb);
   int wj = (int)(lo - first_prefix);
@@ -1487,20 +1677,22 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   bool pc_done = false;
   auto piece_splits = [&](long long gb, int j, int n) {
     const long long P = gb - j;  // global index of block 0 of the sequence
-    const long long cs0 = split_of_block(P, nsplit, N);
-    const long long cs1 = split_of_block(P + n - 1, nsplit, N);
+    long long u = P;  // its unit
+    if constexpr (kWeighted) u += (long long)ctl->weight * (ctl->first_k + npieces);
+    const long long cs0 = split_of_block(u, splits(), units());
+    const long long cs1 = split_of_block(u + n - 1, splits(), units());
     long long pieces = cs1 - cs0 + 1;
-    if (N < nsplit) {
+    if (units() < splits()) {
       pieces = 1;
       for (long long cc = cs0 + 1; cc <= cs1; ++cc)
-        pieces += split_begin(cc, nsplit, N) < split_begin(cc + 1, nsplit, N) ? 1 : 0;
+        pieces += split_begin(cc, splits(), units()) < split_begin(cc + 1, splits(), units()) ? 1 : 0;
     }
     ctl->pc_cs0 = cs0;
     ctl->pc_cs1 = cs1;
     ctl->pc_pieces = (int)pieces;
     pc_done = true;
     const long long last_blk = P + n - 1;
-    if (last_blk >= hi - 1 && (P < lo || last_blk > hi - 1) && N >= nsplit &&
+    if (last_blk >= hi - 1 && (P < lo || last_blk > hi - 1) && units() >= splits() &&
         pieces <= S::MERGE_MAX_PIECES) {
       // the CTA's final piece, cut (and mergeable from shared memory): the
       // epilogue warp watches its sequence's arrival counter meanwhile
@@ -1555,11 +1747,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const long long gb = gb0 + pos, it = it0 + pos;
       const bool piece_last = (m_last >> pos) & 1u;
       if ((m_mine >> pos) & 1u) {
-        const int sidx = (int)(it % S::NST);
+        // (BS: a CTA's blocks fit 32 bits, whose division is a multiplication)
+        const std::conditional_t<BS, unsigned, long long> itn = it;
+        const int sidx = (int)(itn % S::NST);
         const uint32_t sbase = stage0 + sidx * S::STAGE_BYTES;
         // warp-uniform: the collective instructions below need every lane
         const bool have = __all_sync(
-            0xffffffffu, mbar_wait(full0 + 8 * sidx, (int)((it / S::NST) & 1), abort_flag, p.err));
+            0xffffffffu, mbar_wait(full0 + 8 * sidx, (int)((itn / S::NST) & 1), abort_flag, p.err));
         if (need_q) {
           // this warp's first stage of the piece: it carries the q rows
           need_q = false;
@@ -1958,7 +2152,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         L0 += __shfl_xor_sync(0xffffffffu, L0, off);
         L1 += __shfl_xor_sync(0xffffffffu, L1, off);
       }
-      const long long slot_row = ((head_cut ? 0 : 1) * nsplit + c) * S::HQ;
+      const long long slot_row = ((head_cut ? 0 : 1) * splits() + c) * S::HQ;
       const int ha = 2 * qd, hb = 2 * qd + 1;  // heads of this lane's fragment columns
       // red buffer of this piece; the epilogue warp must be done with its use
       // two pieces ago
@@ -2173,7 +2367,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if constexpr (S::PF_PIECES > 0) {
             if (use_pf)
               merged = merge_sequence_bulk<S::HQ, S::PF_PIECES, NT>(
-                  p, b, cs0, cs1, nsplit, N, mw + S::PF_W, t, bar, c, own_o, own_lse,
+                  p, b, cs0, cs1, splits(), units(), mw + S::PF_W, t, bar, c, own_o, own_lse,
                   red + ((npieces & 1) ^ 1) * S::RED_ONE_FLOATS,
                   (long long)S::RED_ONE_FLOATS * 4, smem_addr(&ctl->pf_bar), abort_flag, true);
           }
@@ -2181,12 +2375,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           constexpr int MAXP = NT == S::CW * 32 ? S::MERGE_MAX_PIECES : S::DEF_W / S::HQ - 1;
           if (!merged && !use_pf)
             merged = merge_sequence_bulk<S::HQ, MAXP, NT>(
-                p, b, cs0, cs1, nsplit, N, mw, t, bar, c, own_o, own_lse, mbuf, mbuf_bytes,
+                p, b, cs0, cs1, splits(), units(), mw, t, bar, c, own_o, own_lse, mbuf, mbuf_bytes,
                 smem_addr(&ctl->merge_bar), abort_flag);
           if (!merged)
             for (int h = t >> 5; h < S::HQ; h += NT / 32)
               merge_row(p.part_o, p.part_lse, p.out, p.out_f32, (long long)b * S::HQ + h, S::HQ, h,
-                        cs0, cs1, nsplit, N, lane);
+                        cs0, cs1, splits(), units(), lane);
           if (t == 0) p.counters[cs1] = 0;
         };
         // the owed merge: every piece from the workspace, rows into the ring
@@ -2198,11 +2392,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           float *dbuf = own_o + buf_begin;
           const long long dbuf_bytes = ((long long)S::NST * S::STAGE_BYTES / 4 - buf_begin) * 4;
           if (!merge_sequence_bulk<S::HQ, S::DEF_MAX_PIECES, NT>(
-                  p, db, d0, d1, nsplit, N, mw + S::DEF_W, t, bar, -1, nullptr, nullptr, dbuf,
+                  p, db, d0, d1, splits(), units(), mw + S::DEF_W, t, bar, -1, nullptr, nullptr, dbuf,
                   dbuf_bytes, smem_addr(&ctl->merge_bar2), abort_flag))
             for (int h = t >> 5; h < S::HQ; h += NT / 32)
               merge_row(p.part_o, p.part_lse, p.out, p.out_f32, (long long)db * S::HQ + h, S::HQ,
-                        h, d0, d1, nsplit, N, lane);
+                        h, d0, d1, splits(), units(), lane);
           if (t == 0) p.counters[d1] = 0;
         };
         constexpr int RING_FLOATS = S::NST * S::STAGE_BYTES / 4;
@@ -2257,12 +2451,12 @@ consumers_done:
       const int db = ctl->def_b;
       const long long d0 = ctl->def_cs0, d1 = ctl->def_cs1;
       if (!merge_sequence_bulk<S::HQ, S::MERGE_MAX_PIECES, S::CW * 32>(
-              p, db, d0, d1, nsplit, N, mw, ct, 1, -1, nullptr, nullptr,
+              p, db, d0, d1, splits(), units(), mw, ct, 1, -1, nullptr, nullptr,
               reinterpret_cast<float *>(smem), (long long)S::NST * S::STAGE_BYTES,
               smem_addr(&ctl->merge_bar2), abort_flag))
         for (int h = cw; h < S::HQ; h += S::CW)
           merge_row(p.part_o, p.part_lse, p.out, p.out_f32, (long long)db * S::HQ + h, S::HQ, h,
-                    d0, d1, nsplit, N, lane);
+                    d0, d1, splits(), units(), lane);
       if (ct == 0) p.counters[d1] = 0;
     }
   }

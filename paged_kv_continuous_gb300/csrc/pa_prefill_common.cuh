@@ -11,15 +11,6 @@ namespace pa {
 constexpr int kPfRows = 128;  // M: rows of a query tile
 constexpr int kPfKeys = 64;   // keys per KV tile (N of the score MMA)
 
-// mbar_wait where the phase is most likely over, or soon to be: the first try,
-// which the hardware suspends for a while, stands alone in the instruction
-// stream and the rest out of its way.
-__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, volatile int *abort,
-                                               int32_t *err) {
-  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
-  return mbar_wait(bar, parity, abort, err);
-}
-
 // ---- tcgen05 helpers ----------------------------------------------------------
 
 // Shared-memory matrix descriptor (K- or MN-major, 128-byte swizzle):

@@ -33,8 +33,8 @@
 // tensor pipe.
 //
 // What bounds it (two chunks of 2 k queries behind 15 k keys, Hq 32, Hkv 8:
-// 851 us, 1.14 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
-// 1700 cycles, of which the tensor pipe is busy about 1280 (the score MMAs at N
+// 818 us, 1.19 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
+// 1630 cycles, of which the tensor pipe is busy about 1280 (the score MMAs at N
 // = 64 read their A and B tiles from shared memory at 48 cycles each, against
 // 32 of arithmetic), and the latency of the single warps' instruction streams
 // sets the rest; the last of four waves of CTAs is a sixth full.  Tried: two
@@ -425,8 +425,9 @@ __device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, in
 // with mt, so the tiles of a sequence that are at least v long are a closed
 // form; every warp finds the length of rank r by bisection over such counts and
 // the item by one scan, a sequence per lane (kSeqsPerLane of them at most), with
-// no barrier.  (A histogram over all items took 8 to 16 thousand cycles, a
-// tenth of a CTA's life; this takes about 2 thousand.)
+// no barrier.  (With a histogram over all items in shared memory, 8 to 16
+// thousand cycles a CTA, and registers spilled: sixteen mixed chunks 56.3 us
+// against 54.9, two long ones 852 against 818.)
 constexpr int kSeqsPerLane = 8;
 struct WorkItem {
   int s, mt, g;  // s < 0: none

@@ -337,6 +337,36 @@ def test_decode_many_sequences(ops):
 
 
 @pytest.mark.parametrize("Hkv", [1, 2, 4, 8])
+@pytest.mark.parametrize("order", ["short first", "long first", "mixed", "none between"])
+def test_decode_short_sequences_beside_long(ops, order, Hkv):
+    """Runs of short sequences beside long ones, whose piece ends weigh in the
+    division of the work: bounds that fall between, at the start and at the end
+    of sequences, empty sequences among them."""
+    rng = np.random.default_rng(900 + Hkv)
+    short, long = rng.integers(1, 40, 70), rng.integers(900, 2500, 5)
+    ctx = {"short first": np.concatenate([short, long]),
+           "long first": np.concatenate([long, short]),
+           "mixed": rng.permutation(np.concatenate([short, long])),
+           "none between": np.concatenate([[0, 0], short * (rng.random(70) < 0.6), long, [0],
+                                           short[:9], [0]])}[order].astype(np.int32)
+    tables = random_tables(rng, np.maximum(ctx, 1), 1200)
+    Hq = 3 * Hkv
+    check_decode(ops, normal_bits(rng, (len(ctx), Hq, 128)), ref.random_cache(rng, 1200, Hkv),
+                 tables, ctx, SCALE)
+
+
+@pytest.mark.parametrize("batch", [151, 152, 153, 160, 352, 353, 700])
+def test_decode_one_block_sequences(ops, batch):
+    """As many sequences as splits and a few more, and as many as a block has
+    threads and one more; one or two blocks each."""
+    rng = np.random.default_rng(950 + batch)
+    ctx = rng.integers(1, 18, batch).astype(np.int32)
+    tables = random_tables(rng, ctx, 1500)
+    check_decode(ops, normal_bits(rng, (batch, 4, 128)), ref.random_cache(rng, 1500, 2), tables,
+                 ctx, SCALE)
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 4, 8])
 def test_decode_default_splits_over_batches(ops, Hkv):
     """The splits in use with the default count, from one block to thousands,
     alone and beside others."""
