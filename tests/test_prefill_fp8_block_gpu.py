@@ -174,6 +174,16 @@ def test_many_sequences(ops):
     check(ops, *case(rng, spec, 6, 1, extra_blocks=320))
 
 
+@pytest.mark.parametrize("seqs", [31, 32, 33, 65, 255, 256, 257])
+def test_work_order_at_any_count(ops, seqs):
+    """Every row once, whatever the number of sequences a lane holds: ragged
+    chunks of up to four tiles, empty ones and single rows among them."""
+    rng = np.random.default_rng(600 + seqs)
+    spec = [(int(rng.choice([0, 1, 1, rng.integers(2, 70)])), int(rng.integers(0, 90)))
+            for _ in range(seqs)]
+    check(ops, *case(rng, spec, 7, 1, extra_blocks=seqs + 40))
+
+
 def test_decode_is_a_chunk_of_one(ops):
     """Single-token chunks against pa_decode_fp8_block, both within the bound
     of the same reference."""
