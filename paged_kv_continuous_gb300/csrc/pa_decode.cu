@@ -100,7 +100,10 @@ __device__ __forceinline__ MergePart merge_part(const float *part_o, const float
 // The block counts and the partition come from context_lens alone, before
 // the wait for the kernel before it (the decode kernel, under a
 // programmatic dependent launch); the partials after it.  The next kernel in
-// the stream may begin at once: its own wait covers this one.
+// the stream may begin at once: its own wait covers this grid, and so the
+// decode kernel too, since every CTA here waits for that one before it leaves,
+// those with nothing to merge included (a grid none of whose CTAs waits could
+// be over while the decode still reads its pages).
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergeParams p) {
   griddep_launch_dependents();
   __shared__ long long red[2][kMergeWarps];
@@ -133,10 +136,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const MergePara
   }
   const long long S = splits_in_use(p.num_splits, N, p.batch, p.split_rule);
   const int n = seq_blocks(p.context_lens, b);
-  if (n == 0) return;
-  const long long c0 = split_of_block(P, S, N), c1 = split_of_block(P + n - 1, S, N);
-  if (c0 == c1) return;  // held by one split: its rows are written already
+  const long long c0 = n > 0 ? split_of_block(P, S, N) : 0;
+  const long long c1 = n > 0 ? split_of_block(P + n - 1, S, N) : 0;
   griddep_wait();
+  if (c0 == c1) return;  // empty, or held by one split: its rows are written already
   const long long q = (c1 - c0 + kMergeWarps) / kMergeWarps;  // splits per warp
   const long long ca = c0 + warp * q, cb = min(c1, ca + q - 1);
   const MergePart r = merge_part(p.part_o, p.part_lse, p.num_q_heads, h, c0, ca, cb, S, N, lane);
