@@ -6,9 +6,19 @@ element strides and the current CUDA stream to the C entry point of the same
 name.  All arithmetic runs in the library's sm_103a kernels; there is no
 fallback path.  Importing this module loads the library and raises if it has
 not been built (``python -m paged_kv_continuous_gb300.build``).
+
+A call is enqueued on ``stream`` (default: the current stream), and an output
+or workspace that it allocates because none was given belongs to that stream,
+as if made under ``torch.cuda.stream(stream)``: use it on another stream as
+torch asks for (an event, ``record_stream``).  The prepared calls (``*Call``)
+allocate on the stream that is current when they are made; the first call on
+another stream makes that one wait for it, which a call under capture cannot:
+make the call object before the capture, capture behind a synchronize (as
+``torch.cuda.graph`` does), and keep the object as long as the graph.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -137,6 +147,37 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """Where a call on ``stream`` allocates its default buffers: on that stream,
+    so that filling, use and reuse of their memory follow one another."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+class _Defaults:
+    """The buffers that a prepared call made for itself, on the stream that was
+    current then.  Another stream that it is called on waits for that one
+    (which may still fill them, or run what had their memory before), once, and
+    the allocator is told of the stream."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        self.home = torch.cuda.current_stream(self.tensors[0].device)
+        self.known = {self.home.cuda_stream}
+
+    def share(self, stream):
+        for t in self.tensors:
+            t.record_stream(stream)
+        if _capturing(stream) or _capturing(self.home):
+            return  # the wait would become part of the capture, or break it
+        stream.wait_stream(self.home)
+        self.known.add(stream.cuda_stream)
+
+
+def _capturing(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _need(t, dtype, name, dims=None):
     if not t.is_cuda:
         raise PagedAttentionError(f"{name} must be a CUDA tensor")
@@ -212,7 +253,8 @@ def rope_store_kv(q, k, v, positions, cos_table, sin_table, k_cache, v_cache, sl
     if positions.shape[0] != T or slot_mapping.shape[0] != T:
         raise PagedAttentionError("positions and slot_mapping need one entry per token")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        with _on(stream):
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     _need(q_out, torch.bfloat16, "q_out", 3)
     if q_out.shape != q.shape or q_out.stride(2) != 1 or q_out.stride(1) != D:
         raise PagedAttentionError("q_out must be [T, Hq, D] with contiguous heads")
@@ -278,10 +320,11 @@ def decode(q, k_cache, v_cache, block_tables, context_lens, scale, out=None,
         raise PagedAttentionError("block_tables rows must be contiguous")
     B, Hq, D = q.shape
     NB, bs, Hkv, _ = k_cache.shape
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
-    if workspace is None:
-        workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        if workspace is None:
+            workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_decode(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(k_cache),
                          _ptr(v_cache), NB, _ptr(block_tables), block_tables.stride(0),
                          _ptr(context_lens), B, Hq, Hkv, D, bs, float(scale), int(num_splits),
@@ -316,10 +359,11 @@ def store_decode(q, new_k, new_v, k_cache, v_cache, slot_mapping, block_tables, 
     if tuple(new_k.shape) != (B, Hkv, D) or new_v.shape != new_k.shape or \
             slot_mapping.shape[0] != B:
         raise PagedAttentionError("new_k / new_v / slot_mapping need one row per sequence")
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
-    if workspace is None:
-        workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        if workspace is None:
+            workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_store_decode(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
                                _ptr(new_v), new_k.stride(0), new_v.stride(0), _ptr(slot_mapping),
                                _ptr(k_cache), _ptr(v_cache), NB, _ptr(block_tables),
@@ -363,8 +407,10 @@ class StoreDecodeCall:
             raise PagedAttentionError("new_k / new_v / slot_mapping need one row per sequence")
         if out.shape != (B, Hq, D) or not out.is_contiguous():
             raise PagedAttentionError("out must be a contiguous [B, Hq, D] tensor")
+        self._defaults = None
         if workspace is None:
             workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+            self._defaults = _Defaults([workspace])
         self._keep = (q, new_k, new_v, k_cache, v_cache, slot_mapping, block_tables,
                       context_lens, out, workspace)
         c = ctypes
@@ -383,6 +429,10 @@ class StoreDecodeCall:
         self.workspace = workspace
 
     def __call__(self, stream=None):
+        if self._defaults is not None:
+            s = torch.cuda.current_stream(self.workspace.device) if stream is None else stream
+            if s.cuda_stream not in self._defaults.known:
+                self._defaults.share(s)
         st = lib.pa_store_decode(*self._args, _stream(stream))
         if st != PA_OK:
             _check(st, "pa_store_decode")
@@ -462,10 +512,11 @@ def rope_store_decode(q, new_k, new_v, k_cache, v_cache, slot_mapping, block_tab
     if cos_table.shape != sin_table.shape or cos_table.shape[1] != D // 2 or \
             not cos_table.is_contiguous() or not sin_table.is_contiguous():
         raise PagedAttentionError("cos_table / sin_table must be contiguous [max_position, D/2]")
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
-    if workspace is None:
-        workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        if workspace is None:
+            workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_rope_store_decode(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
                                     _ptr(new_v), new_k.stride(0), new_v.stride(0),
                                     _ptr(positions), _ptr(cos_table), _ptr(sin_table),
@@ -538,10 +589,11 @@ def decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens
         raise PagedAttentionError("block_tables rows must be contiguous")
     NB, bs, Hkv, _ = _need_fp8_pools(k_cache, v_cache, k_scale, v_scale)
     B, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
-    if workspace is None:
-        workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        if workspace is None:
+            workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_decode_fp8(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(k_cache),
                              _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), NB,
                              _ptr(block_tables), block_tables.stride(0), _ptr(context_lens), B,
@@ -574,10 +626,11 @@ def store_decode_fp8(q, new_k, new_v, k_cache, v_cache, k_scale, v_scale, slot_m
     if tuple(new_k.shape) != (B, Hkv, D) or new_v.shape != new_k.shape or \
             slot_mapping.shape[0] != B:
         raise PagedAttentionError("new_k / new_v / slot_mapping need one row per sequence")
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
-    if workspace is None:
-        workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+        if workspace is None:
+            workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_store_decode_fp8(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
                                    _ptr(new_v), new_k.stride(0), new_v.stride(0),
                                    _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
@@ -603,7 +656,8 @@ class _Prepared:
     call is enqueued on ``stream`` (default: the current stream of the
     tensors' device, which also becomes the device of the launch)."""
 
-    def _prepare(self, fn, what, args, keep, result=None):
+    def _prepare(self, fn, what, args, keep, result=None, made=()):
+        """made: the tensors among ``keep`` that the call allocated itself."""
         self._fn, self._what, self._keep, self._result = fn, what, keep, result
         # (pinned host memory, which the device reaches, counts for none)
         devices = {t.device for t in keep if t is not None and t.is_cuda}
@@ -612,9 +666,13 @@ class _Prepared:
         self._device = devices.pop().index
         # marshalled once: a call converts nothing but the stream
         self._args = tuple(a if t is None else t(a) for a, t in zip(args, fn.argtypes))
+        self._defaults = _Defaults(made) if made else None
 
     def __call__(self, stream=None):
         handle = _raw_stream(self._device) if stream is None else stream.cuda_stream
+        if self._defaults is not None and handle not in self._defaults.known:
+            self._defaults.share(torch.cuda.current_stream(self._device) if stream is None
+                                 else stream)
         if _current_device() == self._device:
             status = self._fn(*self._args, handle)
         else:
@@ -739,8 +797,10 @@ class DecodeFp8BlockCall(_Prepared):
             raise PagedAttentionError("out must be a CUDA tensor or pinned host memory")
         if out.shape != q.shape or not out.is_contiguous():
             raise PagedAttentionError("out must be a contiguous [B, Hq, D] tensor")
+        made = ()
         if workspace is None:
             workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
+            made = (workspace,)
         _need_contiguous(workspace, workspace.dtype, "workspace")
         self.out, self.workspace = out, workspace
         self._prepare(
@@ -751,7 +811,7 @@ class DecodeFp8BlockCall(_Prepared):
              int(num_splits), _address(workspace), workspace.numel() * workspace.element_size(),
              _decode_flags(pdl, early_kv)),
             (q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace),
-            out)
+            out, made)
 
 
 def decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
@@ -759,10 +819,12 @@ def decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, contex
                      stream=None, pdl=False, early_kv=False):
     """pa_decode_fp8_block: q bf16 [B, Hq, D] over block-scaled FP8 pools
     (see fp8_block_pools); returns out [B, Hq, D]."""
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-    return DecodeFp8BlockCall(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-                              scale, out, num_splits, workspace, pdl, early_kv)(stream)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        return DecodeFp8BlockCall(q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                  context_lens, scale, out, num_splits, workspace, pdl,
+                                  early_kv)(stream)
 
 
 class PrefillFp8BlockCall(_Prepared):
@@ -802,7 +864,8 @@ def prefill_varlen_fp8_block(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, 
     [N + 1]) over block-scaled FP8 pools that hold the chunks' own keys too
     (store_kv_fp8_block first); returns out [T, Hq, D]."""
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     return PrefillFp8BlockCall(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tables,
                                context_lens, scale, max_q_len, out, error_flags)(stream)
 
@@ -893,13 +956,14 @@ class ForkPagesCall(_Prepared):
         self.copy_dst = _i32_out(copy_dst, n, "copy_dst", parents)
         self.forked = _i32_out(forked, n, "forked", parents)
         result = (self.copy_src, self.copy_dst, self.forked)
+        made = [t for t, given in zip(result, (copy_src, copy_dst, forked)) if given is None]
         self._prepare(
             lib.pa_fork_pages, "pa_fork_pages",
             (_address(block_tables), block_tables.stride(0), _address(context_lens), rows,
              _address(parents), _address(children), n, _address(ref_counts), NB, block_size,
              *map(_address, result), _address(error_flags), PA_LAUNCH_PDL if pdl else 0),
             (block_tables, context_lens, parents, children, ref_counts, *result, error_flags),
-            result)
+            result, made)
 
 
 def fork_pages(block_tables, context_lens, parents, children, ref_counts, copy_src=None,
@@ -908,8 +972,9 @@ def fork_pages(block_tables, context_lens, parents, children, ref_counts, copy_s
     parents[i] (int32 [n]) that shares its full pages; the part-filled last
     page gets a free page, to be filled by ``copy_pages(pools, copy_src,
     copy_dst)``.  Returns (copy_src, copy_dst, forked), int32 [n] each."""
-    return ForkPagesCall(block_tables, context_lens, parents, children, ref_counts, copy_src,
-                         copy_dst, forked, error_flags, pdl)(stream)
+    with _on(stream):
+        return ForkPagesCall(block_tables, context_lens, parents, children, ref_counts, copy_src,
+                             copy_dst, forked, error_flags, pdl)(stream)
 
 
 class FreePagesCall(_Prepared):
@@ -947,12 +1012,14 @@ class CompactPagesCall(_Prepared):
         self.counts = _i32_out(counts, 2, "counts", ref_counts)
         self.remap = _i32_out(remap, NB, "remap", ref_counts)
         result = (self.copy_src, self.copy_dst, self.counts, self.remap)
+        made = [t for t, given in zip(result, (copy_src, copy_dst, counts, remap))
+                if given is None]
         self._prepare(
             lib.pa_compact_pages, "pa_compact_pages",
             (_address(block_tables), block_tables.stride(0), _address(context_lens), rows,
              _address(ref_counts), NB, block_size, *map(_address, result),
              _address(error_flags), PA_LAUNCH_PDL if pdl else 0),
-            (block_tables, context_lens, ref_counts, *result, error_flags), result)
+            (block_tables, context_lens, ref_counts, *result, error_flags), result, made)
 
 
 def compact_pages(block_tables, context_lens, ref_counts, copy_src=None, copy_dst=None,
@@ -961,8 +1028,9 @@ def compact_pages(block_tables, context_lens, ref_counts, copy_src=None, copy_ds
     pool and bring tables and counts up to date; ``copy_pages(pools, copy_src,
     copy_dst, count=counts)`` then moves the contents.  Returns (copy_src,
     copy_dst [NB / 2], counts [moves, live pages], remap [NB]), int32."""
-    return CompactPagesCall(block_tables, context_lens, ref_counts, copy_src, copy_dst, counts,
-                            remap, error_flags, pdl)(stream)
+    with _on(stream):
+        return CompactPagesCall(block_tables, context_lens, ref_counts, copy_src, copy_dst,
+                                counts, remap, error_flags, pdl)(stream)
 
 
 def decode_merge(out, workspace, context_lens, num_splits, block_size=16, stream=None):
@@ -986,7 +1054,8 @@ def prefill_varlen(q, cu_seqlens, k_cache, v_cache, block_tables, context_lens, 
     T, Hq, D = q.shape
     NB, bs, Hkv, _ = k_cache.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        with _on(stream):
+            out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
     _check(lib.pa_prefill_varlen(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(cu_seqlens),
                                  cu_seqlens.shape[0] - 1, T, int(max_q_len), _ptr(k_cache),
                                  _ptr(v_cache), NB, _ptr(block_tables), block_tables.stride(0),
@@ -1017,7 +1086,8 @@ def prefill_store_varlen(q, new_k, new_v, slot_mapping, cu_seqlens, k_cache, v_c
             slot_mapping.shape[0] != T:
         raise PagedAttentionError("new_k / new_v / slot_mapping need one row per token")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        with _on(stream):
+            out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
     _check(lib.pa_prefill_store_varlen(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
                                        _ptr(new_v), new_k.stride(0), new_v.stride(0),
                                        _ptr(slot_mapping), _ptr(cu_seqlens),
