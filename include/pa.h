@@ -816,7 +816,7 @@ PA_API pa_status pa_prefill_store_varlen(void *out, int32_t out_dtype, const voi
  * and errors as pa_prefill_varlen, plus k_scale / v_scale (uint8
  * [num_blocks][num_kv_heads]).  Products run on the tensor cores with fp32
  * accumulation.  A query row times a power of two enters as the sum of two
- * E4M3 terms, exact for elements down to 2^-10 of the row's largest and within
+ * E4M3 terms, exact for elements down to 2^-9 of the row's largest and within
  * 2^-17 of that largest below; the codes are exact; the softmax weights are
  * rounded to f16 (11 bits) after taking in the V scale of their block.  A
  * query row with a NaN or an infinity gives NaN.  Rows past

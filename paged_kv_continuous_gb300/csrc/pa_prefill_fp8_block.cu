@@ -16,11 +16,11 @@
 // K codes feed the score MMA as they are: a query row times 2^-eq, its
 // largest magnitude in (224, 448], is the sum of two E4M3 terms.  A bf16 has 8
 // significant bits; the rounded first term leaves a remainder of at most 4
-// bits, which the second holds exactly wherever the element is at least
-// 2^-10 of the row's largest (below, the error is under 2^-17 of the largest).
-// Two
-// passes at the FP8 rate cost what one f16 pass would, and K needs no
-// conversion: its pages arrive by TMA in the layout the MMA reads.
+// bits, which the second holds exactly wherever the element is at least 2^-9
+// of the row's largest (the last inexact one is 0.249 where the largest is 226;
+// below, the error is under 2^-17 of the largest).  Two passes at the FP8 rate
+// cost what one f16 pass would, and K needs no conversion: its pages arrive by
+// TMA in the layout the MMA reads.
 //
 // V codes are widened to f16 by one warp, from a staging buffer that bulk
 // copies fill (a page of a head is 2 KB contiguous).  V pages are dim-major,
