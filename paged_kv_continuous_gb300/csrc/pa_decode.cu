@@ -70,7 +70,8 @@ __device__ __forceinline__ MergePart merge_part(const float *part_o, const float
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, off));
     const float Mn = fmaxf(r.M, mc);
-    if (Mn == -INFINITY) continue;  // no piece with a key so far
+    // no piece with a key so far (a NaN lse has some, and makes the sums NaN)
+    if (Mn == -INFINITY && !__any_sync(0xffffffffu, ls != ls)) continue;
     const float sc = __expf(r.M - Mn);  // 0 for the first chunk (M = -inf)
     r.W *= sc;
     r.acc.x *= sc;

@@ -653,6 +653,13 @@ __device__ __forceinline__ void store_out4(void *out, int out_f32, long long idx
   }
 }
 
+// Natural-log sum-exp of a piece from its reference m and sum l (base 2): -inf
+// without a key.  A NaN sum (a NaN score) stays NaN, so that the merges give
+// NaN; -inf would leave the piece out.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
 // Log-sum-exp merge of one output row (sequence b, query head h) from the
 // split-K partials of splits c0..c1 (slot 1 of c0, slot 0 of the others;
 // partials are [slot][split][head][dim]),
@@ -1562,8 +1569,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
           for (int w = 0; w < S::NPH; ++w) eww[w * S::HQ + qh] = mk[w] * inv;
           if (d.kind == kPieceCut)
-            p.part_lse[d.slot_row + qh] =
-                L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+            p.part_lse[d.slot_row + qh] = lse_of(M, L);
         }
         __syncwarp();
         for (int item = lane; item < S::HQ * (kHeadDim / 4); item += 32) {
@@ -2193,8 +2199,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
         }
         if (!whole && gid == 0) {
-          const float lse_a = L0 > 0.f ? (m0 + __log2f(L0)) * 0.69314718055994531f : -INFINITY;
-          const float lse_b = L1 > 0.f ? (m1 + __log2f(L1)) * 0.69314718055994531f : -INFINITY;
+          const float lse_a = lse_of(m0, L0), lse_b = lse_of(m1, L1);
           if (ha < G) {
             p.part_lse[slot_row + g * G + ha] = lse_a;
             if (keep_own) own_lse[g * G + ha] = lse_a;
@@ -2258,7 +2263,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
             for (int k = 0; k < S::NPH; ++k) cwt[k * S::HQ + qh] = mk[k] * inv;
             if (!whole) {
-              const float lse = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+              const float lse = lse_of(M, L);
               p.part_lse[slot_row + qh] = lse;
               if (keep_own) own_lse[qh] = lse;
             }
