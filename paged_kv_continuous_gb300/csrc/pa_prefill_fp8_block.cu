@@ -45,9 +45,16 @@
 // the PV warp, 931 us; P' in a rolled loop that reads the scores twice, 1055 us;
 // the widening's loads a page ahead, 927 us.
 //
-// A NaN code of a value reaches every row of the tiles that meet it, those that
-// do not attend to that key included (0 * NaN in the MMA); a query row with a
-// NaN or an infinity gives NaN.
+// A NaN code of a value may only reach the rows that see its key, but in the MMA
+// 0 * NaN is NaN.  So the widening warp looks through the few tiles that the
+// causal limit cuts (two of 270 in a long chunk), turns NaN codes past the query
+// tile's first position into zeros and keeps the first such key of each dim; the
+// rows that see it write NaN there at the end.  The rest of that is out of line:
+// inlined, it moved registers of the tile loops, 2 % (and 14 % for a search by the
+// softmax threads before they start).  As it is, the long case takes 824 us
+// against 812 without, the mixed one 54.5 against 54.9.  A query row with a NaN or
+// an infinity gives NaN.
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -78,15 +85,17 @@ constexpr int kQpOffBar = kQpOffV + kQpVStages * kQpTile;
 // 8-byte slots: K full / empty per stage, V codes full / empty, widened V full
 // / empty, Q ready, two score, two P and two PV barriers, eight scale
 // barriers, TMEM address, abort flag; then the page scales of eight tiles (K's
-// four bytes, V's four)
+// four bytes, V's four).  From kQpOffNan on the first NaN key of each dim, and in
+// the word before whether there is one.
 constexpr int kSlKFull = 0, kSlKEmpty = kSlKFull + kQpKStages;
 constexpr int kSlCFull = kSlKEmpty + kQpKStages, kSlCEmpty = kSlCFull + kQpCStages;
 constexpr int kSlVFull = kSlCEmpty + kQpCStages, kSlVEmpty = kSlVFull + 2;
 constexpr int kSlQ = kSlVEmpty + 2, kSlS = kSlQ + 1, kSlP = kSlS + 2, kSlO = kSlP + 2;
 constexpr int kSlScale = kSlO + 2, kSlTmem = kSlScale + 8, kSlAbort = kSlTmem + 1;
 constexpr int kSlScales = kSlAbort + 1;
-constexpr int kQpBarBytes = 512;
-static_assert((kSlScales + 8) * 8 <= kQpBarBytes, "barrier slots do not fit");
+constexpr int kQpOffNan = kQpOffBar + 512;
+constexpr int kQpBarBytes = 512 + 4 * kHeadDim;
+static_assert((kSlScales + 8) * 8 + 4 <= 512, "barrier slots do not fit");
 constexpr int kQpSmem = 1024 + kQpOffBar + kQpBarBytes;
 // TMEM (256 columns, two CTAs per SM): scores of tile j in buffer j % 2 at 0
 // and 64, P' over the scores it came from (32 columns, two keys each), O at 128
@@ -259,6 +268,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                "r"(d)
                : "memory");
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
@@ -356,8 +373,38 @@ __device__ __forceinline__ void request_tiles(const PrefillQParams &p, const CUt
   __syncwarp();
 }
 
+// High bit of each byte that is a NaN code (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_codes4(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// A staged V tile (its first key is key0) holds NaN codes: those past `seen`, the
+// last key of the query tile's first row, become zeros, word `dim` at nan0 keeps
+// the first of them, and the word before tells that there is one.
+__device__ __noinline__ void take_nan_codes(uint32_t codes, uint32_t nan0, int key0, int seen) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) sts32(nan0 - 4, 1u);
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {  // page c / 4, dims 32 (c % 4) + lane
+    const int first = key0 + (c >> 2) * kBlockSize, past = seen + 1 - first;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {  // tokens 4 i .. 4 i + 3
+      const int b = min(max(past - 4 * i, 0), 4);
+      const uint32_t at = codes + c * 512 + 16 * lane + 4 * i;
+      const uint32_t x = lds32(at);
+      const uint32_t m = b >= 4 ? 0u : nan_codes4(x) & (0xFFFFFFFFu << (8 * b));
+      if (!m) continue;
+      sts32(at, x & ~((m >> 7) * 0xFFu));
+      const int key = first + 4 * i + ((__ffs((int)m) - 1) >> 3);
+      const uint32_t d = nan0 + 4 * (32 * (c & 3) + lane);
+      if (key < (int)lds32(d)) sts32(d, (uint32_t)key);
+    }
+  }
+  __syncwarp();
+}
+
 // Warp 2: the V codes of each tile to f16.
-__device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, int nkv,
+__device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, int nkv, int seen,
                                               uint32_t base, uint32_t slot0,
                                               volatile int *abort_flag) {
   const int lane = threadIdx.x & 31;
@@ -369,6 +416,16 @@ __device__ __forceinline__ void widen_v_tiles(const PrefillQParams &p, int n, in
     if (ok && j >= 2)
       ok = mbar_wait_soon(slot(kSlVEmpty + st), ((j >> 1) - 1) & 1, abort_flag, p.err);
     if (!__all_sync(0xffffffffu, ok)) return;
+    if ((j + 1) * kPfKeys - 1 > seen) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint4 w = lds128(base + kQpOffC + cs * kQpCodes + 16 * lane + c * 512);
+        any |= nan_codes4(w.x) | nan_codes4(w.y) | nan_codes4(w.z) | nan_codes4(w.w);
+      }
+      if (__any_sync(0xffffffffu, any != 0))
+        take_nan_codes(base + kQpOffC + cs * kQpCodes, base + kQpOffNan, j * kPfKeys, seen);
+    }
     const uint32_t from = base + kQpOffC + cs * kQpCodes + 16 * lane;
     const uint32_t to = base + kQpOffV + st * kQpTile + lane * 128;
     // chunk q of a page: dims 32 q .. + 31, one per lane, 16 tokens
@@ -514,6 +571,20 @@ __device__ __forceinline__ WorkItem pick_item(const PrefillQParams &p, int gx, i
   return item;
 }
 
+// Dims of which the row of last key `limit` sees a NaN code that was taken out of
+// its tile; `at` is the row's first output element.
+__device__ __noinline__ void write_nan_dims(const PrefillQParams &p, uint32_t nan0, int limit,
+                                            long long at) {
+#pragma unroll 1
+  for (int d = 0; d < kHeadDim; ++d) {
+    if ((int)lds32(nan0 + 4 * d) > limit) continue;
+    if (p.out_f32)
+      static_cast<uint32_t *>(p.out)[at + d] = 0x7FC00000u;
+    else
+      static_cast<uint16_t *>(p.out)[at + d] = 0x7FC0u;
+  }
+}
+
 template <int G>
 __global__ void __launch_bounds__(kQpThreads, 2)
     prefill_fp8_block_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -598,8 +669,10 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     mbar_init(slot(kSlQ), kQpSoft);
     for (int i = 0; i < 8; ++i) mbar_init(slot(kSlScale + i), 1);
     *abort_flag = 0;
+    sts32(base + kQpOffNan - 4, 0u);
     fence_barrier_init();
   }
+  if (tid < kHeadDim) sts32(base + kQpOffNan + 4 * tid, (uint32_t)INT_MAX);
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
@@ -617,7 +690,7 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   if (warp == 0) {
     request_tiles(p, &tmap_k, row, n, nkv, g, base, slot0, abort_flag);
   } else if (warp == 2) {
-    widen_v_tiles(p, n, nkv, base, slot0, abort_flag);
+    widen_v_tiles(p, n, nkv, prefix + pos0, base, slot0, abort_flag);
   } else if (warp == 1 || warp == 3) {
     // ---- MMA issuers, each a whole converged warp: 1 issues S_j = Q K_j^T
     //      into buffer j & 1 once the PV of tile j - 2, which read that
@@ -847,6 +920,12 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     tc_fence_before();
   }
   __syncthreads();
+  if (warp >= 4 && lds32(base + kQpOffNan - 4)) {
+    const int r = 32 * (warp & 3) + lane;
+    if (r < rows)
+      write_nan_dims(p, base + kQpOffNan, prefix + pos0 + r / G,
+                     ((long long)(q0 + pos0 + r / G) * p.hq + g * G + r % G) * kHeadDim);
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
