@@ -567,8 +567,10 @@ PA_API pa_status pa_store_kv_fp8_block(
 /*
  * pa_decode_fp8_block -- pa_decode over a block-scaled FP8 cache: the
  * attention over the values code * 2^(scale byte - 127).  Products run on the
- * tensor cores in f16 as in pa_decode_fp8 (codes exact, q rounded to f16);
- * the softmax weights are rounded to f16 (11 bits) after taking in the V
+ * tensor cores in f16 (codes exact); a query row enters times a power of two,
+ * exact for elements down to 2^-31 of the row's largest and within 2^-39 of
+ * that largest below, whatever its size (scores have to stay within fp32), and
+ * a row with a NaN or an infinity gives NaN; the softmax weights are rounded to f16 (11 bits) after taking in the V
  * scale of their block, the scores, sums and outputs stay fp32.  Same
  * workspace, flags and outputs as pa_decode, and the same splits for
  * num_splits > 0; with num_splits = 0 the kernel uses as many of the

@@ -70,7 +70,11 @@
 //   P' = 2^(t - m),  O += P' code_v,  l += 2^-ev P',  out = O / l,
 // so the f16 weights carry the V scale relative to the largest weight times
 // scale and stay <= 256, the sum stays the plain softmax sum, and the lse
-// m + log2 l is that of the scores.
+// m + log2 l is that of the scores.  A query row enters as f16 times a power of
+// two of its own, which joins the score scale: its largest magnitude in [2^14,
+// 2^15) keeps a bf16 element exact down to 2^-31 of it (an error of at most
+// 2^-39 of it below), whatever the row's size; a row with a NaN or an infinity
+// is NaN.
 // Early K/V requests (p.early_kv, a
 // launch flag): the producers issue the first ring stages' pages before the
 // wait for the previous kernel.
@@ -1652,7 +1656,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // into the rows at each piece end (codes widen exactly, so the products
   // equal those of the widened values)
   // (F8: the scales are read after the wait, below)
-  float cl2 = p.qk_scale_log2;
+  // (BS: the scale of head 2 qd, with its query row's power of two; cl2b: 2 qd + 1)
+  float cl2 = p.qk_scale_log2, cl2b = 0.f;
   float vsc = 1.f;
   // F8: the 16 score rows of an MMA are the tokens tperm(r), so that a
   // thread's two token pairs of the PV operand are 4 consecutive bytes of
@@ -1775,11 +1780,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                   // fragments use: columns 2qd, 2qd + 1 = dims dk, dk + 1,
                   // columns 2qd + 8, 2qd + 9 = dims dk + 2, dk + 3
                   const int dk = 16 * f8_k_chunk<S::HB>(qd, ks >> 2) + 4 * (ks & 3);
-                  const uint32_t w0 = lds32(qrow + dk * 2);
-                  const uint32_t w1 = lds32(qrow + (dk + 2) * 2);
-                  const float2 f0 = bf16x2_to_float2(w0), f1 = bf16x2_to_float2(w1);
-                  x0 = float2_to_f16x2(f0.x, f0.y);
-                  x1 = float2_to_f16x2(f1.x, f1.y);
+                  x0 = lds32(qrow + dk * 2);
+                  x1 = lds32(qrow + (dk + 2) * 2);
+                  if constexpr (!BS) {
+                    const float2 f0 = bf16x2_to_float2(x0), f1 = bf16x2_to_float2(x1);
+                    x0 = float2_to_f16x2(f0.x, f0.y);
+                    x1 = float2_to_f16x2(f1.x, f1.y);
+                  }
                 } else {
                   x0 = lds32(qrow + (16 * ks + 2 * qd) * 2);
                   x1 = lds32(qrow + (16 * ks + 8 + 2 * qd) * 2);
@@ -1787,6 +1794,30 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
               }
               qf[ks][0] = x0;
               qf[ks][1] = x1;
+            }
+            if constexpr (BS) {
+              // the row's power of two (its dims lie in the four lanes of gid)
+              uint32_t top = 0;  // magnitudes of bf16 order like their bits
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) top = __vmaxu2(top, qf[ks][h] & 0x7FFF7FFFu);
+              top = max(top >> 16, top & 0xFFFFu);
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              const int eq = min(max((int)(top >> 7) - (kScaleBias + 14), -112), 113);
+              const float inv = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                                               : inv_scale_of(eq + kScaleBias);
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float2 f = bf16x2_to_float2(qf[ks][h]);
+                  qf[ks][h] = float2_to_f16x2(f.x * inv, f.y * inv);
+                }
+              cl2 = p.qk_scale_log2 * scale_of(__shfl_sync(0xffffffffu, eq, 8 * qd) + kScaleBias);
+              cl2b =
+                  p.qk_scale_log2 * scale_of(__shfl_sync(0xffffffffu, eq, 8 * qd + 4) + kScaleBias);
             }
             if constexpr (ROPE) {
               // rotate-half: dims d < 64 (k-steps 0..3) pair with d + 64
@@ -2006,12 +2037,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if constexpr (BS) {
             const int bk = (int)lds8(scale0 + 16 * sidx + g);
             const int bv = (int)lds8(scale0 + 16 * sidx + 8 + g);
-            const float ck = cl2 * scale_of(bk), ev = (float)(bv - kScaleBias);
+            const float ev = (float)(bv - kScaleBias);
+            const float ck = cl2 * scale_of(bk), ckb = cl2b * scale_of(bk);
             inv_v = inv_scale_of(bv);
             s0 = v0 ? fmaf(sa[0] + sb[0], ck, ev) : -INFINITY;
-            s1 = v0 ? fmaf(sa[1] + sb[1], ck, ev) : -INFINITY;
+            s1 = v0 ? fmaf(sa[1] + sb[1], ckb, ev) : -INFINITY;
             s2 = v1 ? fmaf(sa[2] + sb[2], ck, ev) : -INFINITY;
-            s3 = v1 ? fmaf(sa[3] + sb[3], ck, ev) : -INFINITY;
+            s3 = v1 ? fmaf(sa[3] + sb[3], ckb, ev) : -INFINITY;
           } else {
             s0 = v0 ? (sa[0] + sb[0]) * cl2 : -INFINITY;
             s1 = v0 ? (sa[1] + sb[1]) * cl2 : -INFINITY;

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from paged_kv_continuous_gb300.synth import bf16_bits, bf16_to_f64
 from tests import fp8_block_reference as ref
 from tests.helpers import normal_bits, random_tables, to_dev_bf16, to_dev_i32
 
@@ -107,3 +108,76 @@ def test_prefill_nan_codes_reach_the_rows_that_see_them(ops, Hq, Hkv):
             got = prefill(ops, q, cu, cache, tables, ctx)
             check(got, want, mag, tiny)
             assert np.array_equal(got[~np.isnan(got)], good[~np.isnan(got)])
+
+
+def test_decode_query_rows_of_any_size(ops):
+    """Rows whose magnitudes lie far apart and far from 1 (each takes its own
+    power of two), elements of one row far apart.  An element of less than
+    2^-31 of its row's largest may be off by 2^-39 of that, which moves a score
+    by at most that times the sum of the key's magnitudes."""
+    rng = np.random.default_rng(10)
+    B, Hq, Hkv = 20, 8, 2
+    ctx = rng.integers(1, 90, B).astype(np.int32)
+    NB = int(((ctx + 15) // 16).sum()) + 2
+    tables = random_tables(rng, ctx, NB)
+    cache = ref.random_cache(rng, NB, Hkv)
+    kk = np.abs(ref.widen(*cache)[0]).sum(-1).max()
+    f = bf16_to_f64(normal_bits(rng, (B, Hq, 128)))
+    rows = 2.0 ** rng.integers(-60, 60, (B, Hq, 1))
+    for spread in (0, 40):
+        x = f * 2.0 ** rng.integers(-spread, 1, f.shape)
+        for scale, y in ((SCALE, x), (SCALE * 2.0 ** -60, x * 2.0 ** 60),
+                         (SCALE * 2.0 ** 60, x * 2.0 ** -60), (SCALE * 2.0 ** -17, x * 2.0 ** 17),
+                         (SCALE * 2.0 ** 26, x * 2.0 ** -26), (2.0 ** -40, x * rows)):
+            bits = bf16_bits(y.astype(np.float32))
+            want, mag, tiny = ref.attention(bits, *cache, tables, ctx, scale)
+            top = np.abs(bf16_to_f64(bits)).max(-1, keepdims=True)
+            # only rows whose scores stay where a rounding of fp32 is small
+            fine = (scale * top * kk < 2000).squeeze(-1)
+            move = scale * top * 2.0 ** -39 * kk
+            got = decode(ops, bits, cache, tables, ctx, scale)
+            bound = ref.tolerance(want, mag, tiny, score=3000.0) + \
+                2 * np.expm1(np.minimum(move, 1.0)) * mag
+            assert fine.any() and np.all(np.abs(got - want)[fine] <= bound[fine]), scale
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (12, 2), (32, 8)])
+def test_decode_query_rows_at_the_ends_of_bf16(ops, Hq, Hkv):
+    """The largest and the smallest (subnormal) magnitudes, and rows of zeros."""
+    rng = np.random.default_rng(Hq)
+    ctx = np.array([40, 200, 17], np.int32)
+    tables = random_tables(rng, ctx, 30)
+    cache = ref.random_cache(rng, 30, Hkv)
+    f = bf16_to_f64(normal_bits(rng, (3, Hq, 128)))
+    q = bf16_bits((f * 2.0 ** 120).astype(np.float32))
+    q[:, 3, 5] = 0xFF7F  # the largest finite one, negative
+    q[:, 1] = bf16_bits((f[:, 1] * 2.0 ** -130).astype(np.float32))
+    q[:, 2] = 0
+    scale = SCALE * 2.0 ** -120
+    want = ref.attention(q, *cache, tables, ctx, scale)
+    check(decode(ops, q, cache, tables, ctx, scale), *want, score=512.0)
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 4, 8])
+@pytest.mark.parametrize("lens", [[1, 40], [128], [3000, 5]])
+def test_decode_query_rows_that_are_not_finite(ops, Hkv, lens):
+    """A NaN or an infinity in a query row makes that row NaN and no other,
+    as in the prefill."""
+    rng = np.random.default_rng(11)
+    ctx = np.array(lens, np.int32)
+    NB = int(((ctx + 15) // 16).sum()) + 2
+    tables = random_tables(rng, ctx, NB)
+    cache = ref.random_cache(rng, NB, Hkv)
+    Hq = 4 * Hkv
+    q = normal_bits(rng, (len(lens), Hq, 128))
+    good = decode(ops, q, cache, tables, ctx)
+    bad = np.zeros((len(lens), Hq), bool)
+    for h, d, x in ((0, 7, 0x7FC0), (2, 0, 0x7F80), (Hq - 1, 127, 0xFF80)):
+        q[0, h, d] = x
+        bad[0, h] = True
+    got = decode(ops, q, cache, tables, ctx)
+    assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], good[~bad])
+    out = ops.prefill_varlen_fp8_block(
+        to_dev_bf16(q), to_dev_i32(np.arange(len(lens) + 1)), *[dev(a) for a in cache],
+        to_dev_i32(tables), to_dev_i32(ctx), SCALE, 1, out_dtype=torch.float32)
+    assert np.array_equal(np.isnan(out.cpu().numpy()), np.isnan(got))
