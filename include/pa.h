@@ -578,8 +578,10 @@ PA_API pa_status pa_store_kv_fp8_block(
  * batch); the workspace is that of pa_decode_default_splits) and may count
  * the end of a sequence like some blocks when it divides them.  (With
  * PA_LAUNCH_EARLY_KV the pools must not be written by the kernel before; the
- * scale arrays are read after it).  k_scale and v_scale must be 8-byte
- * aligned; NULL or unaligned: PA_ERR_INVALID_ARG.
+ * scale arrays are read after it).  k_scale and v_scale must be aligned to
+ * num_kv_heads bytes and start at the same place modulo 8 (as a layer of two
+ * aligned [layers][num_blocks][num_kv_heads] tensors does, whatever num_blocks);
+ * NULL or placed otherwise: PA_ERR_INVALID_ARG.
  */
 PA_API pa_status pa_decode_fp8_block(
     void *out, int32_t out_dtype, const void *q, const void *k_cache, const void *v_cache,

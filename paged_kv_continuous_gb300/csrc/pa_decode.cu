@@ -611,9 +611,12 @@ extern "C" pa_status pa_decode_fp8_block(
   r.k_bscale = k_scale;
   r.v_bscale = v_scale;
   if (batch > 0 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
-  // a block's scale bytes are read as one word
-  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 7)
-    return PA_ERR_INVALID_ARG;
+  // A block's scale bytes are read as one word of num_kv_heads bytes.  The same
+  // layer of two aligned tensors starts at the same place modulo 8; arrays that
+  // do not are refused.
+  const uintptr_t ka = reinterpret_cast<uintptr_t>(k_scale);
+  const uintptr_t va = reinterpret_cast<uintptr_t>(v_scale);
+  if (((ka ^ va) & 7) || (ka & 7 & (uintptr_t)(num_kv_heads - 1))) return PA_ERR_INVALID_ARG;
   int device = -1;
   const pa_status st = check_decode_request(r, &device);
   if (st != PA_OK || batch == 0) return st;

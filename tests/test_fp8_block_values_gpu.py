@@ -181,3 +181,28 @@ def test_decode_query_rows_that_are_not_finite(ops, Hkv, lens):
         to_dev_bf16(q), to_dev_i32(np.arange(len(lens) + 1)), *[dev(a) for a in cache],
         to_dev_i32(tables), to_dev_i32(ctx), SCALE, 1, out_dtype=torch.float32)
     assert np.array_equal(np.isnan(out.cpu().numpy()), np.isnan(got))
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 4, 8])
+def test_scale_arrays_of_layers_in_one_tensor(ops, Hkv):
+    """Layers as views of [layers, num_blocks, Hkv] scale tensors with an odd
+    number of pages: stored, decoded and prefilled like arrays of their own."""
+    rng = np.random.default_rng(Hkv)
+    layers, NB, Hq = 5, 13, 2 * Hkv
+    ctx = np.array([40, 100], np.int32)
+    tables = random_tables(rng, ctx, NB)
+    q = normal_bits(rng, (2, Hq, 128))
+    k, v = (to_dev_bf16(normal_bits(rng, (2, Hkv, 128))) for _ in range(2))
+    td, cd, one = to_dev_i32(tables), to_dev_i32(ctx), to_dev_i32([0, 1, 2])
+    ks, vs = (torch.zeros((layers, NB, Hkv), dtype=torch.uint8, device="cuda") for _ in range(2))
+    for i in range(layers):
+        cache = [dev(a) for a in ref.random_cache(rng, NB, Hkv)]
+        ks[i], vs[i] = cache[2], cache[3]
+        views = [cache[0].clone(), cache[1].clone(), ks[i], vs[i]]
+        outs = []
+        for c in (cache, views):
+            ops.store_kv_fp8_block(k, v, *c, one, td, cd)
+            outs.append(ops.decode_fp8_block(to_dev_bf16(q), *c, td, cd, SCALE))
+            outs.append(ops.prefill_varlen_fp8_block(to_dev_bf16(q), one, *c, td, cd, SCALE, 1))
+        assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3]), i
+        assert all(torch.equal(a, b) for a, b in zip(cache, views))
