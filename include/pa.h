@@ -547,7 +547,8 @@ PA_API pa_status pa_decode_fp8(void *out, int32_t out_dtype, const void *q, cons
  *   error_flags    optional int32 word (may be NULL): a chunk outside k / v,
  *                  longer than its context or past its table row sets
  *                  PA_DEVERR_SHAPE, a table entry outside the pool sets
- *                  PA_DEVERR_BLOCK_INDEX; that sequence or block is skipped.
+ *                  PA_DEVERR_BLOCK_INDEX; that sequence or block is skipped
+ *                  (with cu_seqlens that fall, other sequences too may be).
  *   flags          0 or PA_LAUNCH_PDL, which mean the same here: nothing is
  *                  read or written before the kernel before is over, and the
  *                  kernel after may be set up early.

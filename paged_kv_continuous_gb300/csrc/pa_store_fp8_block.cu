@@ -19,7 +19,9 @@
 // Work list.  A sequence of q tokens touches at most floor(q / 16) + 2 pages,
 // so unit u = floor(cu_seqlens[s] / 16) + 2 s + i names the i-th page of
 // sequence s without overlap, the host sizes the grid from total_tokens and
-// num_seqs alone, and a warp finds its s by a 32-way search.
+// num_seqs alone, and a warp finds its s by a 32-way search.  A chunk that is not
+// consistent may have no unit, so warps behind the units look at all sequences,
+// one per lane, and report.
 //
 // Measured: 5 x 5-8 k tokens at 8 kv heads (204 MB) 34.1 us, 6.0 TB/s, 88 % of
 // the measured copy bandwidth; 32 k tokens at 2 kv heads (49 MB) 9.8 us; the 64
@@ -73,6 +75,12 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int num_seqs, long lo
     n = min(step, n - from);
   }
   return lo;
+}
+
+// A chunk cu_seqlens[s] = c0 .. c1 - 1 that lies outside the rows or is longer than
+// its context n.
+__device__ __forceinline__ bool inconsistent(int c0, int c1, int n, int total_tokens) {
+  return c0 < 0 || c1 < c0 || c1 > total_tokens || n < c1 - c0;
 }
 
 // One warp's share of a page: rows r0 .. r1 - 1 of one head of K (dst = row 0 of
@@ -190,8 +198,14 @@ __global__ void __launch_bounds__(32 * kQsWarps, 8)
       (long long)blockIdx.x * kQsWarps + __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
   const int per = 2 * p.hkv;
   const long long u = w / per;
-  if (u >= p.units) return;
   const int x = (int)(w % per), is_v = x & 1, h = x >> 1;
+  if (u >= p.units) {
+    const long long m = 32 * (u - p.units) + lane;
+    if (x == 0 && m < p.num_seqs &&
+        inconsistent(p.cu_seqlens[m], p.cu_seqlens[m + 1], p.context_lens[m], p.total_tokens))
+      report(p.err, PA_DEVERR_SHAPE);
+    return;
+  }
 
   int s, c0, c1, n;
   if (p.num_seqs <= 32) {
@@ -211,10 +225,7 @@ __global__ void __launch_bounds__(32 * kQsWarps, 8)
     n = p.context_lens[s];
   }
   const long long i = u - (((long long)(c0 >> 4)) + 2ll * s);  // page of the chunk
-  if (c0 < 0 || c1 < c0 || c1 > p.total_tokens || n < c1 - c0) {
-    if (i == 0 && x == 0 && lane == 0) report(p.err, PA_DEVERR_SHAPE);
-    return;
-  }
+  if (inconsistent(c0, c1, n, p.total_tokens)) return;
   const int first = n - (c1 - c0);         // position of the chunk's first token
   const long long j = (first >> 4) + i;    // logical page
   if (c1 == c0 || i < 0 || j * kBlockSize >= n) return;
@@ -312,7 +323,7 @@ extern "C" pa_status pa_store_kv_fp8_block(
   p.context_lens = context_lens;
   p.err = error_flags;
   p.units = (long long)(total_tokens / kBlockSize) + 2ll * num_seqs;
-  const long long warps = p.units * 2 * num_kv_heads;
+  const long long warps = (p.units + (num_seqs + 31ll) / 32) * 2 * num_kv_heads;
   const long long blocks = (warps + kQsWarps - 1) / kQsWarps;
   if (blocks > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
   // rows are read 8 bytes a lane where base and strides allow it
