@@ -201,7 +201,8 @@ __device__ __forceinline__ void apply_fork(const ForkParams &p, const Fork &f, i
 // the child holds pages or is an earlier fork's child, or the parent's
 // context does not fit its table row.  The children claim their rows: the
 // context length of an empty child row takes INT_MIN + i of the lowest fork i
-// that names it until the plan is applied (a length below 1 reads as empty).
+// that names it until the plan is applied (a length below 1 reads as empty; a
+// negative one becomes 0 first, so that none is taken for a claim).
 //
 // The plan is a chain of dependent loads by one block (about 4 us), so up to
 // 1024 forks keep their rows and plan in shared memory between its steps.
@@ -216,9 +217,13 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
   const int32_t *parents = small ? kept[0] : p.parents, *children = small ? kept[1] : p.children;
   int32_t *src = small ? kept[2] : p.src, *dst = small ? kept[3] : p.dst;
   int32_t *forked = small ? kept[4] : p.forked;
-  if (small && tid < p.n) {
-    kept[0][tid] = p.parents[tid];
-    kept[1][tid] = p.children[tid];
+  for (int i = tid; i < p.n; i += kPlanThreads) {
+    const int c = p.children[i];
+    if (small) {
+      kept[0][i] = p.parents[i];
+      kept[1][i] = c;
+    }
+    if (c >= 0 && c < p.rows && ctx[c] < 0) ctx[c] = 0;
   }
   // the first pages' counts, for step 3
   unsigned first_mask = 0;
