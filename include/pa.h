@@ -704,7 +704,8 @@ PA_API pa_status pa_copy_pages(const pa_page_pool *pools, int32_t num_pools, int
  * (PA_DEVERR_PAGES).  A parent that is empty when the call begins gives an
  * empty child, whatever else the call does to it.  Table entries past the
  * child's pages are left as they are.  An entry outside the pool is copied
- * and reported (PA_DEVERR_BLOCK_INDEX).
+ * and reported (PA_DEVERR_BLOCK_INDEX), a part-filled last one too (its pair
+ * is -1, -1, and the page picked for it stays free).
  *   copy_src, copy_dst, forked   int32 [num_forks], written.
  */
 PA_API pa_status pa_fork_pages(int32_t *block_tables, int32_t block_table_stride,

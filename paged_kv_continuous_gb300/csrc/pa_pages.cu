@@ -281,6 +281,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
     if (n > 0 && n % kBlockSize != 0) {
       if (dst[i] >= 0) {
         s = p.tables[(long long)parents[i] * p.stride + n / kBlockSize];
+        // an entry outside the pool is copied like any other (and reported by
+        // apply_fork): the page picked for it stays free
+        if (s < 0 || s >= p.num_blocks) s = dst[i] = -1;
       } else {
         forked[i] = -1;  // no page left
         report(p.err, PA_DEVERR_PAGES);

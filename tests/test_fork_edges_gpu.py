@@ -48,3 +48,20 @@ def test_empty_rows_of_any_negative_length(ops, n):
     assert err == ops.DEVERR_SHAPE
     assert list(forked) == [0, 20, -1] and list(dst) == [-1, 2, -1]
     assert c[2] == 0 and c[3] == 20
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 12, 2 ** 31 - 1])
+def test_last_entry_outside_the_pool(ops, bad):
+    """Copied and reported like any other: no page is taken in its place and
+    no pair names it."""
+    tables = np.array([[0, bad], [1, 2], [-1, -1], [-1, -1]], np.int32)
+    refs = np.zeros(12, np.int32)
+    refs[:3] = 1
+    err, src, dst, forked, t, c, r = fork(ops, tables, [20, 20, 0, 0], refs, [0, 1], [2, 3])
+    assert err == ops.DEVERR_BLOCK_INDEX
+    assert list(forked) == [20, 20] and list(c) == [20] * 4
+    assert (src[0], dst[0]) == (-1, -1) and list(t[2]) == [0, bad]
+    assert src[1] == 2 and dst[1] >= 3 and list(t[3]) == [1, dst[1]]
+    want = np.zeros(12, np.int32)
+    want[[0, 1, 2, dst[1]]] = [2, 2, 1, 1]
+    assert np.array_equal(r, want)
