@@ -827,8 +827,9 @@ PA_API pa_status pa_prefill_store_varlen(void *out, int32_t out_dtype, const voi
  * rounded to f16 (11 bits) after taking in the V scale of their block.  A
  * query row with a NaN or an infinity gives NaN.  Rows past
  * cu_seqlens[num_seqs] are neither read nor written; a chunk with rows outside
- * [0, total_tokens) sets PA_DEVERR_SHAPE and is skipped.  A NaN code reaches the
- * rows that see its key and no other.
+ * [0, total_tokens), or whose context is longer than its table row, sets
+ * PA_DEVERR_SHAPE and is skipped.  A NaN code reaches the rows that see its key
+ * and no other.
  */
 PA_API pa_status pa_prefill_fp8_block(
     void *out, int32_t out_dtype, const void *q, const int32_t *cu_seqlens, int32_t num_seqs,

@@ -119,6 +119,7 @@ struct PrefillQParams {
   float qk_scale_log2;    // > 0: a scale <= 0 is folded into q as staged
   uint32_t q_and, q_xor;  // staged q pairs = (q & q_and) ^ q_xor
   int32_t *err;
+  int max_context;  // keys that a table row has entries for
 };
 
 // Instruction descriptor, fp32 D, M = 128, N = n, both operands K-major and of
@@ -501,9 +502,9 @@ __device__ __forceinline__ WorkItem pick_item(const PrefillQParams &p, int gx, i
     const int s = lane * per + k;
     if (k < per && s < p.num_seqs) {
       const int q = p.cu_seqlens[s + 1] - p.cu_seqlens[s];
-      const int pre = p.context_lens[s] - q;
-      // (reported once, by the CTA of rank 0)
-      if (r == 0 && threadIdx.x < 32 && q > 0 && (pre < 0 || q > (long long)gx * PT))
+      const int pre = max(p.context_lens[s], 0) - q;
+      // (reported once, by the CTA of rank 0; q < 0: cu_seqlens that fall)
+      if (r == 0 && threadIdx.x < 32 && (pre < 0 || (unsigned)q > (unsigned)(gx * PT)))
         report(p.err, PA_DEVERR_SHAPE);
       if (q > 0 && pre >= 0) {
         prefix[k] = pre;
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kQpThreads, 2)
     g = blockIdx.y;
     s = blockIdx.z;
     const int ql = p.cu_seqlens[s + 1] - p.cu_seqlens[s];
-    if (mt == (int)gridDim.x - 1 && mt * PT + PT < ql && tid == 0)
+    if (mt == (int)gridDim.x - 1 && (unsigned)(mt * PT + PT) < (unsigned)ql && tid == 0)
       report(p.err, PA_DEVERR_SHAPE);  // rows past max_q_len: no CTA covers them
     if (mt * PT >= ql) return;
     if (p.context_lens[s] < ql) {
@@ -642,12 +643,15 @@ __global__ void __launch_bounds__(kQpThreads, 2)
   const int n = p.context_lens[s];
   const int prefix = n - q_len;
   const int npos = min(PT, q_len - pos0);
-  // a chunk with rows outside q: none of the tile's rows is read or written
-  // (an early return here made the whole kernel 8 % slower)
-  const bool inside = q0 >= 0 && q0 + (long long)q_len <= p.total_tokens;
+  // a chunk with rows outside q or a context longer than its table row: none of
+  // the tile's rows is read or written (an early return here made the whole kernel
+  // 8 % slower), and the keys end where the table row does
+  const bool inside =
+      q0 >= 0 && q0 + (long long)q_len <= p.total_tokens && n <= p.max_context;
   if (!inside && tid == 0) report(p.err, PA_DEVERR_SHAPE);
   const int rows = inside ? npos * G : 0;
-  const int kmax = prefix + pos0 + npos - 1;  // last key any row of the tile sees
+  // last key any row of the tile sees
+  const int kmax = min(prefix + pos0 + npos, p.max_context) - 1;
   const int nkv = kmax / kPfKeys + 1;
 
   if (tid == 0) {
@@ -1024,6 +1028,8 @@ extern "C" pa_status pa_prefill_fp8_block(
   p.num_blocks = num_blocks;
   p.block_tables = block_tables;
   p.bt_stride = block_table_stride;
+  p.max_context = block_table_stride < INT_MAX / kBlockSize ? block_table_stride * kBlockSize
+                                                            : INT_MAX;
   p.context_lens = context_lens;
   p.hq = num_q_heads;
   p.hkv = num_kv_heads;

@@ -206,3 +206,39 @@ def test_scale_arrays_of_layers_in_one_tensor(ops, Hkv):
             outs.append(ops.prefill_varlen_fp8_block(to_dev_bf16(q), one, *c, td, cd, SCALE, 1))
         assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3]), i
         assert all(torch.equal(a, b) for a, b in zip(cache, views))
+
+
+@pytest.mark.parametrize("seqs", [3, 300])
+def test_prefill_context_past_its_table_row(ops, seqs):
+    """A context that needs more entries than its table row has, one below its
+    chunk and a chunk that ends before it starts: reported, skipped (their rows
+    stay as they were), the other sequences attended."""
+    rng = np.random.default_rng(seqs)
+    cu = np.arange(seqs + 1, dtype=np.int32) * 2
+    ctx = rng.integers(2, 33, seqs).astype(np.int32)
+    NB = int(((ctx + 15) // 16).sum()) + 2
+    tables = random_tables(rng, ctx, NB)
+    assert tables.shape[1] == 2
+    cache = ref.random_cache(rng, NB, 2)
+    q = normal_bits(rng, (2 * seqs, 12, 128))
+    args = [to_dev_bf16(q), to_dev_i32(cu), *[dev(a) for a in cache], to_dev_i32(tables)]
+    good = ops.prefill_varlen_fp8_block(*args, to_dev_i32(ctx), SCALE, 2,
+                                        out_dtype=torch.float32)
+    for wrong in (33, 4000, 2 ** 20, 1, -2 ** 31, -2 ** 31 + 1):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        bad = ctx.copy()
+        bad[1] = wrong
+        out = torch.full((2 * seqs, 12, 128), 7.0, device="cuda")
+        ops.prefill_varlen_fp8_block(*args, to_dev_i32(bad), SCALE, 2, out=out, error_flags=err)
+        assert int(err.item()) & ops.DEVERR_SHAPE, wrong
+        assert torch.all(out[2:4] == 7.0)
+        assert torch.equal(out[:2], good[:2]) and torch.equal(out[4:], good[4:])
+    # cu_seqlens that fall, at the last sequence
+    err.zero_()
+    fall = cu.copy()
+    fall[-1] = fall[-2] - 1
+    args[1] = to_dev_i32(fall)
+    out.fill_(7.0)
+    ops.prefill_varlen_fp8_block(*args, to_dev_i32(ctx), SCALE, 2, out=out, error_flags=err)
+    assert int(err.item()) & ops.DEVERR_SHAPE
+    assert torch.equal(out[:-2], good[:-2]) and torch.all(out[-2:] == 7.0)
