@@ -1335,87 +1335,90 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         cur = next;
       }
       if (broken && lane == 0) report(p.err, PA_DEVERR_SHAPE);
-    }
-    while (!BS && gb < hi && !stop) {
-      int lb, lj, lctx;
-      const int count = walk_chunk<BS>(p.context_lens, p.batch, b, ctx, j, hi - gb, lane, lb, lj, lctx);
-      if (count == 0) {
-        wait_prev_then_release();
-        if (lane == 0) report(p.err, PA_DEVERR_SHAPE);
-        break;
-      }
-      // all block-table entries of the chunk in one round of loads
-      const bool in_row = lane < count && lj < p.bt_stride;
-      const long long phys = in_row ? ld_index<BS>(p.block_tables + (long long)lb * p.bt_stride + lj) : -1;
-      int n_early = 0;  // stages of this chunk whose K/V pages went out before the wait
-      if (!waited) {
-        // the first chunk's descriptors are ready.  With p.early_kv the K/V
-        // pages of the first ring stages go out now (issued == 0 here, so
-        // stage i of the chunk is ring slot i and needs no empty wait): lane
-        // 0 raises the slot's expected bytes without arriving, so the stage
-        // cannot complete before its arrival (with the q copy) below.  The
-        // rest waits for the previous kernel, which may write q, the new
-        // rows and the workspace.
-        if (p.early_kv) {
-          n_early = min(count, min(S::NST, kDecodeEarlyStages));
-          for (int i = pw; i < n_early; i += kDecodeProducerWarps)
-            issue_kv_stage(i, __shfl_sync(0xffffffffu, phys, i), true);
-        }
-        wait_prev_then_release();
-        waited = true;
-      }
-      // the q rows go with the first NPH stages of every piece: each consumer
-      // warp reads them from its own first stage of the piece
-      const bool with_q = min(gb + lane - lo, (long long)lj) < S::NPH;
-      for (int i = 0; i < count; ++i, ++issued) {
-        if ((int)(issued % kDecodeProducerWarps) != pw) continue;
-        const int st = (int)(issued % S::NST);
-        const int round = (int)(issued / S::NST);
-        if (round > 0 &&
-            !__all_sync(0xffffffffu,
-                        mbar_wait(empty0 + 8 * st, (round - 1) & 1, abort_flag, p.err))) {
-          stop = true;
+    } else {
+      while (gb < hi && !stop) {
+        int lb, lj, lctx;
+        const int count = walk_chunk<false>(p.context_lens, p.batch, b, ctx, j, hi - gb, lane, lb, lj,
+                                           lctx);
+        if (count == 0) {
+          wait_prev_then_release();
+          if (lane == 0) report(p.err, PA_DEVERR_SHAPE);
           break;
         }
-        const long long ph_i = __shfl_sync(0xffffffffu, phys, i);
-        const int b_i = __shfl_sync(0xffffffffu, lb, i);
-        const bool q_i = __shfl_sync(0xffffffffu, with_q ? 1 : 0, i) != 0;
-        const bool row_i = __shfl_sync(0xffffffffu, in_row ? 1 : 0, i) != 0;
-        // every value here is warp-uniform (shuffled from lane i); lane 0
-        // arms the barrier, then the warp issues the copies (elect.sync)
-        const bool ok = ph_i >= 0 && ph_i < p.num_blocks;
-        const uint32_t dst = stage0 + st * S::STAGE_BYTES;
-        const uint32_t bar = full0 + 8 * st;
-        const bool pre = i < n_early;  // K/V already requested and counted
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, (ok && !pre ? 2u * S::KV_BYTES : 0u) +
-                                         (q_i ? S::Q_BYTES + S::ROPE_BYTES : 0u));
-          // a context longer than the table row (caller error) or an entry
-          // outside the pool: reported, not read
-          if (!ok) report(p.err, row_i ? PA_DEVERR_BLOCK_INDEX : PA_DEVERR_SHAPE);
+        // all block-table entries of the chunk in one round of loads
+        const bool in_row = lane < count && lj < p.bt_stride;
+        const long long phys =
+            in_row ? __ldg(p.block_tables + (long long)lb * p.bt_stride + lj) : -1;
+        int n_early = 0;  // stages of this chunk whose K/V pages went out before the wait
+        if (!waited) {
+          // the first chunk's descriptors are ready.  With p.early_kv the K/V
+          // pages of the first ring stages go out now (issued == 0 here, so
+          // stage i of the chunk is ring slot i and needs no empty wait): lane
+          // 0 raises the slot's expected bytes without arriving, so the stage
+          // cannot complete before its arrival (with the q copy) below.  The
+          // rest waits for the previous kernel, which may write q, the new
+          // rows and the workspace.
+          if (p.early_kv) {
+            n_early = min(count, min(S::NST, kDecodeEarlyStages));
+            for (int i = pw; i < n_early; i += kDecodeProducerWarps)
+              issue_kv_stage(i, __shfl_sync(0xffffffffu, phys, i), true);
+          }
+          wait_prev_then_release();
+          waited = true;
         }
-        __syncwarp();
-        if (!pre) issue_kv_stage(st, ph_i, false);
-        if (q_i) {
-          bulk_load_elect(dst + 2 * S::KV_BYTES, q_base + (long long)b_i * S::HQ * kHeadDim,
-                          S::Q_BYTES, bar, pol_q);
-          if constexpr (ROPE) {
-            // the cos and sin rows of the new token's position (row 0 for a
-            // position outside the tables: reported, and the new row is
-            // then neither stored nor patched)
-            long long pos = __ldg(p.positions + b_i);
-            if (pos < 0 || pos >= p.max_position) {
-              if (lane == 0) report(p.err, PA_DEVERR_POSITION);
-              pos = 0;
+        // the q rows go with the first NPH stages of every piece: each consumer
+        // warp reads them from its own first stage of the piece
+        const bool with_q = min(gb + lane - lo, (long long)lj) < S::NPH;
+        for (int i = 0; i < count; ++i, ++issued) {
+          if ((int)(issued % kDecodeProducerWarps) != pw) continue;
+          const int st = (int)(issued % S::NST);
+          const int round = (int)(issued / S::NST);
+          if (round > 0 &&
+              !__all_sync(0xffffffffu,
+                          mbar_wait(empty0 + 8 * st, (round - 1) & 1, abort_flag, p.err))) {
+            stop = true;
+            break;
+          }
+          const long long ph_i = __shfl_sync(0xffffffffu, phys, i);
+          const int b_i = __shfl_sync(0xffffffffu, lb, i);
+          const bool q_i = __shfl_sync(0xffffffffu, with_q ? 1 : 0, i) != 0;
+          const bool row_i = __shfl_sync(0xffffffffu, in_row ? 1 : 0, i) != 0;
+          // every value here is warp-uniform (shuffled from lane i); lane 0
+          // arms the barrier, then the warp issues the copies (elect.sync)
+          const bool ok = ph_i >= 0 && ph_i < p.num_blocks;
+          const uint32_t dst = stage0 + st * S::STAGE_BYTES;
+          const uint32_t bar = full0 + 8 * st;
+          const bool pre = i < n_early;  // K/V already requested and counted
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, (ok && !pre ? 2u * S::KV_BYTES : 0u) +
+                                           (q_i ? S::Q_BYTES + S::ROPE_BYTES : 0u));
+            // a context longer than the table row (caller error) or an entry
+            // outside the pool: reported, not read
+            if (!ok) report(p.err, row_i ? PA_DEVERR_BLOCK_INDEX : PA_DEVERR_SHAPE);
+          }
+          __syncwarp();
+          if (!pre) issue_kv_stage(st, ph_i, false);
+          if (q_i) {
+            bulk_load_elect(dst + 2 * S::KV_BYTES, q_base + (long long)b_i * S::HQ * kHeadDim,
+                            S::Q_BYTES, bar, pol_q);
+            if constexpr (ROPE) {
+              // the cos and sin rows of the new token's position (row 0 for a
+              // position outside the tables: reported, and the new row is
+              // then neither stored nor patched)
+              long long pos = __ldg(p.positions + b_i);
+              if (pos < 0 || pos >= p.max_position) {
+                if (lane == 0) report(p.err, PA_DEVERR_POSITION);
+                pos = 0;
+              }
+              const uint32_t rd = dst + 2 * S::KV_BYTES + S::Q_BYTES;
+              bulk_load_elect(rd, p.cos_table + pos * (kHeadDim / 2), S::ROPE_BYTES / 2, bar, pol_q);
+              bulk_load_elect(rd + S::ROPE_BYTES / 2, p.sin_table + pos * (kHeadDim / 2),
+                              S::ROPE_BYTES / 2, bar, pol_q);
             }
-            const uint32_t rd = dst + 2 * S::KV_BYTES + S::Q_BYTES;
-            bulk_load_elect(rd, p.cos_table + pos * (kHeadDim / 2), S::ROPE_BYTES / 2, bar, pol_q);
-            bulk_load_elect(rd + S::ROPE_BYTES / 2, p.sin_table + pos * (kHeadDim / 2),
-                            S::ROPE_BYTES / 2, bar, pol_q);
           }
         }
+        gb += count;
       }
-      gb += count;
     }
     if (lane == 0 && *abort_flag) {
       // Drain: copies this warp still has in flight must land before the
