@@ -9,8 +9,9 @@ not been built (``python -m paged_kv_continuous_gb300.build``).
 
 A call is enqueued on ``stream`` (default: the current stream), and an output
 or workspace that it allocates because none was given belongs to that stream,
-as if made under ``torch.cuda.stream(stream)``: use it on another stream as
-torch asks for (an event, ``record_stream``).  The prepared calls (``*Call``)
+as if made under ``torch.cuda.stream(stream)``: wait for the stream before using
+it on another, and tell the allocator (``record_stream``) of any but the one
+that was current at the call.  The prepared calls (``*Call``)
 allocate on the stream that is current when they are made; the first call on
 another stream makes that one wait for it, which a call under capture cannot:
 make the call object before the capture, capture behind a synchronize (as
@@ -18,7 +19,6 @@ make the call object before the capture, capture behind a synchronize (as
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -147,10 +147,31 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _on(stream):
+class _on:
     """Where a call on ``stream`` allocates its default buffers: on that stream,
-    so that filling, use and reuse of their memory follow one another."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    so that filling, use and reuse of their memory follow one another.  Gives a
+    function for those that the caller gets, which also tells the allocator of
+    the stream that is current outside."""
+
+    def __init__(self, stream):
+        self._stream = stream
+
+    def __enter__(self):
+        if self._stream is not None:
+            self._outside = torch.cuda.current_stream()
+            self._inside = torch.cuda.stream(self._stream)
+            self._inside.__enter__()
+        return self._handed
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._inside.__exit__(*exc)
+
+    def _handed(self, t):
+        if self._stream is not None and self._outside != self._stream and \
+                self._outside.device == t.device:
+            t.record_stream(self._outside)
+        return t
 
 
 class _Defaults:
@@ -253,8 +274,8 @@ def rope_store_kv(q, k, v, positions, cos_table, sin_table, k_cache, v_cache, sl
     if positions.shape[0] != T or slot_mapping.shape[0] != T:
         raise PagedAttentionError("positions and slot_mapping need one entry per token")
     if q_out is None:
-        with _on(stream):
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        with _on(stream) as handed:
+            q_out = handed(torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device))
     _need(q_out, torch.bfloat16, "q_out", 3)
     if q_out.shape != q.shape or q_out.stride(2) != 1 or q_out.stride(1) != D:
         raise PagedAttentionError("q_out must be [T, Hq, D] with contiguous heads")
@@ -320,9 +341,9 @@ def decode(q, k_cache, v_cache, block_tables, context_lens, scale, out=None,
         raise PagedAttentionError("block_tables rows must be contiguous")
     B, Hq, D = q.shape
     NB, bs, Hkv, _ = k_cache.shape
-    with _on(stream):
+    with _on(stream) as handed:
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+            out = handed(torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
         if workspace is None:
             workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_decode(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(k_cache),
@@ -359,9 +380,9 @@ def store_decode(q, new_k, new_v, k_cache, v_cache, slot_mapping, block_tables, 
     if tuple(new_k.shape) != (B, Hkv, D) or new_v.shape != new_k.shape or \
             slot_mapping.shape[0] != B:
         raise PagedAttentionError("new_k / new_v / slot_mapping need one row per sequence")
-    with _on(stream):
+    with _on(stream) as handed:
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+            out = handed(torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
         if workspace is None:
             workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_store_decode(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
@@ -512,9 +533,9 @@ def rope_store_decode(q, new_k, new_v, k_cache, v_cache, slot_mapping, block_tab
     if cos_table.shape != sin_table.shape or cos_table.shape[1] != D // 2 or \
             not cos_table.is_contiguous() or not sin_table.is_contiguous():
         raise PagedAttentionError("cos_table / sin_table must be contiguous [max_position, D/2]")
-    with _on(stream):
+    with _on(stream) as handed:
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+            out = handed(torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
         if workspace is None:
             workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_rope_store_decode(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
@@ -589,9 +610,9 @@ def decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens
         raise PagedAttentionError("block_tables rows must be contiguous")
     NB, bs, Hkv, _ = _need_fp8_pools(k_cache, v_cache, k_scale, v_scale)
     B, Hq, D = q.shape
-    with _on(stream):
+    with _on(stream) as handed:
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+            out = handed(torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
         if workspace is None:
             workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_decode_fp8(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(k_cache),
@@ -626,9 +647,9 @@ def store_decode_fp8(q, new_k, new_v, k_cache, v_cache, k_scale, v_scale, slot_m
     if tuple(new_k.shape) != (B, Hkv, D) or new_v.shape != new_k.shape or \
             slot_mapping.shape[0] != B:
         raise PagedAttentionError("new_k / new_v / slot_mapping need one row per sequence")
-    with _on(stream):
+    with _on(stream) as handed:
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=out_dtype, device=q.device)
+            out = handed(torch.empty((B, Hq, D), dtype=out_dtype, device=q.device))
         if workspace is None:
             workspace = decode_workspace(Hq, Hkv, num_splits, D, q.device)
     _check(lib.pa_store_decode_fp8(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
@@ -819,9 +840,9 @@ def decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, contex
                      stream=None, pdl=False, early_kv=False):
     """pa_decode_fp8_block: q bf16 [B, Hq, D] over block-scaled FP8 pools
     (see fp8_block_pools); returns out [B, Hq, D]."""
-    with _on(stream):
+    with _on(stream) as handed:
         if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+            out = handed(torch.empty(q.shape, dtype=out_dtype, device=q.device))
         return DecodeFp8BlockCall(q, k_cache, v_cache, k_scale, v_scale, block_tables,
                                   context_lens, scale, out, num_splits, workspace, pdl,
                                   early_kv)(stream)
@@ -864,8 +885,8 @@ def prefill_varlen_fp8_block(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, 
     [N + 1]) over block-scaled FP8 pools that hold the chunks' own keys too
     (store_kv_fp8_block first); returns out [T, Hq, D]."""
     if out is None:
-        with _on(stream):
-            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        with _on(stream) as handed:
+            out = handed(torch.empty(q.shape, dtype=out_dtype, device=q.device))
     return PrefillFp8BlockCall(q, cu_seqlens, k_cache, v_cache, k_scale, v_scale, block_tables,
                                context_lens, scale, max_q_len, out, error_flags)(stream)
 
@@ -972,9 +993,10 @@ def fork_pages(block_tables, context_lens, parents, children, ref_counts, copy_s
     parents[i] (int32 [n]) that shares its full pages; the part-filled last
     page gets a free page, to be filled by ``copy_pages(pools, copy_src,
     copy_dst)``.  Returns (copy_src, copy_dst, forked), int32 [n] each."""
-    with _on(stream):
-        return ForkPagesCall(block_tables, context_lens, parents, children, ref_counts, copy_src,
-                             copy_dst, forked, error_flags, pdl)(stream)
+    with _on(stream) as handed:
+        out = ForkPagesCall(block_tables, context_lens, parents, children, ref_counts, copy_src,
+                            copy_dst, forked, error_flags, pdl)(stream)
+        return tuple(map(handed, out))
 
 
 class FreePagesCall(_Prepared):
@@ -1028,9 +1050,10 @@ def compact_pages(block_tables, context_lens, ref_counts, copy_src=None, copy_ds
     pool and bring tables and counts up to date; ``copy_pages(pools, copy_src,
     copy_dst, count=counts)`` then moves the contents.  Returns (copy_src,
     copy_dst [NB / 2], counts [moves, live pages], remap [NB]), int32."""
-    with _on(stream):
-        return CompactPagesCall(block_tables, context_lens, ref_counts, copy_src, copy_dst,
-                                counts, remap, error_flags, pdl)(stream)
+    with _on(stream) as handed:
+        out = CompactPagesCall(block_tables, context_lens, ref_counts, copy_src, copy_dst,
+                               counts, remap, error_flags, pdl)(stream)
+        return tuple(map(handed, out))
 
 
 def decode_merge(out, workspace, context_lens, num_splits, block_size=16, stream=None):
@@ -1054,8 +1077,8 @@ def prefill_varlen(q, cu_seqlens, k_cache, v_cache, block_tables, context_lens, 
     T, Hq, D = q.shape
     NB, bs, Hkv, _ = k_cache.shape
     if out is None:
-        with _on(stream):
-            out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        with _on(stream) as handed:
+            out = handed(torch.empty((T, Hq, D), dtype=out_dtype, device=q.device))
     _check(lib.pa_prefill_varlen(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(cu_seqlens),
                                  cu_seqlens.shape[0] - 1, T, int(max_q_len), _ptr(k_cache),
                                  _ptr(v_cache), NB, _ptr(block_tables), block_tables.stride(0),
@@ -1086,8 +1109,8 @@ def prefill_store_varlen(q, new_k, new_v, slot_mapping, cu_seqlens, k_cache, v_c
             slot_mapping.shape[0] != T:
         raise PagedAttentionError("new_k / new_v / slot_mapping need one row per token")
     if out is None:
-        with _on(stream):
-            out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        with _on(stream) as handed:
+            out = handed(torch.empty((T, Hq, D), dtype=out_dtype, device=q.device))
     _check(lib.pa_prefill_store_varlen(_ptr(out), _out_code(out.dtype), _ptr(q), _ptr(new_k),
                                        _ptr(new_v), new_k.stride(0), new_v.stride(0),
                                        _ptr(slot_mapping), _ptr(cu_seqlens),

@@ -139,3 +139,25 @@ def test_store_decode_call_made_on_a_busy_stream(ops):
     call(side)
     side.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_output_used_and_dropped_on_the_current_stream(ops, data, name):
+    """The output of a call on another stream, read late by the current one and
+    let go at once: later calls on that stream do not get its memory early."""
+    fn = calls(ops, data)[name]
+    want = fn(None).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = fn(side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(LONG // 4)
+        late = got.clone()  # runs when the sleep is over
+        shape, dtype = got.shape, got.dtype
+        del got
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                torch.full(shape, 1, dtype=dtype, device="cuda")
+        side.synchronize()
+        assert torch.equal(late, want)
