@@ -316,9 +316,12 @@ pa_status run_decode(const DecodeRequest &r, void *workspace, int32_t *err, int 
   const bool split_merge = !r.positions && r.num_kv_heads >= 4 &&
                            (long long)r.splits >= 8LL * r.batch;
   // (explicit counts are kept: their partition is documented).  Measured against
-  // all 152 splits: 8 sequences of 55 blocks 15.4 against 21.8 us, one of 250
-  // 15.6 / 35.4, 96 of one block 7.4 / 7.7, and with the merge kernel 4 of 44
-  // blocks 13.4 / 12.7, one of 250 14.7 / 17.9.
+  // all 152 splits, us in a chain of calls at 12/2 heads: one sequence of 19
+  // blocks 11.3 against 360 (splits without a block), of 250 14.5 / 35.6, of 1250
+  // 22.6 / 37.0, 64 of ten 12.8 / 15.8, 96 of one 7.6 / 7.6; the other way round 8 of
+  // 55 13.6 / 13.1 and one block alone 7.3 / 6.9.  With the merge kernel, 32/8
+  // heads: 4 of two 7.5 / 11.7, one of 19 11.0 / 23.0, of 250 14.8 / 17.5, 4 of 44
+  // 11.9 / 12.0; the other way round nothing over 0.2 us.
   p.split_rule = r.num_splits != 0 ? kSplitsAll : split_merge ? kSplitsHalf : kSplitsRoot;
   // (units of a piece's end: 2 / 4 / 6 / 8 / 12 took 22.8 / 22.0 / 20.1 / 20.2 /
   // 20.5 us for 64 log-uniform sequences at 2 kv heads, 28.6 / 27.7 / 28.1 /

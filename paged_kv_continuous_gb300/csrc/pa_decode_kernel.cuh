@@ -1232,8 +1232,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       // before it is issued, and a stage is one request and one arrival by the
       // lane that holds its scales: with the loads at the chunk's head and a
       // value at a time shuffled, the producers set the pace below 4 kv heads:
-      // 0.33 us a block and CTA at 2 heads, 0.20 so (155 -> 101 us for
-      // 8 x 131072 keys, 5.3 TB/s).
+      // 0.33 us a block and CTA at 2 heads, 0.20 so (155 -> 102 us for
+      // 8 x 131072 keys, 5.2 TB/s).
       struct Chunk {
         int count, lb, x;    // lane L: sequence and table entry of block L
         unsigned with_q;     // blocks whose stage carries the q rows

@@ -33,7 +33,7 @@
 // tensor pipe.
 //
 // What bounds it (two chunks of 2 k queries behind 15 k keys, Hq 32, Hkv 8:
-// 818 us, 1.19 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
+// 823 us, 1.18 PFLOP/s causal): a 64-key step of both CTAs of an SM takes about
 // 1630 cycles, of which the tensor pipe is busy about 1280 (the score MMAs at N
 // = 64 read their A and B tiles from shared memory at 48 cycles each, against
 // 32 of arithmetic), and the latency of the single warps' instruction streams
@@ -52,8 +52,8 @@
 // rows that see it write NaN there at the end.  The rest of that is out of line:
 // inlined, it moved registers of the tile loops, 2 % (and 14 % for a search by the
 // softmax threads before they start).  As it is, the long case takes 824 us
-// against 812 without, the mixed one 54.5 against 54.9.  A query row with a NaN or
-// an infinity gives NaN.
+// against 812 without, the mixed one 54.5 against 54.9, timed in turn.  A query row
+// with a NaN or an infinity gives NaN.
 #include <climits>
 #include <cmath>
 #include <cstring>

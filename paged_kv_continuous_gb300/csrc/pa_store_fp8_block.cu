@@ -23,9 +23,10 @@
 // consistent may have no unit, so warps behind the units look at all sequences,
 // one per lane, and report.
 //
-// Measured: 5 x 5-8 k tokens at 8 kv heads (204 MB) 34.1 us, 6.0 TB/s, 88 % of
-// the measured copy bandwidth; 32 k tokens at 2 kv heads (49 MB) 9.8 us; the 64
-// tokens of a decode step 3.6 us (launch and four dependent loads).  It was
+// Measured in chains of calls: 5 x 5-8 k tokens at 8 kv heads (204 MB) 33.9 us,
+// 6.0 TB/s, 89 % of the measured copy bandwidth; 32 k tokens at 2 kv heads (49 MB)
+// 9.5 us; the 64 tokens of a decode step 3.6 us (launch and four dependent
+// loads).  It was
 // bound by its instructions, not by memory: pages that are all new take a path
 // without row masks, two bf16 per maximum and byte transposes of two rounds of
 // permutes (about 280 instructions a warp, from 700), 45.3 -> 34.1 us.  A warp

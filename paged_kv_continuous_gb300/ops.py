@@ -11,11 +11,11 @@ A call is enqueued on ``stream`` (default: the current stream), and an output
 or workspace that it allocates because none was given belongs to that stream,
 as if made under ``torch.cuda.stream(stream)``: wait for the stream before using
 it on another, and tell the allocator (``record_stream``) of any but the one
-that was current at the call.  The prepared calls (``*Call``)
-allocate on the stream that is current when they are made; the first call on
-another stream makes that one wait for it, which a call under capture cannot:
-make the call object before the capture, capture behind a synchronize (as
-``torch.cuda.graph`` does), and keep the object as long as the graph.
+that was current at the call.  The prepared calls (``*Call``) allocate on the
+stream that is current when they are made; the first call on another stream
+makes that one wait for it, which a call under capture cannot: make the call
+object before the capture, capture behind a synchronize (as ``torch.cuda.graph``
+does), and keep the object as long as the graph.
 """
 from __future__ import annotations
 
