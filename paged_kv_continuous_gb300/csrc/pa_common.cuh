@@ -249,7 +249,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ int ceil_div_blocks(int n) { return (n + kBlockSize - 1) / kBlockSize; }
+// Blocks of n >= 0 keys (unsigned: the largest int32 lengths do not wrap).
+__device__ __forceinline__ int ceil_div_blocks(int n) {
+  return (int)(((unsigned)n + (unsigned)(kBlockSize - 1)) / (unsigned)kBlockSize);
+}
 
 // Decode split partition.  Split c of S over N global blocks starts at
 // floor(N W(c) / W(S)), W(c) the summed weights of splits 0 .. c - 1.
