@@ -21,7 +21,10 @@
  * pa_store_kv_fp8_block appends to it, pa_decode_fp8_block and
  * pa_prefill_fp8_block attend to it.
  * Pages of any of the caches are managed by pa_fork_pages, pa_free_pages,
- * pa_compact_pages and pa_copy_pages.
+ * pa_compact_pages and pa_copy_pages.  A speculative step over the bf16 cache
+ * is pa_decode_tree (attention of a tree of drafted tokens), pa_verify_tree
+ * (which of them the target's probabilities accept) and pa_commit_tree (their
+ * rows become the sequence's).
  *
  * Sources (web pages that describe the method):
  *   [EAS] koas-w, "errors and solutions" (Qwen2.5-1.5B inference from
@@ -118,12 +121,14 @@ typedef int32_t pa_status;
 #define PA_DEVERR_SHAPE 8         /* context_lens / cu_seqlens inconsistent */
 #define PA_DEVERR_POSITION 16     /* a position outside the rotary tables */
 #define PA_DEVERR_PAGES 32        /* no free page left, or a page freed that nobody holds */
+#define PA_DEVERR_TOKEN 64        /* a drafted token outside the vocabulary */
 
 /*
  * Launch flags (the `flags` argument of pa_store_kv, pa_store_kv_fp8,
  * pa_rope_store_kv, pa_decode, pa_store_decode, pa_rope_store_decode,
  * pa_decode_fp8, pa_store_decode_fp8, pa_decode_noalloc, pa_store_kv_fp8_block,
- * pa_decode_fp8_block and the page operators).  Any other bit returns PA_ERR_INVALID_ARG.
+ * pa_decode_fp8_block, the page operators, pa_decode_tree, pa_verify_tree and
+ * pa_commit_tree).  Any other bit returns PA_ERR_INVALID_ARG.
  *
  * PA_LAUNCH_PDL: programmatic dependent launch.  The call's kernel may begin
  * while the kernel launched just before it on the same stream is still
@@ -838,6 +843,154 @@ PA_API pa_status pa_prefill_fp8_block(
     const int32_t *block_tables, int32_t block_table_stride, const int32_t *context_lens,
     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, float scale,
     int32_t *error_flags, void *stream);
+
+/*
+ * Speculative decoding over the bf16 cache (the pages describe none).  A
+ * sequence has P committed keys and a tree of T drafted nodes behind them:
+ * nodes are packed by cu_seqlens like a prefill's chunks, node i of a sequence
+ * is row cu_seqlens[s] + i, its K/V rows are at position P + i of the sequence
+ * (store them with pa_store_kv or pa_rope_store_kv first), and context_lens[s]
+ * = P + T.  parents[cu_seqlens[s] + i] is the node before it, an index within
+ * the sequence below i, or -1 for a node that follows the committed keys
+ * directly.  Node 0 is commonly the last token that is certain (its K/V not
+ * yet in the cache) and the others guesses; a chain (parents i - 1) is a
+ * causal chunk.
+ *
+ * pa_decode_tree -- attention of every node to the committed keys and to the
+ * nodes on its way to the root, itself included:
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . K[j][g]) V[j][g]
+ * over j < P and j = P + a for each such node a.
+ *
+ *   out            [total_tokens][num_q_heads][head_dim], out_dtype; rows at
+ *                  or past cu_seqlens[num_seqs] are neither read nor written.
+ *   q              bf16 [total_tokens][num_q_heads][head_dim], contiguous.
+ *   cu_seqlens     int32 [num_seqs + 1], non-decreasing, from 0.
+ *   parents        int32 [total_tokens].
+ *   max_q_len      upper bound of every T.
+ *   context_lens   int32 [num_seqs], the nodes included.
+ *   scale          any finite value, of either sign.
+ *   num_splits     CTAs that share the work; 0 = as many of
+ *                  pa_decode_tree_default_splits as suit the work they find.
+ *   workspace      >= pa_decode_tree_workspace_size(S) bytes, 16-byte aligned,
+ *                  S = num_splits or the default: int32 error word at byte 0
+ *                  (zero it once; the library only ORs bits in), the rest is
+ *                  written before it is read.  One call in flight at a time.
+ *   flags          0 or PA_LAUNCH_PDL, which mean the same here: nothing is
+ *                  read or written before the kernel before is over, and the
+ *                  kernel after may be set up early.
+ * Products run on the tensor cores with fp32 accumulation, the softmax weights
+ * as two bf16 terms (16 bits).  A V row's infinities and NaN among the drafted
+ * nodes give NaN to the nodes that see it, and to no others.  A sequence with
+ * rows outside [0, total_tokens), more than max_q_len nodes, fewer keys than
+ * nodes, or a context past its table row sets PA_DEVERR_SHAPE and is skipped; a
+ * parent outside [-1, i) sets it too and leaves the rows of the node and of
+ * those after it unspecified; a table entry outside the pool sets
+ * PA_DEVERR_BLOCK_INDEX, with the sequence's rows unspecified.  Results are
+ * deterministic for a fixed num_splits and do not depend on where pages lie.
+ */
+PA_API size_t pa_decode_tree_workspace_size(int32_t num_splits);
+PA_API int32_t pa_decode_tree_default_splits(int32_t device);
+PA_API pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
+                                const int32_t *cu_seqlens, const int32_t *parents,
+                                int32_t num_seqs, int32_t total_tokens, int32_t max_q_len,
+                                const void *k_cache, const void *v_cache, int64_t num_blocks,
+                                const int32_t *block_tables, int32_t block_table_stride,
+                                const int32_t *context_lens, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                float scale, int32_t num_splits, void *workspace,
+                                size_t workspace_bytes, uint32_t flags, void *stream);
+
+/*
+ * pa_verify_tree -- which drafted nodes are kept, and the token after them,
+ * so that the tokens are distributed as the target's own.  The walk starts at
+ * node 0 of each tree, which is certain.  At node c, with p the row of
+ * target_probs for c, q the row of draft_probs that c's children were drawn
+ * from, and beta = 0, W = 1, gone = 0, the children of c are tried in the order
+ * of their index.  A child with token x and random number u is accepted iff
+ *   u * W * q[x] / max(1 - gone, 2^-24) < p[x] - beta q[x],
+ * and the walk goes on from it.  If it is rejected,
+ *   beta += W / max(1 - gone, 2^-24);   W = sum_y max(p[y] - beta q[y], 0);
+ *   gone += q[x]   (only where siblings were drawn without replacement),
+ * which is the usual replacement of the target by the normalised positive part
+ * of (target - draft), taken together over the siblings rejected so far.
+ * Where no child is left, the next token is drawn from the weights w[y] =
+ * max(p[y] - beta q[y], 0) (p itself if they are all zero): with u' the
+ * sequence's sample_uniforms and C the running sum of w, the smallest y with
+ * C[y] > u' C[last], or the last y of positive weight if there is none.
+ * Without draft_probs (guesses that were looked up) a child is accepted iff
+ * u W < p[x], and a rejected one takes its weight out: W -= p[x], p[x] = 0.
+ * These are taken as if in 64 bits (sums to within 2^-44 of their total).
+ *
+ *   accepted       int32 [num_seqs], written: nodes on the walk, node 0
+ *                  included (0 for a sequence without nodes).
+ *   path           int32 [num_seqs][max_q_len], written: their indices, -1
+ *                  behind them.
+ *   out_tokens     int32 [num_seqs][max_q_len], written: the tokens of path[1
+ *                  ..], then the drawn one, -1 behind it: as many new tokens
+ *                  as accepted nodes.
+ *   tokens         int32 [total_tokens] (node 0's is not read).
+ *   target_probs   fp32 [total_tokens][vocab_size], rows target_stride
+ *                  elements apart: probabilities, which sum to one up to
+ *                  rounding; a negative or NaN weight counts as zero.
+ *   draft_probs    the same with draft_stride, or NULL.
+ *   uniforms       fp32 [total_tokens], in [0, 1): one for each node's test.
+ *   sample_uniforms  fp32 [num_seqs], in [0, 1).
+ *   draws          PA_DRAWS_WITHOUT_REPLACEMENT or PA_DRAWS_WITH_REPLACEMENT:
+ *                  how siblings were drawn from their row.
+ *   error_flags    optional int32 word (may be NULL): rows outside [0,
+ *                  total_tokens) or more than max_q_len nodes set
+ *                  PA_DEVERR_SHAPE (accepted 0); a node whose parent is its own
+ *                  or a later node sets it too and is never reached; a tried
+ *                  token outside [0, vocab_size) sets PA_DEVERR_TOKEN and its
+ *                  node is passed over.  All target weights zero: the drawn
+ *                  token is -1.
+ *   flags          as for pa_decode_tree.
+ */
+#define PA_DRAWS_WITHOUT_REPLACEMENT 0
+#define PA_DRAWS_WITH_REPLACEMENT 1
+PA_API pa_status pa_verify_tree(int32_t *accepted, int32_t *path, int32_t *out_tokens,
+                                const int32_t *tokens, const int32_t *parents,
+                                const int32_t *cu_seqlens, int32_t num_seqs,
+                                int32_t total_tokens, int32_t max_q_len,
+                                const float *target_probs, int64_t target_stride,
+                                const float *draft_probs, int64_t draft_stride,
+                                int32_t vocab_size, const float *uniforms,
+                                const float *sample_uniforms, int32_t draws,
+                                int32_t *error_flags, uint32_t flags, void *stream);
+
+/*
+ * pa_commit_tree -- the accepted nodes become the sequence's last keys: in
+ * every pool, the row at position P + path[s][i] moves to position P + i, for
+ * i < accepted[s], with P = context_lens[s] - T; then context_lens[s] = P +
+ * accepted[s].  With ref_counts, the pages that the row no longer needs are
+ * let go (the counts of entries ceil(new / 16) .. ceil(old / 16) - 1 fall by
+ * one, PA_DEVERR_PAGES where a count is below 1 already).  Moves are exact.
+ *
+ *   pools          HOST array, read before the call returns, as for
+ *                  pa_copy_pages; the pools are token-major, a page being
+ *                  block_size rows (bf16 K and V; the E4M3 codes of K), so a
+ *                  page size is a multiple of block_size bytes.  Pages that a
+ *                  node lies in are held by their sequence alone.
+ *   context_lens   int32 [num_seqs], the nodes included; updated.
+ *   path           int32 [num_seqs][path_stride], increasing from path[s][0]
+ *                  >= 0, as pa_verify_tree writes it.
+ *   accepted       int32 [num_seqs]; 0 moves nothing and drops every node.
+ *   ref_counts     int32 [num_blocks], or NULL.
+ *   error_flags    optional int32 word (may be NULL): cu_seqlens that fall,
+ *                  more nodes than keys, a context past its table row,
+ *                  accepted outside [0, min(T, path_stride)] or a path that is
+ *                  not increasing within [0, T) set PA_DEVERR_SHAPE and the
+ *                  sequence stays as it was; a table entry outside the pool
+ *                  sets PA_DEVERR_BLOCK_INDEX and skips its rows.
+ *   flags          as for pa_decode_tree.
+ */
+PA_API pa_status pa_commit_tree(const pa_page_pool *pools, int32_t num_pools, int64_t num_blocks,
+                                const int32_t *block_tables, int32_t block_table_stride,
+                                int32_t *context_lens, const int32_t *cu_seqlens,
+                                int32_t num_seqs, const int32_t *path, int32_t path_stride,
+                                const int32_t *accepted, int32_t *ref_counts,
+                                int32_t block_size, int32_t *error_flags, uint32_t flags,
+                                void *stream);
 
 #ifdef __cplusplus
 }

@@ -42,10 +42,6 @@
 // warp 2) through slot_mapping.
 #include <cmath>
 #include <cstring>
-#include <mutex>
-
-#include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "pa_prefill_common.cuh"
 
@@ -801,41 +797,11 @@ __global__ void __launch_bounds__(kPfThreads, 2)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-// (dim 128, kv head, token slot) view of a pool; one box = 64 dims x 1 head x
-// 16 slots (one page of one head), 128-byte swizzle.
-bool pool_map(CUtensorMap *map, const void *pool, long long num_blocks, int hkv) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv,
-                        (cuuint64_t)num_blocks * kBlockSize};
-  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)hkv * kHeadDim * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)kBlockSize};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // (dim 128, kv head, token) view of the new rows (token stride in elements,
-// a multiple of 8); the same box as pool_map: 64 dims x 1 head x 16 tokens.
+// a multiple of 8); the same box as pf_pool_map: 64 dims x 1 head x 16 tokens.
 bool rows_map(CUtensorMap *map, const void *rows, long long num_tokens, int hkv,
               long long tok_stride) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = pf_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv, (cuuint64_t)num_tokens};
   cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)tok_stride * 2};
@@ -909,8 +875,8 @@ pa_status prefill_entry(void *out, int32_t out_dtype, const void *q, const int32
   CUtensorMap tk, tv, tnk, tnv;
   memset(&tk, 0, sizeof tk);
   memset(&tv, 0, sizeof tv);
-  if (!pool_map(&tk, k_cache, num_blocks, num_kv_heads) ||
-      !pool_map(&tv, v_cache, num_blocks, num_kv_heads))
+  if (!pf_pool_map(&tk, k_cache, num_blocks, num_kv_heads) ||
+      !pf_pool_map(&tv, v_cache, num_blocks, num_kv_heads))
     return PA_ERR_DEVICE;
   tnk = tk;
   tnv = tv;

@@ -1,8 +1,11 @@
 // Pieces shared by the varlen prefill kernels: the tcgen05 and TMEM wrappers
-// in inline PTX and packed fp32 arithmetic.
+// in inline PTX, packed fp32 arithmetic and the tensor map of a bf16 pool.
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
 
 #include "pa_common.cuh"
 
@@ -222,6 +225,36 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // Byte offset of (row, 16-byte chunk) inside a [128 rows][128 B] swizzled half.
 __device__ __forceinline__ uint32_t sw128(int row, int chunk) {
   return row * 128 + ((chunk ^ (row & 7)) << 4);
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 pf_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// (dim 128, kv head, token slot) view of a pool; one box = 64 dims x 1 head x
+// 16 slots (one page of one head), 128-byte swizzle.
+inline bool pf_pool_map(CUtensorMap *map, const void *pool, long long num_blocks, int hkv) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = pf_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv,
+                        (cuuint64_t)num_blocks * kBlockSize};
+  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)hkv * kHeadDim * 2};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)kBlockSize};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace pa

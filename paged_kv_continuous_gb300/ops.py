@@ -39,6 +39,9 @@ DEVERR_WAIT_TIMEOUT = 4
 DEVERR_SHAPE = 8
 DEVERR_POSITION = 16
 DEVERR_PAGES = 32
+DEVERR_TOKEN = 64
+PA_DRAWS_WITHOUT_REPLACEMENT = 0
+PA_DRAWS_WITH_REPLACEMENT = 1
 
 EXPORTED = (
     "pa_abi_version", "pa_status_string", "pa_store_kv", "pa_decode_workspace_size",
@@ -47,7 +50,8 @@ EXPORTED = (
     "pa_store_decode", "pa_store_decode_fp8", "pa_prefill_store_varlen",
     "pa_rope_store_decode", "pa_get_device_error", "pa_copy", "pa_store_kv_fp8_block",
     "pa_decode_fp8_block", "pa_copy_pages", "pa_fork_pages", "pa_free_pages",
-    "pa_compact_pages", "pa_prefill_fp8_block",
+    "pa_compact_pages", "pa_prefill_fp8_block", "pa_decode_tree_workspace_size",
+    "pa_decode_tree_default_splits", "pa_decode_tree", "pa_verify_tree", "pa_commit_tree",
 )
 
 
@@ -127,6 +131,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_prefill_store_varlen.restype = i32
     lib.pa_prefill_store_varlen.argtypes = [P, i32, P, P, P, i64, i64, P, P, i32, i32, i32, P,
                                             P, i64, P, i32, P, i32, i32, i32, i32, f32, P, P]
+    lib.pa_decode_tree_workspace_size.restype = sz
+    lib.pa_decode_tree_workspace_size.argtypes = [i32]
+    lib.pa_decode_tree_default_splits.restype = i32
+    lib.pa_decode_tree_default_splits.argtypes = [i32]
+    lib.pa_decode_tree.restype = i32
+    lib.pa_decode_tree.argtypes = [P, i32, P, P, P, i32, i32, i32, P, P, i64, P, i32, P, i32,
+                                   i32, i32, i32, f32, i32, P, sz, u32, P]
+    lib.pa_verify_tree.restype = i32
+    lib.pa_verify_tree.argtypes = [P, P, P, P, P, P, i32, i32, i32, P, i64, P, i64, i32, P, P,
+                                   i32, P, u32, P]
+    lib.pa_commit_tree.restype = i32
+    lib.pa_commit_tree.argtypes = [P, i32, i64, P, i32, P, P, i32, P, i32, P, P, i32, P, u32, P]
     return lib
 
 
@@ -1054,6 +1070,189 @@ def compact_pages(block_tables, context_lens, ref_counts, copy_src=None, copy_ds
         out = CompactPagesCall(block_tables, context_lens, ref_counts, copy_src, copy_dst,
                                counts, remap, error_flags, pdl)(stream)
         return tuple(map(handed, out))
+
+
+def tree_workspace(num_splits: int = 0, device=None):
+    """A workspace for pa_decode_tree (its error word starts at zero)."""
+    s = num_splits
+    if s <= 0:
+        s = int(lib.pa_decode_tree_default_splits(_device_index(device)))
+    n = int(lib.pa_decode_tree_workspace_size(s))
+    if n == 0:
+        raise PagedAttentionError("bad workspace request")
+    t = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    t[:256].zero_()
+    return t
+
+
+def _need_tree(cu_seqlens, parents):
+    _need_contiguous(cu_seqlens, torch.int32, "cu_seqlens", dims=1)
+    if cu_seqlens.shape[0] < 1:
+        raise PagedAttentionError("cu_seqlens needs num_seqs + 1 entries")
+    _need_contiguous(parents, torch.int32, "parents", dims=1)
+    return cu_seqlens.shape[0] - 1, parents.shape[0]
+
+
+class DecodeTreeCall(_Prepared):
+    """A prepared pa_decode_tree (arguments as ``decode_tree``); the output
+    tensor and, if none is given, the workspace are kept with it."""
+
+    def __init__(self, q, cu_seqlens, parents, k_cache, v_cache, block_tables, context_lens,
+                 scale, max_q_len, out, num_splits=0, workspace=None, pdl=False):
+        _need_contiguous(q, torch.bfloat16, "q", dims=3)
+        T, Hq, D = q.shape
+        B, nodes = _need_tree(cu_seqlens, parents)
+        if nodes != T:
+            raise PagedAttentionError("parents needs one entry per row of q")
+        _need_contiguous(k_cache, torch.bfloat16, "k_cache", dims=4)
+        _need_contiguous(v_cache, torch.bfloat16, "v_cache", k_cache.shape)
+        NB, bs, Hkv, Dk = k_cache.shape
+        if Dk != D:
+            raise PagedAttentionError("q and the pools differ in head_dim")
+        _need_tables(block_tables, context_lens, B)
+        code = _out_code(out.dtype)
+        _need_contiguous(out, out.dtype, "out", q.shape)
+        made = ()
+        if workspace is None:
+            workspace = tree_workspace(num_splits, q.device)
+            made = (workspace,)
+        _need_contiguous(workspace, workspace.dtype, "workspace")
+        self.out, self.workspace = out, workspace
+        self._prepare(
+            lib.pa_decode_tree, "pa_decode_tree",
+            (_address(out), code, _address(q), _address(cu_seqlens), _address(parents), B, T,
+             int(max_q_len), _address(k_cache), _address(v_cache), NB, _address(block_tables),
+             block_tables.stride(0), _address(context_lens), Hq, Hkv, D, bs, float(scale),
+             int(num_splits), _address(workspace), workspace.numel() * workspace.element_size(),
+             PA_LAUNCH_PDL if pdl else 0),
+            (q, cu_seqlens, parents, k_cache, v_cache, block_tables, context_lens, out,
+             workspace), out, made)
+
+
+def decode_tree(q, cu_seqlens, parents, k_cache, v_cache, block_tables, context_lens, scale,
+                max_q_len, out=None, out_dtype=torch.bfloat16, num_splits=0, workspace=None,
+                stream=None, pdl=False):
+    """pa_decode_tree: the nodes of trees of drafted tokens, q bf16 [T, Hq, D]
+    packed by cu_seqlens (int32 [N + 1]), each attending to its sequence's
+    committed keys and to the nodes on its way to the root (parents int32 [T]:
+    indices within the sequence, -1 at a root).  The nodes' K/V are in the pools
+    already and counted in context_lens.  Returns out [T, Hq, D]."""
+    with _on(stream) as handed:
+        if out is None:
+            out = handed(torch.empty(q.shape, dtype=out_dtype, device=q.device))
+        return DecodeTreeCall(q, cu_seqlens, parents, k_cache, v_cache, block_tables,
+                              context_lens, scale, max_q_len, out, num_splits, workspace,
+                              pdl)(stream)
+
+
+def _need_probs(t, name, nodes, vocab=None):
+    _need(t, torch.float32, name, 2)
+    if t.shape[0] != nodes or (vocab is not None and t.shape[1] != vocab):
+        raise PagedAttentionError(f"{name} needs one row per node and one column per token")
+    if t.numel() and (t.shape[1] > 1 and t.stride(1) != 1 or
+                      t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise PagedAttentionError(f"{name} rows must be contiguous and apart")
+
+
+class VerifyTreeCall(_Prepared):
+    """A prepared pa_verify_tree (arguments as ``verify_tree``); ``accepted``,
+    ``path`` and ``out_tokens`` hold the results of the latest call."""
+
+    def __init__(self, tokens, parents, cu_seqlens, target_probs, uniforms, sample_uniforms,
+                 max_q_len, draft_probs=None, with_replacement=False, accepted=None, path=None,
+                 out_tokens=None, error_flags=None, pdl=False):
+        B, T = _need_tree(cu_seqlens, parents)
+        _need_contiguous(tokens, torch.int32, "tokens", (T,))
+        _need_probs(target_probs, "target_probs", T)
+        V = target_probs.shape[1]
+        if draft_probs is not None:
+            _need_probs(draft_probs, "draft_probs", T, V)
+        _need_contiguous(uniforms, torch.float32, "uniforms", (T,))
+        _need_contiguous(sample_uniforms, torch.float32, "sample_uniforms", (B,))
+        _need_error_flags(error_flags)
+        width = int(max_q_len)
+        if width < 0:
+            raise PagedAttentionError("max_q_len must not be negative")
+        given = (accepted, path, out_tokens)
+        result = tuple(
+            torch.empty(shape, dtype=torch.int32, device=tokens.device) if t is None else t
+            for t, shape in zip(given, ((B,), (B, width), (B, width))))
+        for t, name, shape in zip(result, ("accepted", "path", "out_tokens"),
+                                  ((B,), (B, width), (B, width))):
+            _need_contiguous(t, torch.int32, name, shape)
+        self.accepted, self.path, self.out_tokens = result
+        made = [t for t, was in zip(result, given) if was is None]
+        # (the stride of a single row, and of no draft, is not looked at)
+        self._prepare(
+            lib.pa_verify_tree, "pa_verify_tree",
+            (*map(_address, result), _address(tokens), _address(parents), _address(cu_seqlens),
+             B, T, width, _address(target_probs), max(V, target_probs.stride(0)),
+             _address(draft_probs), V if draft_probs is None else max(V, draft_probs.stride(0)),
+             V, _address(uniforms), _address(sample_uniforms),
+             PA_DRAWS_WITH_REPLACEMENT if with_replacement else PA_DRAWS_WITHOUT_REPLACEMENT,
+             _address(error_flags), PA_LAUNCH_PDL if pdl else 0),
+            (*result, tokens, parents, cu_seqlens, target_probs, draft_probs, uniforms,
+             sample_uniforms, error_flags), result, made)
+
+
+def verify_tree(tokens, parents, cu_seqlens, target_probs, uniforms, sample_uniforms, max_q_len,
+                draft_probs=None, with_replacement=False, accepted=None, path=None,
+                out_tokens=None, error_flags=None, stream=None, pdl=False):
+    """pa_verify_tree: which drafted nodes (tokens, parents int32 [T], packed by
+    cu_seqlens) the target's probabilities (fp32 [T, V], a row per node; rows
+    may be apart) accept, given the probabilities that they were drawn from
+    (fp32 [T, V], the row of a node that of its children; None: looked up) and
+    random numbers in [0, 1) (uniforms fp32 [T], sample_uniforms fp32 [N]).
+    Returns (accepted [N], path [N, max_q_len], out_tokens [N, max_q_len]),
+    int32."""
+    with _on(stream) as handed:
+        out = VerifyTreeCall(tokens, parents, cu_seqlens, target_probs, uniforms,
+                             sample_uniforms, max_q_len, draft_probs, with_replacement, accepted,
+                             path, out_tokens, error_flags, pdl)(stream)
+        return tuple(map(handed, out))
+
+
+class CommitTreeCall(_Prepared):
+    """A prepared pa_commit_tree (arguments as ``commit_tree``)."""
+
+    def __init__(self, pools, cu_seqlens, block_tables, context_lens, path, accepted,
+                 ref_counts=None, error_flags=None, pdl=False, block_size=16):
+        _need_contiguous(cu_seqlens, torch.int32, "cu_seqlens", dims=1)
+        B = cu_seqlens.shape[0] - 1
+        if B < 0:
+            raise PagedAttentionError("cu_seqlens needs num_seqs + 1 entries")
+        _need_tables(block_tables, context_lens, B)
+        _need_contiguous(path, torch.int32, "path", dims=2)
+        _need_contiguous(accepted, torch.int32, "accepted", (B,))
+        if path.shape[0] != B:
+            raise PagedAttentionError("path needs one row per sequence")
+        for t in pools.tensors:
+            if t.dim() < 2 or t.shape[1] != block_size:
+                raise PagedAttentionError("pools must be token-major: [num_blocks, block_size, ..]")
+        if ref_counts is not None:
+            _need_contiguous(ref_counts, torch.int32, "ref_counts", (pools.num_blocks,))
+        _need_error_flags(error_flags)
+        self.pools = pools
+        self._prepare(
+            lib.pa_commit_tree, "pa_commit_tree",
+            (ctypes.addressof(pools.array), len(pools.tensors), pools.num_blocks,
+             _address(block_tables), block_tables.stride(0), _address(context_lens),
+             _address(cu_seqlens), B, _address(path), path.shape[1], _address(accepted),
+             _address(ref_counts), block_size, _address(error_flags),
+             PA_LAUNCH_PDL if pdl else 0),
+            (*pools.tensors, block_tables, context_lens, cu_seqlens, path, accepted, ref_counts,
+             error_flags))
+
+
+def commit_tree(pools, cu_seqlens, block_tables, context_lens, path, accepted, ref_counts=None,
+                error_flags=None, stream=None, pdl=False):
+    """pa_commit_tree: in every pool of ``pools`` (a PagePools of token-major
+    pools), the rows of the accepted nodes (path int32 [N, W], accepted int32
+    [N], as verify_tree returns them) move up behind the committed keys;
+    context_lens shrinks to them, and with ref_counts (int32 [NB]) the pages that
+    are no longer needed are let go."""
+    CommitTreeCall(pools, cu_seqlens, block_tables, context_lens, path, accepted, ref_counts,
+                   error_flags, pdl)(stream)
 
 
 def decode_merge(out, workspace, context_lens, num_splits, block_size=16, stream=None):
