@@ -17,9 +17,11 @@
 //
 // A drawn token is a whole number next to a border of the running sum, so the
 // sums carry more than fp32: a weight is an unevaluated pair of floats (the
-// product's and the difference's rounding errors kept), added into a pair, and the
-// pairs of the 32 lanes are joined in fp64: some 20 fp32 operations an element,
-// against five of fp64, whose rate on this chip is a sixty-fourth.
+// product's and the difference's rounding errors kept), and pairs are added into
+// pairs, in lanes, warps and over the segments, some 20 fp32 operations an
+// element.  fp64 is for the tests of single nodes alone: its rate on this chip is
+// so low that joining lanes and segments in it took 61 us for 64 sequences of
+// 32000 tokens against 12 for one.
 //
 // Bound by latency for few sequences, and by HBM for many: a pass reads 8 bytes
 // an element.
@@ -56,19 +58,47 @@ struct VerifyParams {
   int32_t *err;
 };
 
-// A weight as hi + lo, zero unless it is positive.
+// hi + lo, with hi the sum's rounding to a float.
 struct Pair {
   float hi, lo;
 };
+__device__ __forceinline__ bool above(const Pair &a, const Pair &b) {
+  return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+}
+// The sum, within 2^-46 of it where both are positive.  The order of the two does
+// not matter.
+__device__ __forceinline__ Pair plus(const Pair &a, const Pair &b) {
+  const float s = a.hi + b.hi, bb = s - a.hi;
+  const float e = ((a.hi - (s - bb)) + (b.hi - bb)) + (a.lo + b.lo);
+  const float hi = s + e;
+  return {hi, e - (hi - s)};
+}
+__device__ __forceinline__ Pair shfl_up(const Pair &a, int by) {
+  return {__shfl_up_sync(0xffffffffu, a.hi, by), __shfl_up_sync(0xffffffffu, a.lo, by)};
+}
+__device__ __forceinline__ Pair shfl(const Pair &a, int lane) {
+  return {__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+// Sums over the lanes up to this one.
+__device__ __forceinline__ Pair warp_upto(Pair x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair y = shfl_up(x, o), z = plus(x, y);
+    if ((int)(threadIdx.x & 31) >= o) x = z;
+  }
+  return x;
+}
+
+// max(p - beta q, 0) as a pair, beta = bh + bl.
 __device__ __forceinline__ Pair weight(float p, float q, float bh, float bl) {
   const float ph = q * bh;
   const float pl = fmaf(q, bl, fmaf(q, bh, -ph));
   const float s = p - ph, bb = s - p;
-  const float e = (p - (s - bb)) - (ph + bb);  // p - ph = s + e
-  const float lo = e - pl;
-  const float hi = s + lo;  // (the pair's own rounding: |lo - (hi - s)| <= 2^-24 hi)
+  const float lo = ((p - (s - bb)) - (ph + bb)) - pl;  // p - ph = s + ...
+  const float hi = s + lo;
   return {hi > 0.f ? hi : 0.f, hi > 0.f ? lo - (hi - s) : 0.f};
 }
+// a + x without bringing hi up to date: x's low part and the error go to lo.
 __device__ __forceinline__ void add(Pair &a, const Pair &x) {
   const float s = a.hi + x.hi, bb = s - a.hi;
   a.lo += ((a.hi - (s - bb)) + (x.hi - bb)) + x.lo;
@@ -115,7 +145,7 @@ __device__ __forceinline__ void weights4(const Rows &r, const float (&p)[4], con
 
 // The sum of a warp's segment [s0, s1): a lane's four tokens of every 128.
 template <bool kVec>
-__device__ double segment_sum(const Rows &r, int s0, int s1, const uint32_t *out) {
+__device__ Pair segment_sum(const Rows &r, int s0, int s1, const uint32_t *out) {
   const int lane = threadIdx.x & 31;
   Pair acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
   constexpr int kAhead = 4;
@@ -137,53 +167,64 @@ __device__ double segment_sum(const Rows &r, int s0, int s1, const uint32_t *out
       }
     }
   }
-  double sum = 0.0;
+  Pair sum = plus(plus(acc[0], acc[1]), plus(acc[2], acc[3]));
 #pragma unroll
-  for (int k = 0; k < 4; ++k) sum += (double)acc[k].hi + (double)acc[k].lo;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int o = 16; o > 0; o >>= 1)
+    sum = plus(sum, {__shfl_xor_sync(0xffffffffu, sum.hi, o),
+                     __shfl_xor_sync(0xffffffffu, sum.lo, o)});
   return sum;
 }
 
 // The first token of segment [s0, s1) where `before` plus the running sum is over
 // `target`; its last of positive weight if there is none (-1: no such).
 template <bool kVec>
-__device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, double before,
-                            double target) {
+__device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, Pair before,
+                            const Pair &target) {
   const int lane = threadIdx.x & 31;
   int last = -1;
-  for (int b = s0; b < s1; b += 128) {
-    const int i = b + 4 * lane;
-    float p[4], q[4];
-    Pair w[4];
-    load4<kVec>(r.p, i, s1 - i, p);
-    if (r.q) load4<kVec>(r.q, i, s1 - i, q);
-    weights4(r, p, q, out, i, w);
-    double c[4], run = 0.0;
+  constexpr int kAhead = 2;
+  for (int b = s0; b < s1; b += 128 * kAhead) {
+    float p[kAhead][4], q[kAhead][4];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = b + 128 * a + 4 * lane;
+      load4<kVec>(r.p, i, s1 - i, p[a]);
+      if (r.q) load4<kVec>(r.q, i, s1 - i, q[a]);
+    }
+    Pair upto[kAhead], c[kAhead][4];
     int mine = -1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const double x = (double)w[k].hi + (double)w[k].lo;  // (0 past the end)
-      if (w[k].hi > 0.f) mine = i + k;
-      run += x;
-      c[k] = run;
-    }
-    double upto = run;  // inclusive over lanes
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = b + 128 * a + 4 * lane;
+      Pair w[4];
+      weights4(r, p[a], q[a], out, i, w);
+      c[a][0] = w[0];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
+      for (int k = 1; k < 4; ++k) c[a][k] = plus(c[a][k - 1], w[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (w[k].hi > 0.f)
+          mine = i + k;
+        else
+          c[a][k].hi = -1.f;  // (no token to draw: below any target)
+      }
+      Pair run = plus(plus(w[0], w[1]), plus(w[2], w[3]));
+      upto[a] = warp_upto(run);
     }
-    const double base = before + (upto - run);
     int found = INT_MAX;
 #pragma unroll
-    for (int k = 3; k >= 0; --k)
-      if (w[k].hi > 0.f && base + c[k] > target)
-        found = i + k;
+    for (int a = 0; a < kAhead; ++a) {
+      Pair base = shfl_up(upto[a], 1);
+      base = lane == 0 ? before : plus(before, base);
+#pragma unroll
+      for (int k = 3; k >= 0; --k)
+        if (c[a][k].hi > 0.f && above(plus(base, c[a][k]), target))
+          found = min(found, b + 128 * a + 4 * lane + k);
+      before = plus(before, shfl(upto[a], 31));
+    }
     found = __reduce_min_sync(0xffffffffu, found);
     if (found != INT_MAX) return found;
     last = max(last, __reduce_max_sync(0xffffffffu, mine));
-    before += __shfl_sync(0xffffffffu, upto, 31);
   }
   return last;
 }
@@ -193,45 +234,41 @@ __device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, 
 // next one's, and the pass after that waits for it at the barrier between.
 template <bool kVec>
 __device__ void sum_rows(cg::cluster_group &cluster, const Rows &r, const uint32_t *out, int s0,
-                         int s1, double (&mine)[2][kVfWarps], double *sums, int pass) {
+                         int s1, Pair (&mine)[2][kVfWarps], Pair *sums, int pass) {
   const int tid = threadIdx.x, warp = tid >> 5;
-  const double sum = segment_sum<kVec>(r, s0, s1, out);
+  const Pair sum = segment_sum<kVec>(r, s0, s1, out);
   if ((tid & 31) == 0) mine[pass & 1][warp] = sum;
   cluster.sync();
   if (tid < kVfSegments) {
     const int from = tid / kVfWarps;
     sums[tid] = from < (int)cluster.num_blocks()
                     ? *cluster.map_shared_rank(&mine[pass & 1][tid % kVfWarps], from)
-                    : 0.0;
+                    : Pair{0.f, 0.f};
   }
   __syncthreads();
 }
 
-// What lies up to each of the lane's four segments; returns the total.  Every
-// warp of every CTA adds in the same order.
-__device__ __forceinline__ double scan_sums(const double *sums, double (&upto)[4]) {
+// What lies before the lane's four segments and up to each of them; returns the
+// total.  Every warp of every CTA adds in the same order.
+__device__ __forceinline__ Pair scan_sums(const Pair *sums, Pair &before, Pair (&upto)[4]) {
   static_assert(kVfSegments == 128, "four segments a lane");
   const int lane = threadIdx.x & 31;
-  double run = 0.0;
+  upto[0] = sums[4 * lane];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) upto[k] = run += sums[4 * lane + k];
-  double x = run;
+  for (int k = 1; k < 4; ++k) upto[k] = plus(upto[k - 1], sums[4 * lane + k]);
+  before = shfl_up(warp_upto(upto[3]), 1);
+  if (lane == 0) before = {0.f, 0.f};
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) upto[k] += x - run;
-  return __shfl_sync(0xffffffffu, upto[3], 31);
+  for (int k = 0; k < 4; ++k) upto[k] = plus(before, upto[k]);
+  return shfl(upto[3], 31);
 }
 
 template <bool kVec>
-__global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParams p) {
   __shared__ int n_par[kVfNodes], n_tok[kVfNodes];
   __shared__ float n_u[kVfNodes], n_p[kVfNodes], n_q[kVfNodes];
-  __shared__ double mine[2][kVfWarps];  // this CTA's segment sums, of alternate passes
-  __shared__ double sums[kVfSegments];  // all CTAs', of the last pass
+  __shared__ Pair mine[2][kVfWarps];  // this CTA's segment sums, of alternate passes
+  __shared__ Pair sums[kVfSegments];  // all CTAs', of the last pass
   __shared__ double s_beta;
   __shared__ int s_cur, s_act, s_next, s_count;
   extern __shared__ uint32_t out_bits[];  // looked-up guesses rejected at this node
@@ -306,11 +343,14 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
       const bool last = s_act == kSum;
       sum_rows<kVec>(cluster, r, looked ? out_bits : nullptr, s0, s1, mine, sums, passes++);
       if (last) break;
-      double upto[4];
-      mass = scan_sums(sums, upto);
-      summed = true;
     }
     if (warp == 0) {
+      if (s_act == kPass) {
+        Pair before, upto[4];
+        const Pair total = scan_sums(sums, before, upto);
+        mass = (double)total.hi + (double)total.lo;
+        summed = true;
+      }
       int act = kLoad;
       while (true) {
         if (at + 1 >= nodes) {
@@ -346,10 +386,12 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
             dirty = true;
           }
         } else {
-          const double left = fmax(1.0 - gone, kVfLeast), qx = (double)n_q[j];
-          ok = (double)n_u[j] * (qx / left) * mass < fma(-beta, qx, (double)n_p[j]);
+          // (the first child of a node: u q < p, exact)
+          const double left = gone == 0.0 ? 1.0 : fmax(1.0 - gone, kVfLeast);
+          const double qx = (double)n_q[j];
+          ok = (double)n_u[j] * qx * mass < left * fma(-beta, qx, (double)n_p[j]);
           if (!ok) {
-            beta += mass / left;
+            beta += gone == 0.0 ? mass : mass / left;
             if (!p.again) gone += qx;
             act = kPass;
             break;
@@ -391,33 +433,33 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VerifyParams p
   Rows r{p.p + row * p.p_stride, looked || s_beta == 0.0 ? nullptr : p.q + row * p.q_stride, bh,
          bl};
   const uint32_t *out = looked ? out_bits : nullptr;
-  double upto[4], total = scan_sums(sums, upto);
-  if (!(total > 0.0)) {  // nothing left, by rounding alone: the target's row
-    __syncthreads();     // all warps have read `sums`
+  Pair before, upto[4], total = scan_sums(sums, before, upto);
+  if (!(total.hi > 0.f)) {  // nothing left, by rounding alone: the target's row
+    __syncthreads();        // all warps have read `sums`
     r.q = nullptr;
     out = nullptr;
     sum_rows<kVec>(cluster, r, out, s0, s1, mine, sums, passes++);
-    total = scan_sums(sums, upto);
+    total = scan_sums(sums, before, upto);
   }
-  const double target = (double)p.u_last[seq] * total;
-  const double before0 = __shfl_up_sync(0xffffffffu, upto[3], 1);
+  const float ul = p.u_last[seq], th = ul * total.hi;  // u' times the total
+  const float tl = fmaf(ul, total.hi, -th) + ul * total.lo, t2 = th + tl;
+  const Pair target = {t2, tl - (t2 - th)};
   int seg = INT_MAX, filled = -1;
 #pragma unroll
   for (int k = 3; k >= 0; --k) {
-    if (sums[4 * lane + k] > 0.0) {
+    if (sums[4 * lane + k].hi > 0.f) {
       filled = max(filled, 4 * lane + k);
-      if (upto[k] > target) seg = 4 * lane + k;
+      if (above(upto[k], target)) seg = 4 * lane + k;
     }
   }
   seg = __reduce_min_sync(0xffffffffu, seg);
   filled = __reduce_max_sync(0xffffffffu, filled);
   if (seg == INT_MAX) seg = filled;  // -1: no weight at all
   if (seg == rank * kVfWarps + warp) {
-    const double pick0 = (seg & 3) == 0 ? before0 : (seg & 3) == 1 ? upto[0] : (seg & 3) == 2
-                                                                          ? upto[1] : upto[2];
-    double before = __shfl_sync(0xffffffffu, pick0, seg >> 2);
-    if (seg == 0) before = 0.0;
-    const int tok = segment_find<kVec>(r, s0, s1, out, before, target);
+    const int k = seg & 3;
+    const Pair at0 = shfl(k == 0 ? before : k == 1 ? upto[0] : k == 2 ? upto[1] : upto[2],
+                          seg >> 2);
+    const int tok = segment_find<kVec>(r, s0, s1, out, at0, target);
     if (lane == 0) toks[count - 1] = tok;
   }
   if (first) {
