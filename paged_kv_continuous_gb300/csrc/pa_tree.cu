@@ -39,29 +39,51 @@ constexpr int kTrPages = kPfKeys / kBlockSize;  // pages per KV tile
 constexpr int kTrHalf = kPfKeys * 128;          // 64 keys x 64 dims, 128-byte swizzle
 constexpr int kTrTile = 2 * kTrHalf;            // one K or V tile
 constexpr int kTrQHalf = kPfRows * 128;         // 128 rows x 64 dims of Q
-constexpr int kTrStages = 2;
+// K is needed a step before V of the same tile, and a loaded memory system takes
+// longer than a step: three K stages and two V stages, all the shared memory that
+// leaves room for two CTAs on an SM (so nothing is declared static).
+#ifndef TR_KST
+#define TR_KST 3
+#endif
+constexpr int kTrKStages = TR_KST, kTrVStages = 2;
 constexpr int kTrOffQ = 0;
 constexpr int kTrOffK = kTrOffQ + 2 * kTrQHalf;
-constexpr int kTrOffV = kTrOffK + kTrStages * kTrTile;
-constexpr int kTrOffBar = kTrOffV + kTrStages * kTrTile;
+constexpr int kTrOffV = kTrOffK + kTrKStages * kTrTile;
+constexpr int kTrOffBar = kTrOffV + kTrVStages * kTrTile;
 // 8-byte slots: K full / empty and V full / empty per stage, Q, two score, two
 // P and two PV barriers, the TMEM address, the abort flag, the last piece with
-// a V row that is not finite
-constexpr int kTsKFull = 0, kTsKEmpty = kTsKFull + kTrStages, kTsVFull = kTsKEmpty + kTrStages;
-constexpr int kTsVEmpty = kTsVFull + kTrStages, kTsQ = kTsVEmpty + kTrStages, kTsS = kTsQ + 1;
+// a V row that is not finite, the sums of the plan's scan, the CTA's place
+constexpr int kTsKFull = 0, kTsKEmpty = kTsKFull + kTrKStages, kTsVFull = kTsKEmpty + kTrKStages;
+constexpr int kTsVEmpty = kTsVFull + kTrVStages, kTsQ = kTsVEmpty + kTrVStages, kTsS = kTsQ + 1;
 constexpr int kTsP = kTsS + 2, kTsO = kTsP + 2, kTsTmem = kTsO + 2, kTsAbort = kTsTmem + 1;
-constexpr int kTsBad = kTsAbort + 1, kTsSlots = 32;
-static_assert(kTsBad < kTsSlots, "barrier slots do not fit");
-constexpr int kTrSmem = 1024 + kTrOffBar + kTsSlots * 8;
+constexpr int kTsBad = kTsAbort + 1, kTsSum = kTsBad + 1, kTsPlace = kTsSum + kTrThreads / 32;
+constexpr int kTsSlots = 48;
+constexpr int kTrSmem = kTrOffBar + kTsSlots * 8;
 static_assert(2 * (kTrSmem + 1024) <= 228 * 1024, "two CTAs do not fit an SM");
 constexpr int kTrCols = 256;    // tensor memory columns: S_0 0.., S_1 64.., O 128..
 constexpr int kTrSCols = 64, kTrO = 128;
 
+#ifndef TR_PIECE
+#define TR_PIECE 2
+#endif
+#ifndef TR_MIN
+#define TR_MIN 4
+#endif
 // A piece's start and end cost about as much as this many tiles.
-constexpr int kTrPieceTiles = 2;
-// CTAs in use: none is given less than this many tiles.
-constexpr int kTrMinTiles = 4;
+constexpr int kTrPieceTiles = TR_PIECE;
+// A CTA's part of the list is at least this long.
+constexpr int kTrMinPart = TR_MIN;
 
+// What the merge has to know of CTA c's first piece, where it goes on with a unit
+// that an earlier CTA began: the unit's rows, CTAs first .. last and output rows.
+struct TreeCut {
+  int rows, first, last;  // rows 0: the CTA starts with a unit's first tile
+  int q0, g, mt, unused[2];
+};
+
+#ifndef TR_X
+#define TR_X
+#endif
 struct TreeParams {
   void *out;
   int out_f32;
@@ -74,10 +96,12 @@ struct TreeParams {
   long long bt_stride;
   const int32_t *ctx;
   int hq, hkv, group;
+  uint32_t group_inv;     // ceil(2^32 / group): x / group = umulhi(x, group_inv) (x < 2^29)
   float scale_log2;       // > 0: a scale <= 0 is folded into q as staged
   uint32_t q_and, q_xor;  // staged q pairs = (q & q_and) ^ q_xor
   int splits;             // CTAs of the launch
-  int all_splits;         // use them all
+  int min_part;
+  TreeCut *cuts;          // [splits]
   float *part_o;          // [2][splits][128 rows][128]
   float *part_lse;        // [2][splits][128]
   int32_t *err;
@@ -106,36 +130,36 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s, bool tel
   return r;
 }
 
-// Tiles of row tile mt: up to the key of its last node.
-__device__ __forceinline__ int unit_tiles(const TreeSeq &q, int group, int mt) {
-  const int last = (min((mt + 1) * kPfRows, q.nodes * group) - 1) / group;
-  return (q.keys - q.nodes + last) / kPfKeys + 1;
+__device__ __forceinline__ int by_group(const TreeParams &p, int x) {
+  return p.group == 1 ? x : (int)__umulhi((uint32_t)x, p.group_inv);
 }
-__device__ __forceinline__ int row_tiles(const TreeSeq &q, int group) {
-  return (q.nodes * group + kPfRows - 1) / kPfRows;
+// Tiles of row tile mt: up to the key of its last node.
+__device__ __forceinline__ int unit_tiles(const TreeParams &p, const TreeSeq &q, int mt) {
+  const int last = by_group(p, min((mt + 1) * kPfRows, q.nodes * p.group) - 1);
+  return (int)((unsigned)(q.keys - q.nodes + last) / kPfKeys) + 1;
+}
+__device__ __forceinline__ int row_tiles(const TreeParams &p, const TreeSeq &q) {
+  return (int)((unsigned)(q.nodes * p.group + kPfRows - 1) / kPfRows);
 }
 // Length of one kv head of the sequence in the list.
-__device__ __forceinline__ long long head_weight(const TreeSeq &q, int group) {
+__device__ __forceinline__ long long head_weight(const TreeParams &p, const TreeSeq &q) {
   long long w = 0;
-  const int m = row_tiles(q, group);
-  for (int i = 0; i < m; ++i) w += unit_tiles(q, group, i) + kTrPieceTiles;
+  const int m = row_tiles(p, q);
+  for (int i = 0; i < m; ++i) w += unit_tiles(p, q, i) + kTrPieceTiles;
   return w;
 }
 
-__device__ __forceinline__ long long ctas_in_use(const TreeParams &p, long long N) {
-  if (N == 0) return 0;
-  const long long most = p.all_splits ? N : N / (kTrMinTiles + kTrPieceTiles);
-  return max(1ll, min((long long)p.splits, most));
+// The list is cut into parts of this length, one for a CTA, while it lasts.
+__device__ __forceinline__ long long part_length(const TreeParams &p, long long N) {
+  const long long len = N < (1ll << 31) ? ((unsigned)N + (unsigned)p.splits - 1u) / (unsigned)p.splits
+                                        : (N + p.splits - 1) / p.splits;
+  return max((long long)p.min_part, len);
 }
-__device__ __forceinline__ long long cta_begin(long long c, long long C, long long N) {
-  return c * N / C;
-}
-// The CTA that holds place x: the largest c with cta_begin(c) <= x (C <= N).
-__device__ __forceinline__ long long cta_of(long long x, long long C, long long N) {
-  return ((x + 1) * C - 1) / N;
+__device__ __forceinline__ int part_of(long long x, long long len) {
+  return x < (1ll << 31) && len < (1ll << 31) ? (int)((unsigned)x / (unsigned)len) : (int)(x / len);
 }
 
-// Sums of a long long over the block: the total, and what lies before this thread.
+// What lies before this thread's share of the list, and the whole.
 __device__ __forceinline__ long long block_before(long long v, long long *warp_sum,
                                                   long long &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -149,7 +173,8 @@ __device__ __forceinline__ long long block_before(long long v, long long *warp_s
   __syncthreads();
   long long before = x - v;
   total = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+#pragma unroll
+  for (int w = 0; w < kTrThreads / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
@@ -160,7 +185,9 @@ __device__ __forceinline__ long long block_before(long long v, long long *warp_s
 struct TreePlace {
   long long x, end, start;
   int s, g, mt;
+  TreeSeq q;
 };
+static_assert(sizeof(TreePlace) <= (kTsSlots - kTsPlace) * 8, "the place does not fit");
 
 struct TreePiece {
   TreeSeq q;
@@ -170,19 +197,14 @@ struct TreePiece {
 // The next piece of a CTA's part of the list; every warp runs this for itself.
 struct TreeWalk {
   TreePlace at;
-  TreeSeq q;
 
-  __device__ __forceinline__ void begin(const TreeParams &p, const TreePlace &place) {
-    at = place;
-    q = tree_seq(p, at.s, false);
-  }
   __device__ __forceinline__ bool next(const TreeParams &p, TreePiece &r) {
     while (at.x < at.end) {
-      const int tiles = unit_tiles(q, p.group, at.mt);
+      const int tiles = unit_tiles(p, at.q, at.mt);
       const long long rel = at.x - at.start;
       const bool got = rel < tiles;
       if (got) {
-        r.q = q;
+        r.q = at.q;
         r.s = at.s;
         r.g = at.g;
         r.mt = at.mt;
@@ -192,13 +214,13 @@ struct TreeWalk {
       }
       at.start += tiles + kTrPieceTiles;
       at.x = at.start;
-      if (++at.mt == row_tiles(q, p.group)) {
+      if (++at.mt == row_tiles(p, at.q)) {
         at.mt = 0;
         if (++at.g == p.hkv) {
           at.g = 0;
           if (at.x < at.end) do {
-              q = tree_seq(p, ++at.s, false);
-            } while (q.nodes == 0 && at.s + 1 < p.num_seqs);
+              at.q = tree_seq(p, ++at.s, false);
+            } while (at.q.nodes == 0 && at.s + 1 < p.num_seqs);
         }
       }
       if (got) return true;
@@ -207,42 +229,51 @@ struct TreeWalk {
   }
 };
 
-// Finds the place of list position x0 (one thread of the block holds it) and the
-// list's length.
-__device__ __forceinline__ void tree_plan(const TreeParams &p, long long c, long long *warp_sum,
-                                          TreePlace *place, long long &C, bool tell) {
-  const int per = (p.num_seqs + (int)blockDim.x - 1) / (int)blockDim.x;
+// The CTA's part of the list: the thread whose sequences hold its start leaves the
+// place there.  False: nothing to do.
+__device__ __forceinline__ bool tree_plan(const TreeParams &p, long long *warp_sum,
+                                          TreePlace *place, long long &len) {
+  const int per = (int)((unsigned)p.num_seqs + kTrThreads - 1u) / kTrThreads;
   const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
   long long mine = 0, N;
-  for (int s = s0; s < s1; ++s)
-    mine += head_weight(tree_seq(p, s, tell), p.group) * p.hkv;
-  long long before = block_before(mine, warp_sum, N);
-  C = ctas_in_use(p, N);
-  if (c >= C) return;
-  const long long x0 = cta_begin(c, C, N);
-  if (x0 < before || x0 >= before + mine) return;
+  TreeSeq q = {0, 0, 0};
   for (int s = s0; s < s1; ++s) {
-    const TreeSeq q = tree_seq(p, s, false);
-    const long long w = head_weight(q, p.group);
+    q = tree_seq(p, s, blockIdx.x == 0);
+    mine += head_weight(p, q) * p.hkv;
+  }
+  long long before = block_before(mine, warp_sum, N);
+  len = part_length(p, N);
+  const long long x0 = (long long)blockIdx.x * len;
+  if (x0 >= N) return false;
+  if (x0 < before || x0 >= before + mine) return true;
+  for (int s = s0; s < s1; ++s) {
+    if (per > 1) q = tree_seq(p, s, false);
+    const long long w = head_weight(p, q);
     if (x0 < before + w * p.hkv) {
       TreePlace r;
       r.x = x0;
-      r.end = cta_begin(c + 1, C, N);
+      r.end = min(N, x0 + len);
       r.s = s;
-      r.g = (int)((x0 - before) / w);
-      r.start = before + r.g * w;
+      r.q = q;
+      r.g = 0;
+      r.start = before;
+      while (x0 >= r.start + w) {
+        r.start += w;
+        ++r.g;
+      }
       r.mt = 0;
       while (true) {
-        const int len = unit_tiles(q, p.group, r.mt) + kTrPieceTiles;
-        if (x0 < r.start + len) break;
-        r.start += len;
+        const int unit = unit_tiles(p, q, r.mt) + kTrPieceTiles;
+        if (x0 < r.start + unit) break;
+        r.start += unit;
         ++r.mt;
       }
       *place = r;
-      return;
+      break;
     }
     before += w * p.hkv;
   }
+  return true;
 }
 
 // ---- attention ----------------------------------------------------------------
@@ -275,9 +306,7 @@ __device__ __noinline__ uint32_t not_finite(const TreeParams &p, int s, int q0, 
 __global__ void __launch_bounds__(kTrThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_addr(smem);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kTrOffBar);
   const uint32_t b_k_full = smem_addr(bars + kTsKFull), b_k_empty = smem_addr(bars + kTsKEmpty);
@@ -287,15 +316,17 @@ __global__ void __launch_bounds__(kTrThreads, 2)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kTsTmem);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kTsAbort);
   volatile int *bad_piece = reinterpret_cast<volatile int *>(bars + kTsBad);
-  __shared__ long long warp_sum[kTrThreads / 32];
-  __shared__ TreePlace place;
+  long long *warp_sum = reinterpret_cast<long long *>(bars + kTsSum);
+  TreePlace *place = reinterpret_cast<TreePlace *>(bars + kTsPlace);
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
-    for (int i = 0; i < kTrStages; ++i) {
+    for (int i = 0; i < kTrKStages; ++i) {
       mbar_init(b_k_full + 8 * i, 1);
       mbar_init(b_k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kTrVStages; ++i) {
       mbar_init(b_v_full + 8 * i, 1);
       mbar_init(b_v_empty + 8 * i, 1);
     }
@@ -311,58 +342,85 @@ __global__ void __launch_bounds__(kTrThreads, 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
   }
-  griddep_wait();
-  griddep_launch_dependents();
-  long long C;
-  tree_plan(p, blockIdx.x, warp_sum, &place, C, blockIdx.x == 0);
-  if ((long long)blockIdx.x >= C) return;
   if (warp == 1) {
+    // (another kernel's CTAs on this SM may hold it: this waits until they end)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
                  "r"(kTrCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  griddep_wait();
+  griddep_launch_dependents();
+  long long len;
+  const bool busy = tree_plan(p, warp_sum, place, len) && (base & 1023) == 0;
+  // (the swizzle needs it; without static shared memory the base is aligned)
+  if ((base & 1023) != 0 && tid == 0) report(p.err, PA_DEVERR_WAIT_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_o = tmem + kTrO;
+  TreeWalk walk;
+  if (busy)
+    walk.at = *place;
+  else
+    walk.at.x = walk.at.end = walk.at.start = 0;
+  if (tid == 96) {
+    TreeCut cut = {};
+    const long long rel = walk.at.x - walk.at.start;
+    const int tiles = busy ? unit_tiles(p, walk.at.q, walk.at.mt) : 0;
+    if (busy && rel > 0 && rel < tiles) {
+      cut.rows = min(kPfRows, walk.at.q.nodes * p.group - walk.at.mt * kPfRows);
+      cut.first = part_of(walk.at.start, len);
+      cut.last = part_of(walk.at.start + tiles - 1, len);
+      cut.q0 = walk.at.q.q0;
+      cut.g = walk.at.g;
+      cut.mt = walk.at.mt;
+    }
+    p.cuts[blockIdx.x] = cut;
+  }
+  __syncwarp();
   constexpr unsigned kAll = 0xffffffffu;
 
-  TreeWalk walk;
   TreePiece u;
-  walk.begin(p, place);
-  // tiles done so far, over all pieces: their stage is it % 2, their score buffer too
-  int it = 0;
+  int it = 0;  // tiles done so far, over all pieces; tile it's scores are in buffer it % 2
 
   if (warp == 0 || warp == 2) {
-    // ---- loaders: a tile's pages (64 dims x 16 keys a box) into stage it % 2
+    // ---- loaders: a tile's pages (64 dims x 16 keys a box) into the next stage
     //      once the MMAs that read its previous tile are done
     const bool is_k = warp == 0;
     const CUtensorMap *map = is_k ? &tmap_k : &tmap_v;
     const uint32_t dst0 = base + (is_k ? kTrOffK : kTrOffV);
     const uint32_t full0 = is_k ? b_k_full : b_v_full, empty0 = is_k ? b_k_empty : b_v_empty;
+    const int stages = is_k ? kTrKStages : kTrVStages;
+    constexpr int kChunk = 32 / kTrPages;  // tiles whose table entries a warp holds
+    int st = 0, par = 0;                   // stage, and the parity of its round
     bool ok = true;
     while (ok && walk.next(p, u)) {
       const int32_t *row = p.tables + (long long)u.s * p.bt_stride;
-      // table entries of eight tiles, one per lane: -1 no key in the page
-      // (left as it is: masked), -2 a bad entry
-      int ph_lane = -1;
+      // an entry per lane, and those of the next eight tiles on their way: -1 no
+      // key in the page (left as it is: masked), -2 a bad entry
+      auto entry = [&](int chunk) {
+        const long long page = (long long)chunk * 32 + lane;
+        const bool has = chunk >= 0 && page * kBlockSize < u.q.keys;
+        const int ph = has ? row[page] : -1;
+        return !has ? -1 : ph >= 0 && ph < p.num_blocks ? ph : -2;
+      };
+      int chunk = (u.t1 - 1) / kChunk;
+      int ph_lane = entry(chunk), ph_next = entry(chunk - 1);
       for (int j = u.t1 - 1; j >= u.t0; --j, ++it) {
-        const int st = it % kTrStages, round = it / kTrStages;
-        if (j == u.t1 - 1 || j % (32 / kTrPages) == 32 / kTrPages - 1) {
-          const long long page = (long long)(j / (32 / kTrPages)) * 32 + lane;
-          const bool has = page * kBlockSize < u.q.keys;
-          const int ph = has ? row[page] : -1;
-          ph_lane = !has ? -1 : ph >= 0 && ph < p.num_blocks ? ph : -2;
+        if (j / kChunk != chunk) {
+          --chunk;
+          ph_lane = ph_next;
+          ph_next = entry(chunk - 1);
         }
-        if (round > 0 &&
-            !__all_sync(kAll, mbar_wait(empty0 + 8 * st, (round - 1) & 1, abort_flag, p.err))) {
+        if (it >= stages &&
+            !__all_sync(kAll, mbar_wait(empty0 + 8 * st, par ^ 1, abort_flag, p.err))) {
           ok = false;
           break;
         }
-        const int at = (j % (32 / kTrPages)) * kTrPages;
+        const int at = (j % kChunk) * kTrPages;
         const int phys = __shfl_sync(kAll, ph_lane, at + lane % kTrPages);
         const unsigned okm = __ballot_sync(kAll, lane < kTrPages && phys >= 0);
         if (__any_sync(kAll, phys == -2) && lane == 0) report(p.err, PA_DEVERR_BLOCK_INDEX);
@@ -378,13 +436,14 @@ __global__ void __launch_bounds__(kTrThreads, 2)
             tma_load_3d(dst0 + st * kTrTile + h * kTrHalf + pg * kBlockSize * 128, map, h * 64,
                         u.g, z, full);
         }
+        if (++st == stages) st = 0, par ^= 1;
       }
     }
     if (lane == 0 && *abort_flag) {
       // copies in flight must land before the CTA's shared memory is released
       volatile int never = 0;
-      for (int i = it > kTrStages ? it - kTrStages : 0; i < it; ++i)
-        mbar_wait(full0 + 8 * (i % kTrStages), (i / kTrStages) & 1, &never, nullptr);
+      for (int i = it > stages ? it - stages : 0; i < it; ++i)
+        mbar_wait(full0 + 8 * (i % stages), (i / stages) & 1, &never, nullptr);
     }
     __syncwarp();
   } else if (warp == 1 || warp == 3) {
@@ -393,7 +452,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
     //      3: O (+)= (P_hi + P_lo) V
     constexpr uint32_t idesc_qk = umma_idesc(0, kPfKeys), idesc_pv = umma_idesc(1, kHeadDim);
     uint32_t last_bar = 0;
-    int last_par = 0, piece = 0;
+    int last_par = 0, piece = 0, st = 0, ph = 0;  // (of this warp's operand)
     bool ok = true;
     while (ok && walk.next(p, u)) {
       if (warp == 1) {
@@ -402,7 +461,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       }
       const int n = u.t1 - u.t0;
       for (int j = 0; j < n && ok; ++j, ++it) {
-        const int st = it % kTrStages, ph = (it / kTrStages) & 1, buf = it & 1;
+        const int buf = it & 1;
         if (warp == 1) {
           ok = __all_sync(kAll, mbar_wait(b_k_full + 8 * st, ph, abort_flag, p.err));
           if (ok && it >= 2)
@@ -421,6 +480,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           umma_commit(b_s + 8 * buf);
           umma_commit(b_k_empty + 8 * st);
           last_bar = b_s + 8 * buf;
+          if (++st == kTrKStages) st = 0, ph ^= 1;
         } else {
           ok = __all_sync(kAll, mbar_wait(b_p + 8 * buf, (it >> 1) & 1, abort_flag, p.err));
           if (ok) ok = __all_sync(kAll, mbar_wait(b_v_full + 8 * st, ph, abort_flag, p.err));
@@ -437,6 +497,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           umma_commit(b_o + 8 * buf);
           umma_commit(b_v_empty + 8 * st);
           last_bar = b_o + 8 * buf;
+          if (++st == kTrVStages) st = 0, ph ^= 1;
         }
         last_par = (it >> 1) & 1;
       }
@@ -456,65 +517,79 @@ __global__ void __launch_bounds__(kTrThreads, 2)
     bool ok = true;
     int piece = 0;
     while (ok && walk.next(p, u)) {
-      const int R = u.mt * kPfRows + r;
-      const bool valid = R < u.q.nodes * p.group;
-      const bool alive = u.mt * kPfRows + lb < u.q.nodes * p.group;  // any row of the warp
-      const int node = R / p.group;
+      const int R = u.mt * kPfRows + r, limit = u.q.nodes * p.group;
+      const bool valid = R < limit;
+      const bool alive = u.mt * kPfRows + lb < limit;  // any row of the warp
+      const int node = by_group(p, R);
       const int done = u.q.keys - u.q.nodes;
-      const long long head_row =
-          (long long)(u.q.q0 + node) * p.hq + u.g * p.group + R % p.group;
-      // Q rows into the layout the TMA gives K tiles
-      {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + head_row * kHeadDim);
+      // row R of the tile is this row of q and out
+      auto head_row = [&](int x) {
+        const int n = by_group(p, x);
+        return (long long)(u.q.q0 + n) * p.hq + u.g * p.group + (x - n * p.group);
+      };
+      // Q rows, half a warp a row, into the layout the TMA gives K tiles
+      if (alive) {
         uint4 qv[16];
+        const int ch = lane & 15;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          qv[i] = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-          qv[i].x = (qv[i].x & p.q_and) ^ p.q_xor;
-          qv[i].y = (qv[i].y & p.q_and) ^ p.q_xor;
-          qv[i].z = (qv[i].z & p.q_and) ^ p.q_xor;
-          qv[i].w = (qv[i].w & p.q_and) ^ p.q_xor;
+          const int x = u.mt * kPfRows + lb + 2 * i + (lane >> 4);
+          qv[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (x < limit) qv[i] = reinterpret_cast<const uint4 *>(p.q + head_row(x) * kHeadDim)[ch];
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const uint32_t a = base + kTrOffQ + (i >> 3) * kTrQHalf + sw128(r, i & 7);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(qv[i].x),
-                       "r"(qv[i].y), "r"(qv[i].z), "r"(qv[i].w)
+          const uint32_t a = base + kTrOffQ + (ch >> 3) * kTrQHalf +
+                             sw128(lb + 2 * i + (lane >> 4), ch & 7);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
+                       "r"((qv[i].x & p.q_and) ^ p.q_xor), "r"((qv[i].y & p.q_and) ^ p.q_xor),
+                       "r"((qv[i].z & p.q_and) ^ p.q_xor), "r"((qv[i].w & p.q_and) ^ p.q_xor)
                        : "memory");
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(b_q);
       }
+      mbar_arrive(b_q);
       // m: the reference of this row's exponentials (base 2); it moves only when
       // a tile's largest exceeds it by more than 8, so P <= 256 and O is rescaled
       // rarely.  l: the row's sum.  up: the next node of the walk to the root.
       float m = -INFINITY, l = 0.f;
+      // A tile's 64 keys are a window of 64 nodes, whose parents the warp holds,
+      // two a lane: a step of the walk is a shuffle.
       int up = valid ? node : -1;
       const int32_t *par = p.parents + u.q.q0;
+      auto climb = [&](int first, uint32_t (&vis)[2]) {  // window first .. first + 63
+        const int n0 = first + lane, n1 = n0 + 32;
+        const int par0 = n0 >= 0 && n0 < u.q.nodes ? par[n0] : -1;
+        const int par1 = n1 >= 0 && n1 < u.q.nodes ? par[n1] : -1;
+        while (__any_sync(kAll, up >= 0 && up >= first)) {
+          const int k = up - first;
+          const int next0 = __shfl_sync(kAll, par0, k & 31), next1 = __shfl_sync(kAll, par1, k & 31);
+          if (up < 0 || k < 0) continue;
+          if (k < 32)
+            vis[0] |= 1u << k;
+          else
+            vis[1] |= 1u << (k - 32);
+          const int next = k < 32 ? next0 : next1;
+          if (next >= up || next < -1) report(p.err, PA_DEVERR_SHAPE);
+          up = next < up && next >= -1 ? next : -1;
+        }
+      };
+      if (alive && u.t1 * kPfKeys > done) {  // the windows above the piece's last tile
+        uint32_t unused[2] = {0u, 0u};
+        const int top = by_group(p, min(u.mt * kPfRows + lb + 31, limit - 1));
+        for (int j = (done + top) / kPfKeys; j >= u.t1; --j) climb(j * kPfKeys - done, unused);
+      }
       for (int j = u.t1 - 1; j >= u.t0 && ok; --j, ++it) {
-        const int st = it % kTrStages, buf = it & 1;
+        const int st = it % kTrVStages, buf = it & 1;
         const int key0 = j * kPfKeys;
         const bool in_tree = key0 > done - kPfKeys;  // the tile holds drafted nodes
         uint32_t vis[2] = {0u, 0u};
-        if (in_tree) {
+        if (in_tree && alive) {
+          climb(key0 - done, vis);
           if (valid && key0 < done) {
             const int below = done - key0;  // 1 .. 63 committed keys
-            vis[0] = below >= 32 ? 0xffffffffu : (1u << below) - 1u;
-            vis[1] = below > 32 ? (1u << (below - 32)) - 1u : 0u;
-          }
-          while (up >= 0 && done + up >= key0) {
-            const int k = done + up - key0;
-            if (k < 32)
-              vis[0] |= 1u << k;
-            else if (k < 64)
-              vis[1] |= 1u << (k - 32);
-            const int next = par[up];
-            if (next >= up || next < -1) {
-              report(p.err, PA_DEVERR_SHAPE);
-              up = -1;
-            } else {
-              up = next;
-            }
+            vis[0] |= below >= 32 ? 0xffffffffu : (1u << below) - 1u;
+            vis[1] |= below > 32 ? (1u << (below - 32)) - 1u : 0u;
           }
         }
         ok = __all_sync(kAll, mbar_wait(b_s + 8 * buf, (it >> 1) & 1, abort_flag, p.err));
@@ -607,7 +682,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         // hold anything and are cleared; a drafted node's infinities and NaN are
         // cleared here and put into the rows that see it at the end
         if (in_tree) {
-          ok = __all_sync(kAll, mbar_wait(b_v_full + 8 * st, (it / kTrStages) & 1, abort_flag,
+          ok = __all_sync(kAll, mbar_wait(b_v_full + 8 * st, (it / kTrVStages) & 1, abort_flag,
                                           p.err));
           if (!ok) break;
           const uint32_t vb = base + kTrOffV + st * kTrTile;
@@ -646,43 +721,57 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         const bool bad = *bad_piece == piece;
         const bool whole = u.t0 == 0 && u.t1 == u.tiles;
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (l NaN: a NaN row)
-        const long long slot = ((u.t0 > 0 ? 0 : (long long)p.splits) + blockIdx.x) * kPfRows + r;
-        float *dst32 = whole ? static_cast<float *>(p.out) + head_row * kHeadDim
-                             : p.part_o + slot * kHeadDim;
-        uint16_t *dst16 = static_cast<uint16_t *>(p.out) + head_row * kHeadDim;
+        const long long slot = ((u.t0 > 0 ? 0 : (long long)p.splits) + blockIdx.x) * kPfRows + lb;
+        // 32 columns of the warp's rows at a time go through its own Q rows (which
+        // no MMA reads any more), so that eight lanes store a row's 128 bytes
+        const uint32_t stage = base + kTrOffQ + lb * 128;
+        const int x0 = lane >> 3, col = 4 * (lane & 7);
+        char *dst[8];  // of rows x0 + 4 i; null: no such row
+        const bool narrow = whole && !p.out_f32;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = u.mt * kPfRows + lb + x0 + 4 * i;
+          const long long at = whole ? head_row(x) : slot + x0 + 4 * i;
+          dst[i] = static_cast<char *>(whole ? p.out : static_cast<void *>(p.part_o)) +
+                   (at * kHeadDim + col) * (narrow ? 2 : 4);
+          if (x >= limit) dst[i] = nullptr;
+        }
 #pragma unroll 1
         for (int cc = 0; cc < kHeadDim / 32; ++cc) {
           float ov[32];
           tmem_ld32(tmem_o + trow + cc * 32, ov);
+          if (valid && bad TR_X) {
+            const uint32_t dims = not_finite(p, u.s, u.q.q0, done, u.g, node, u.t0 * kPfKeys,
+                                             u.t1 * kPfKeys - 1, cc);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] *= inv;
-          if (valid) {
-            if (bad) {
-              const uint32_t dims = not_finite(p, u.s, u.q.q0, done, u.g, node, u.t0 * kPfKeys,
-                                               u.t1 * kPfKeys - 1, cc);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if ((dims >> i) & 1u) ov[i] = __int_as_float(0x7fffffff);
-            }
-            if (whole && !p.out_f32) {
-              uint4 *dst = reinterpret_cast<uint4 *>(dst16 + cc * 32);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(float2_to_bf16x2(ov[8 * i], ov[8 * i + 1]),
-                                    float2_to_bf16x2(ov[8 * i + 2], ov[8 * i + 3]),
-                                    float2_to_bf16x2(ov[8 * i + 4], ov[8 * i + 5]),
-                                    float2_to_bf16x2(ov[8 * i + 6], ov[8 * i + 7]));
-            } else {
-              float4 *dst = reinterpret_cast<float4 *>(dst32 + cc * 32);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-            }
+            for (int i = 0; i < 32; ++i)
+              if ((dims >> i) & 1u) ov[i] = __int_as_float(0x7fffffff);
           }
           __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + sw128(lane, i)),
+                         "f"(ov[4 * i] * inv), "f"(ov[4 * i + 1] * inv), "f"(ov[4 * i + 2] * inv),
+                         "f"(ov[4 * i + 3] * inv)
+                         : "memory");
+          __syncwarp();
+          uint4 w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = lds128(stage + sw128(x0 + 4 * i, lane & 7));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (dst[i] == nullptr) continue;
+            if (narrow)
+              *reinterpret_cast<uint2 *>(dst[i] + cc * 64) =
+                  make_uint2(float2_to_bf16x2(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
+                             float2_to_bf16x2(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+            else
+              *reinterpret_cast<uint4 *>(dst[i] + cc * 128) = w[i];
+          }
         }
+        __syncwarp();
         if (valid && !whole)
-          p.part_lse[slot] = l == 0.f ? -INFINITY : m + log2f(l);
+          p.part_lse[slot + lane] = l == 0.f ? -INFINITY : m + log2f(l);
       }
       tc_fence_before();
       ++piece;
@@ -698,123 +787,120 @@ __global__ void __launch_bounds__(kTrThreads, 2)
 }
 
 // ---- merge --------------------------------------------------------------------
-// One CTA per (token, query head): where the token's unit was cut, its row is
-// sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over the unit's pieces.  Each of
-// four warps takes a quarter of them, eight rows of loads in flight, a lane
-// four dims.
-constexpr int kTmWarps = 4;
+// Row r of a cut unit is sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over its
+// pieces, M the largest lse.  CTA c serves the unit that part c went on with:
+// such a unit of n + 1 pieces has n of these CTAs, and the i-th of them takes
+// rows i, i + n, ..., so every CTA reads about one piece's worth of rows however
+// long the unit is.  A row is one warp's, or several warps' that share its pieces
+// where a CTA has few rows; eight loads of 512 bytes in flight each.
+constexpr int kTmWarps = 8;
+
+struct RowSum {
+  float m, w;
+  float4 o;
+};
+__device__ __forceinline__ void row_add(RowSum &a, float w, const float4 &o) {
+  a.w += w;
+  a.o.x = fmaf(w, o.x, a.o.x);
+  a.o.y = fmaf(w, o.y, a.o.y);
+  a.o.z = fmaf(w, o.z, a.o.z);
+  a.o.w = fmaf(w, o.w, a.o.w);
+}
 
 __global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreeParams p) {
-  __shared__ long long warp_sum[kTmWarps];
-  __shared__ long long unit_start;
-  __shared__ int unit_seq;
   __shared__ float share_m[kTmWarps], share_w[kTmWarps];
   __shared__ float4 share_o[kTmWarps][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.x, h = blockIdx.y, g = h / p.group;
-  if (tid == 0) unit_seq = -1;
-  const int per = (p.num_seqs + 32 * kTmWarps - 1) / (32 * kTmWarps);
-  const int s0 = min(p.num_seqs, tid * per), s1 = min(p.num_seqs, s0 + per);
-  long long mine = 0, N;
-  for (int s = s0; s < s1; ++s) mine += head_weight(tree_seq(p, s, false), p.group) * p.hkv;
-  long long before = block_before(mine, warp_sum, N);
-  const long long C = ctas_in_use(p, N);
-  for (int s = s0; s < s1; ++s) {
-    const TreeSeq q = tree_seq(p, s, false);
-    const long long w = head_weight(q, p.group);
-    if (q.nodes > 0 && t >= q.q0 && t < q.q0 + q.nodes) {
-      unit_seq = s;
-      unit_start = before + w * g;
-    }
-    before += w * p.hkv;
-  }
-  __syncthreads();
-  if (unit_seq < 0) return;  // a row of no sequence
-  const TreeSeq q = tree_seq(p, unit_seq, false);
-  const int R = (t - q.q0) * p.group + h % p.group, mt = R / kPfRows, r = R % kPfRows;
-  long long U = unit_start;
-  for (int i = 0; i < mt; ++i) U += unit_tiles(q, p.group, i) + kTrPieceTiles;
-  const long long c0 = cta_of(U, C, N), c1 = cta_of(U + unit_tiles(q, p.group, mt) - 1, C, N);
-  if (c0 == c1) return;  // in one piece: written already
-  const long long len = (c1 - c0 + kTmWarps) / kTmWarps;
-  const long long ca = c0 + warp * len, cb = min(c1 + 1, ca + len);
-  float M = -INFINITY, W = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 8;
-  for (long long x = ca; x < cb; x += kBatch) {
-    float lse[kBatch];
-    float4 o[kBatch];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const TreeCut cut = p.cuts[blockIdx.x];
+  if (cut.rows == 0) return;
+  const int n = cut.last - cut.first, i0 = (int)blockIdx.x - cut.first - 1;
+  const int rows = (cut.rows - i0 + n - 1) / n;  // rows of this CTA
+  // warps that share a row
+  const int share = rows >= 5 ? 1 : rows >= 3 ? 2 : rows == 2 ? 4 : 8;
+  const int each = (n + share) / share;  // pieces of a warp
+  const int ca = cut.first + (warp % share) * each, cb = min(cut.last + 1, ca + each);
+  for (int k = 0; k < rows; k += kTmWarps / share) {
+    const int r = i0 + (k + warp / share) * n;
+    const bool mine = r < cut.rows;
+    RowSum a = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    constexpr int kBatch = 8;
+    for (int x = ca; mine && x < cb; x += kBatch) {
+      float lse[kBatch];
+      float4 o[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      lse[i] = -INFINITY;
-      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (x + i < cb) {
-        const long long slot = ((x + i == c0 ? (long long)p.splits : 0) + x + i) * kPfRows + r;
-        lse[i] = p.part_lse[slot];
-        o[i] = reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim)[lane];
+      for (int i = 0; i < kBatch; ++i) {
+        lse[i] = -INFINITY;
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x + i < cb) {
+          const long long slot =
+              ((x + i == cut.first ? (long long)p.splits : 0) + x + i) * kPfRows + r;
+          lse[i] = p.part_lse[slot];
+          o[i] = reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim)[lane];
+        }
+      }
+      float top = a.m;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, lse[i]);
+      const float ref = top == -INFINITY ? 0.f : top;  // nothing seen so far: weights zero
+      const float old = exp2f(a.m - ref);
+      a.w *= old;
+      a.o.x *= old, a.o.y *= old, a.o.z *= old, a.o.w *= old;
+      a.m = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float w = exp2f(lse[i] - ref);
+        if (!(w == 0.f)) row_add(a, w, o[i]);
       }
     }
-    float top = M;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, lse[i]);
-    const float ref = top == -INFINITY ? 0.f : top;  // nothing seen so far: weights zero
-    const float old = exp2f(M - ref);
-    W *= old;
-    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float w = exp2f(lse[i] - ref);
-      if (w == 0.f) continue;
-      W += w;
-      acc.x = fmaf(w, o[i].x, acc.x);
-      acc.y = fmaf(w, o[i].y, acc.y);
-      acc.z = fmaf(w, o[i].z, acc.z);
-      acc.w = fmaf(w, o[i].w, acc.w);
+    if (share > 1) {
+      share_o[warp][lane] = a.o;
+      if (lane == 0) {
+        share_m[warp] = a.m;
+        share_w[warp] = a.w;
+      }
+      __syncthreads();
+      if (warp % share == 0) {
+        float top = -INFINITY;
+        for (int w = warp; w < warp + share; ++w)
+          if (!(share_w[w] == 0.f)) top = fmaxf(top, share_m[w]);
+        a = {top, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int w = warp; w < warp + share; ++w) {
+          if (share_w[w] == 0.f) continue;
+          const float f = exp2f(share_m[w] - top);
+          const float4 o = share_o[w][lane];
+          a.w = fmaf(f, share_w[w], a.w);
+          a.o.x = fmaf(f, o.x, a.o.x);
+          a.o.y = fmaf(f, o.y, a.o.y);
+          a.o.z = fmaf(f, o.z, a.o.z);
+          a.o.w = fmaf(f, o.w, a.o.w);
+        }
+      }
+      __syncthreads();
     }
-    M = top;
+    if (!mine || warp % share != 0) continue;
+    const float inv = a.w > 0.f ? 1.f / a.w : a.w;
+    const int R = cut.mt * kPfRows + r, node = by_group(p, R);
+    const long long at = ((long long)(cut.q0 + node) * p.hq + cut.g * p.group +
+                          (R - node * p.group)) * kHeadDim + lane * 4;
+    const float4 o = make_float4(a.o.x * inv, a.o.y * inv, a.o.z * inv, a.o.w * inv);
+    if (p.out_f32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = o;
+    else
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+          make_uint2(float2_to_bf16x2(o.x, o.y), float2_to_bf16x2(o.z, o.w));
   }
-  share_o[warp][lane] = acc;
-  if (lane == 0) {
-    share_m[warp] = M;
-    share_w[warp] = W;
-  }
-  __syncthreads();
-  if (warp != 0) return;
-  float top = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kTmWarps; ++w)
-    if (!(share_w[w] == 0.f)) top = fmaxf(top, share_m[w]);
-  float sum = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kTmWarps; ++w) {
-    if (share_w[w] == 0.f) continue;
-    const float f = exp2f(share_m[w] - top);
-    const float4 a = share_o[w][lane];
-    sum = fmaf(f, share_w[w], sum);
-    acc.x = fmaf(f, a.x, acc.x);
-    acc.y = fmaf(f, a.y, acc.y);
-    acc.z = fmaf(f, a.z, acc.z);
-    acc.w = fmaf(f, a.w, acc.w);
-  }
-  const float inv = sum > 0.f ? 1.f / sum : sum;
-  acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-  const long long row = ((long long)t * p.hq + h) * kHeadDim + lane * 4;
-  if (p.out_f32)
-    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row) = acc;
-  else
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row) =
-        make_uint2(float2_to_bf16x2(acc.x, acc.y), float2_to_bf16x2(acc.z, acc.w));
 }
 
 constexpr size_t kTrHead = 256;  // the error word
 size_t tree_part_bytes(long long splits) {
   return (size_t)splits * 2 * kPfRows * kHeadDim * sizeof(float);
 }
+size_t tree_lse_bytes(long long splits) { return (size_t)splits * 2 * kPfRows * sizeof(float); }
 size_t tree_workspace(long long splits) {
-  return kTrHead + tree_part_bytes(splits) + (size_t)splits * 2 * kPfRows * sizeof(float);
+  return kTrHead + tree_part_bytes(splits) + tree_lse_bytes(splits) +
+         (size_t)splits * sizeof(TreeCut);
 }
 
 }  // namespace
@@ -854,6 +940,7 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
     return PA_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_tokens == 0 || max_q_len == 0) return PA_OK;
+  if (total_tokens > (1 << 26)) return PA_ERR_UNSUPPORTED;  // (rows of a kv head below 2^29)
   if (num_blocks < 1 || num_blocks > INT_MAX / kBlockSize || block_table_stride < 1)
     return PA_ERR_INVALID_ARG;
   if (!out || !q || !cu_seqlens || !parents || !k_cache || !v_cache || !block_tables ||
@@ -898,23 +985,26 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
   p.hq = num_q_heads;
   p.hkv = num_kv_heads;
   p.group = num_q_heads / num_kv_heads;
+  p.group_inv = (uint32_t)(((1ull << 32) + p.group - 1) / p.group);
   // masked scores are -inf before scaling, which needs a positive factor: a
   // negative scale flips q's signs, a zero one makes q zero
   p.scale_log2 = (scale > 0.f ? scale : scale < 0.f ? -scale : 1.f) * 1.4426950408889634f;
   p.q_and = scale == 0.f ? 0u : 0xFFFFFFFFu;
   p.q_xor = scale < 0.f ? 0x80008000u : 0u;
   p.splits = splits;
-  p.all_splits = num_splits > 0;
+  p.min_part = num_splits > 0 ? 1 : kTrMinPart;
   p.part_o = reinterpret_cast<float *>(ws + kTrHead);
   p.part_lse = reinterpret_cast<float *>(ws + kTrHead + tree_part_bytes(splits));
+  p.cuts = reinterpret_cast<TreeCut *>(ws + kTrHead + tree_part_bytes(splits) +
+                                       tree_lse_bytes(splits));
   p.err = static_cast<int32_t *>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_kernel(tree_kernel, dim3((unsigned)splits), dim3(kTrThreads), kTrSmem, s, true, tk,
                     tv, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   if (splits > 1 &&
-      launch_kernel(tree_merge_kernel, dim3((unsigned)total_tokens, (unsigned)num_q_heads),
-                    dim3(32 * kTmWarps), 0, s, true, p) != cudaSuccess)
+      launch_kernel(tree_merge_kernel, dim3((unsigned)splits), dim3(32 * kTmWarps), 0, s, true,
+                    p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   return PA_OK;
 }
