@@ -42,29 +42,34 @@ constexpr int kTrQHalf = kPfRows * 128;         // 128 rows x 64 dims of Q
 // K is needed a step before V of the same tile, and a loaded memory system takes
 // longer than a step: three K stages and two V stages, all the shared memory that
 // leaves room for two CTAs on an SM (so nothing is declared static).
+#ifndef TR_VST
+#define TR_VST 2
+#endif
+#ifndef TR_Z
+#define TR_Z 1
+#endif
 #ifndef TR_KST
 #define TR_KST 3
 #endif
-constexpr int kTrKStages = TR_KST, kTrVStages = 2;
+constexpr int kTrKStages = TR_KST, kTrVStages = TR_VST;
 constexpr int kTrOffQ = 0;
 constexpr int kTrOffK = kTrOffQ + 2 * kTrQHalf;
 constexpr int kTrOffV = kTrOffK + kTrKStages * kTrTile;
 constexpr int kTrOffBar = kTrOffV + kTrVStages * kTrTile;
 // 8-byte slots: K full / empty and V full / empty per stage, Q, two score, two
 // P and two PV barriers, the TMEM address, the abort flag, the last piece with
-// a V row that is not finite, the sums of the plan's scan, the CTA's place
+// a V row that is not finite, the CTA's place in the second list
 constexpr int kTsKFull = 0, kTsKEmpty = kTsKFull + kTrKStages, kTsVFull = kTsKEmpty + kTrKStages;
 constexpr int kTsVEmpty = kTsVFull + kTrVStages, kTsQ = kTsVEmpty + kTrVStages, kTsS = kTsQ + 1;
 constexpr int kTsP = kTsS + 2, kTsO = kTsP + 2, kTsTmem = kTsO + 2, kTsAbort = kTsTmem + 1;
-constexpr int kTsBad = kTsAbort + 1, kTsSum = kTsBad + 1, kTsPlace = kTsSum + kTrThreads / 32;
-constexpr int kTsSlots = 48;
+constexpr int kTsBad = kTsAbort + 1, kTsPlace = kTsBad + 1, kTsSlots = 32;
 constexpr int kTrSmem = kTrOffBar + kTsSlots * 8;
 static_assert(2 * (kTrSmem + 1024) <= 228 * 1024, "two CTAs do not fit an SM");
 constexpr int kTrCols = 256;    // tensor memory columns: S_0 0.., S_1 64.., O 128..
 constexpr int kTrSCols = 64, kTrO = 128;
 
 #ifndef TR_PIECE
-#define TR_PIECE 2
+#define TR_PIECE 4
 #endif
 #ifndef TR_MIN
 #define TR_MIN 4
@@ -78,7 +83,7 @@ constexpr int kTrMinPart = TR_MIN;
 // that an earlier CTA began: the unit's rows, CTAs first .. last and output rows.
 struct TreeCut {
   int rows, first, last;  // rows 0: the CTA starts with a unit's first tile
-  int q0, g, mt, unused[2];
+  int q0, g, mt, step, base;  // piece i of the unit is CTA base + step i's
 };
 
 #ifndef TR_X
@@ -101,9 +106,10 @@ struct TreeParams {
   uint32_t q_and, q_xor;  // staged q pairs = (q & q_and) ^ q_xor
   int splits;             // CTAs of the launch
   int min_part;
-  TreeCut *cuts;          // [splits]
-  float *part_o;          // [2][splits][128 rows][128]
-  float *part_lse;        // [2][splits][128]
+  int pairs;              // splits / 2
+  TreeCut *cuts;          // [2 lists][splits]
+  float *part_o;          // [2 lists][2][splits][128 rows][128]
+  float *part_lse;        // [2 lists][2][splits][128]
   int32_t *err;
 };
 
@@ -141,49 +147,33 @@ __device__ __forceinline__ int unit_tiles(const TreeParams &p, const TreeSeq &q,
 __device__ __forceinline__ int row_tiles(const TreeParams &p, const TreeSeq &q) {
   return (int)((unsigned)(q.nodes * p.group + kPfRows - 1) / kPfRows);
 }
-// Length of one kv head of the sequence in the list.
-__device__ __forceinline__ long long head_weight(const TreeParams &p, const TreeSeq &q) {
-  long long w = 0;
-  const int m = row_tiles(p, q);
-  for (int i = 0; i < m; ++i) w += unit_tiles(p, q, i) + kTrPieceTiles;
-  return w;
+// Two row tiles of a (sequence, kv head) run side by side, on the two CTAs of a
+// pair, so that what one reads of the cache is in L2 for the other: list 0, cut
+// over the pairs, holds them, a row tile pair under its longer tile's keys.  List
+// 1, cut over the CTAs, holds the row tiles that are left over.
+__device__ __forceinline__ int paired(const TreeParams &p, int row_tiles) {
+  return p.pairs ? row_tiles & ~1 : 0;
+}
+// Length of one kv head of the sequence in the lists (whose whole lengths the host
+// has made sure fit an int).
+__device__ __forceinline__ void head_weight(const TreeParams &p, const TreeSeq &q, int (&w)[2]) {
+  w[0] = w[1] = 0;
+  const int m = row_tiles(p, q), two = paired(p, m);
+  for (int i = 1; i < two; i += 2) w[0] += unit_tiles(p, q, i) + kTrPieceTiles;
+  for (int i = two; i < m; ++i) w[1] += unit_tiles(p, q, i) + kTrPieceTiles;
 }
 
-// The list is cut into parts of this length, one for a CTA, while it lasts.
-__device__ __forceinline__ long long part_length(const TreeParams &p, long long N) {
-  const long long len = N < (1ll << 31) ? ((unsigned)N + (unsigned)p.splits - 1u) / (unsigned)p.splits
-                                        : (N + p.splits - 1) / p.splits;
-  return max((long long)p.min_part, len);
+// A list is cut into parts of this length, while it lasts.
+__device__ __forceinline__ int part_length(const TreeParams &p, int N, int parts) {
+  return max(p.min_part, (int)(((unsigned)N + (unsigned)parts - 1u) / (unsigned)parts));
 }
-__device__ __forceinline__ int part_of(long long x, long long len) {
-  return x < (1ll << 31) && len < (1ll << 31) ? (int)((unsigned)x / (unsigned)len) : (int)(x / len);
+__device__ __forceinline__ int part_of(int x, int len) {
+  return (int)((unsigned)x / (unsigned)len);
 }
 
-// What lies before this thread's share of the list, and the whole.
-__device__ __forceinline__ long long block_before(long long v, long long *warp_sum,
-                                                  long long &total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sum[warp] = x;
-  __syncthreads();
-  long long before = x - v;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kTrThreads / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  return before;
-}
-
-// A CTA's place in the list: the unit it is in and where that unit starts.
+// A CTA's place in a list: the unit it is in and where that unit starts.
 struct TreePlace {
-  long long x, end, start;
+  int x, end, start;
   int s, g, mt;
   TreeSeq q;
 };
@@ -191,89 +181,141 @@ static_assert(sizeof(TreePlace) <= (kTsSlots - kTsPlace) * 8, "the place does no
 
 struct TreePiece {
   TreeSeq q;
-  int s, g, mt, t0, t1, tiles;
+  int s, g, mt, t0, t1, tiles, list;
 };
 
-// The next piece of a CTA's part of the list; every warp runs this for itself.
+// The next piece of a CTA's parts of the lists; every warp runs this for itself.
 struct TreeWalk {
   TreePlace at;
+  const TreePlace *second;
+  int list;
 
   __device__ __forceinline__ bool next(const TreeParams &p, TreePiece &r) {
-    while (at.x < at.end) {
-      const int tiles = unit_tiles(p, at.q, at.mt);
-      const long long rel = at.x - at.start;
+    while (true) {
+      if (at.x >= at.end) {
+        if (list == 1) return false;
+        list = 1;
+        at = *second;
+        continue;
+      }
+      const int m = row_tiles(p, at.q), two = paired(p, m);
+      // of a pair, the first CTA's row tile may end some tiles before the second's
+      const int span = unit_tiles(p, at.q, list == 0 ? at.mt + 1 : at.mt);
+      const int mt = list == 0 ? at.mt + (int)(blockIdx.x & 1) : at.mt;
+      const int tiles = unit_tiles(p, at.q, mt);
+      const int rel = at.x - at.start;
       const bool got = rel < tiles;
       if (got) {
         r.q = at.q;
         r.s = at.s;
         r.g = at.g;
-        r.mt = at.mt;
+        r.mt = mt;
         r.tiles = tiles;
-        r.t0 = (int)rel;
-        r.t1 = (int)min((long long)tiles, at.end - at.start);
+        r.t0 = rel;
+        r.t1 = min(tiles, at.end - at.start);
+        r.list = list;
       }
-      at.start += tiles + kTrPieceTiles;
+      at.start += span + kTrPieceTiles;
       at.x = at.start;
-      if (++at.mt == row_tiles(p, at.q)) {
-        at.mt = 0;
+      at.mt += list == 0 ? 2 : 1;
+      if (at.mt == (list == 0 ? two : m)) {
         if (++at.g == p.hkv) {
           at.g = 0;
-          if (at.x < at.end) do {
-              at.q = tree_seq(p, ++at.s, false);
-            } while (at.q.nodes == 0 && at.s + 1 < p.num_seqs);
+          if (at.x < at.end) at.s = next_seq(p, at.s, list, at.q);
         }
+        at.mt = list == 0 ? 0 : paired(p, row_tiles(p, at.q));
       }
       if (got) return true;
     }
-    return false;
+  }
+  // The next sequence with something in the list (there is one).
+  __device__ __forceinline__ static int next_seq(const TreeParams &p, int s, int list,
+                                                 TreeSeq &q) {
+    bool some;
+    do {
+      q = tree_seq(p, ++s, false);
+      const int m = row_tiles(p, q), two = paired(p, m);
+      some = list == 0 ? two > 0 : two < m;
+    } while (!some && s + 1 < p.num_seqs);
+    return s;
   }
 };
 
-// The CTA's part of the list: the thread whose sequences hold its start leaves the
-// place there.  False: nothing to do.
-__device__ __forceinline__ bool tree_plan(const TreeParams &p, long long *warp_sum,
-                                          TreePlace *place, long long &len) {
-  const int per = (int)((unsigned)p.num_seqs + kTrThreads - 1u) / kTrThreads;
-  const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
-  long long mine = 0, N;
+// The CTA's parts of the lists (places without work: x = end).  Every warp works it
+// out for itself, a lane per run of sequences.
+__device__ __forceinline__ void tree_plan(const TreeParams &p, TreePlace (&places)[2],
+                                          int (&len)[2]) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const int per = (int)(((unsigned)p.num_seqs + 31u) / 32u);
+  const int s0 = min(p.num_seqs, lane * per), s1 = min(p.num_seqs, s0 + per);
+  int mine[2] = {0, 0}, upto[2], w[2];
   TreeSeq q = {0, 0, 0};
   for (int s = s0; s < s1; ++s) {
-    q = tree_seq(p, s, blockIdx.x == 0);
-    mine += head_weight(p, q) * p.hkv;
+    q = tree_seq(p, s, blockIdx.x == 0 && threadIdx.x < 32);
+    head_weight(p, q, w);
+    mine[0] += w[0] * p.hkv;
+    mine[1] += w[1] * p.hkv;
   }
-  long long before = block_before(mine, warp_sum, N);
-  len = part_length(p, N);
-  const long long x0 = (long long)blockIdx.x * len;
-  if (x0 >= N) return false;
-  if (x0 < before || x0 >= before + mine) return true;
-  for (int s = s0; s < s1; ++s) {
-    if (per > 1) q = tree_seq(p, s, false);
-    const long long w = head_weight(p, q);
-    if (x0 < before + w * p.hkv) {
-      TreePlace r;
-      r.x = x0;
-      r.end = min(N, x0 + len);
-      r.s = s;
-      r.q = q;
-      r.g = 0;
-      r.start = before;
-      while (x0 >= r.start + w) {
-        r.start += w;
-        ++r.g;
-      }
-      r.mt = 0;
-      while (true) {
-        const int unit = unit_tiles(p, q, r.mt) + kTrPieceTiles;
-        if (x0 < r.start + unit) break;
-        r.start += unit;
-        ++r.mt;
-      }
-      *place = r;
-      break;
+  upto[0] = mine[0];
+  upto[1] = mine[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(kAll, upto[0], o), b = __shfl_up_sync(kAll, upto[1], o);
+    if (lane >= o) {
+      upto[0] += a;
+      upto[1] += b;
     }
-    before += w * p.hkv;
   }
-  return true;
+#pragma unroll
+  for (int l = 0; l < 2; ++l) {
+    const int N = __shfl_sync(kAll, upto[l], 31);
+    const int part = l == 0 ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int parts = l == 0 ? p.pairs : p.splits;
+    TreePlace &r = places[l];
+    r.x = r.end = 0;
+    len[l] = 1;
+    if (N == 0 || part >= parts) continue;
+    len[l] = part_length(p, N, parts);
+    if (part > (N - 1) / len[l]) continue;
+    const int x0 = part * len[l];
+    const unsigned has = __ballot_sync(kAll, x0 >= upto[l] - mine[l] && x0 < upto[l]);
+    int v[8] = {};
+    if ((has >> lane) & 1u) {
+      int at = upto[l] - mine[l];
+      for (int s = s0; s < s1; ++s) {
+        if (per > 1) q = tree_seq(p, s, false);
+        head_weight(p, q, w);
+        if (x0 >= at + w[l] * p.hkv) {
+          at += w[l] * p.hkv;
+          continue;
+        }
+        int g = 0, mt = l == 0 ? 0 : paired(p, row_tiles(p, q));
+        while (x0 >= at + w[l]) {
+          at += w[l];
+          ++g;
+        }
+        while (true) {
+          const int unit = unit_tiles(p, q, mt + 1 - l) + kTrPieceTiles;
+          if (x0 < at + unit) break;
+          at += unit;
+          mt += 2 - l;
+        }
+        v[0] = at, v[1] = s, v[2] = g, v[3] = mt, v[4] = q.q0, v[5] = q.nodes, v[6] = q.keys;
+        break;
+      }
+    }
+    const int from = __ffs(has) - 1;
+    r.x = x0;
+    r.end = min(N, x0 + len[l]);
+    r.start = __shfl_sync(kAll, v[0], from);
+    r.s = __shfl_sync(kAll, v[1], from);
+    r.g = __shfl_sync(kAll, v[2], from);
+    r.mt = __shfl_sync(kAll, v[3], from);
+    r.q.q0 = __shfl_sync(kAll, v[4], from);
+    r.q.nodes = __shfl_sync(kAll, v[5], from);
+    r.q.keys = __shfl_sync(kAll, v[6], from);
+  }
 }
 
 // ---- attention ----------------------------------------------------------------
@@ -303,6 +345,69 @@ __device__ __noinline__ uint32_t not_finite(const TreeParams &p, int s, int q0, 
   return dims;
 }
 
+// A store without a branch around it.
+__device__ __forceinline__ void store_if(bool yes, char *to, const uint4 &v) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+      "@p st.global.v4.u32 [%1], {%2, %3, %4, %5};\n\t}" ::"r"((int)yes),
+      "l"(__cvta_generic_to_global(to)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+      : "memory");
+}
+__device__ __forceinline__ void store_if(bool yes, char *to, uint32_t a, uint32_t b) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+      "@p st.global.v2.u32 [%1], {%2, %3};\n\t}" ::"r"((int)yes),
+      "l"(__cvta_generic_to_global(to)), "r"(a), "r"(b)
+      : "memory");
+}
+
+// Clears, in a staged V tile, the rows of keys from `end` on and the elements of keys
+// from `done` on that are not finite (then *bad = piece).  Thread r of 128 has the
+// 16-byte chunk r % 16 of keys r / 16 + 8 k.  0 x is NaN exactly where x is not
+// finite, so a sum of such products tells.
+__device__ __forceinline__ void clean_v(uint32_t tile, int r, int key0, int done, int end,
+                                        volatile int *bad, int piece) {
+  const int ch = r & 15, k0 = r >> 4;
+  const uint32_t at = tile + (ch >> 3) * kTrHalf + sw128(k0, ch & 7);  // (+ 1024 a step: k % 8)
+  uint4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = make_uint4(0u, 0u, 0u, 0u);
+    const int key = key0 + k0 + 8 * k;
+    if (key >= done && key < end) v[k] = lds128(at + 1024 * k);
+    if (key >= end)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + 1024 * k), "r"(0u)
+                   : "memory");
+  }
+  uint32_t sum[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[0]) : "r"(v[k].x), "r"(0u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[1]) : "r"(v[k].y), "r"(0u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[2]) : "r"(v[k].z), "r"(0u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[3]) : "r"(v[k].w), "r"(0u));
+  }
+  if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0u) {  // rare
+    *bad = piece;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const int key = key0 + k0 + 8 * k;
+      if (key < done || key >= end) continue;
+      uint4 x = lds128(at + 1024 * k);
+      uint32_t *w = &x.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+      }
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + 1024 * k), "r"(x.x),
+                   "r"(x.y), "r"(x.z), "r"(x.w)
+                   : "memory");
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(kTrThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
@@ -316,8 +421,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kTsTmem);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kTsAbort);
   volatile int *bad_piece = reinterpret_cast<volatile int *>(bars + kTsBad);
-  long long *warp_sum = reinterpret_cast<long long *>(bars + kTsSum);
-  TreePlace *place = reinterpret_cast<TreePlace *>(bars + kTsPlace);
+  TreePlace *second = reinterpret_cast<TreePlace *>(bars + kTsPlace);
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -352,35 +456,50 @@ __global__ void __launch_bounds__(kTrThreads, 2)
   }
   griddep_wait();
   griddep_launch_dependents();
-  long long len;
-  const bool busy = tree_plan(p, warp_sum, place, len) && (base & 1023) == 0;
-  // (the swizzle needs it; without static shared memory the base is aligned)
-  if ((base & 1023) != 0 && tid == 0) report(p.err, PA_DEVERR_WAIT_TIMEOUT);
+  TreeWalk walk;
+  walk.second = second;
+  walk.list = 0;
+  {
+    TreePlace places[2];
+    int len[2];
+    tree_plan(p, places, len);
+    walk.at = places[0];
+    if (tid == 0) *second = places[1];
+    if (warp == 3 && lane == 0) {
+      // what the merge has to know of a part that goes on with a unit
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        const TreePlace &at = places[l];
+        TreeCut cut = {};
+        if (at.x < at.end && at.x > at.start) {
+          const int mt = l == 0 ? at.mt + (int)(blockIdx.x & 1) : at.mt;
+          const int tiles = unit_tiles(p, at.q, mt);
+          if (at.x - at.start < tiles) {
+            cut.rows = min(kPfRows, at.q.nodes * p.group - mt * kPfRows);
+            cut.first = part_of(at.start, len[l]);
+            cut.last = part_of(at.start + tiles - 1, len[l]);
+            cut.q0 = at.q.q0;
+            cut.g = at.g;
+            cut.mt = mt;
+            cut.step = 2 - l;
+            cut.base = l == 0 ? (int)(blockIdx.x & 1) : 0;
+          }
+        }
+        p.cuts[l * p.splits + blockIdx.x] = cut;
+      }
+    }
+    __syncwarp();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_o = tmem + kTrO;
-  TreeWalk walk;
-  if (busy)
-    walk.at = *place;
-  else
-    walk.at.x = walk.at.end = walk.at.start = 0;
-  if (tid == 96) {
-    TreeCut cut = {};
-    const long long rel = walk.at.x - walk.at.start;
-    const int tiles = busy ? unit_tiles(p, walk.at.q, walk.at.mt) : 0;
-    if (busy && rel > 0 && rel < tiles) {
-      cut.rows = min(kPfRows, walk.at.q.nodes * p.group - walk.at.mt * kPfRows);
-      cut.first = part_of(walk.at.start, len);
-      cut.last = part_of(walk.at.start + tiles - 1, len);
-      cut.q0 = walk.at.q.q0;
-      cut.g = walk.at.g;
-      cut.mt = walk.at.mt;
-    }
-    p.cuts[blockIdx.x] = cut;
+  if ((base & 1023) != 0) {  // (the swizzle needs it; without static shared memory it is so)
+    if (tid == 0) report(p.err, PA_DEVERR_WAIT_TIMEOUT);
+    walk.at.x = walk.at.end;
+    walk.list = 1;
   }
-  __syncwarp();
   constexpr unsigned kAll = 0xffffffffu;
 
   TreePiece u;
@@ -522,30 +641,37 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       const bool alive = u.mt * kPfRows + lb < limit;  // any row of the warp
       const int node = by_group(p, R);
       const int done = u.q.keys - u.q.nodes;
-      // row R of the tile is this row of q and out
-      auto head_row = [&](int x) {
-        const int n = by_group(p, x);
-        return (long long)(u.q.q0 + n) * p.hq + u.g * p.group + (x - n * p.group);
-      };
+      // this lane's row of q and out (T * Hq < 2^32); another lane's comes by shuffle
+      const uint32_t my_row = (uint32_t)(u.q.q0 + node) * (uint32_t)p.hq +
+                              (uint32_t)(u.g * p.group + R - node * p.group);
+      // parents of the window first .. first + 63 of nodes, two a lane
+      const int32_t *par = p.parents + u.q.q0;
+      auto parent = [&](int n) { return n >= 0 && n < u.q.nodes ? par[n] : -1; };
+      int par0 = -1, par1 = -1;
+      if (alive && u.t1 * kPfKeys > done) {
+        const int first = (u.t1 - 1) * kPfKeys - done;
+        par0 = parent(first + lane);
+        par1 = parent(first + lane + 32);
+      }
       // Q rows, half a warp a row, into the layout the TMA gives K tiles
       if (alive) {
         uint4 qv[16];
         const int ch = lane & 15;
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q) + ch;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int x = u.mt * kPfRows + lb + 2 * i + (lane >> 4);
+          const int x = 2 * i + (lane >> 4);
+          const uint32_t row = __shfl_sync(kAll, my_row, x);
           qv[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (x < limit) qv[i] = reinterpret_cast<const uint4 *>(p.q + head_row(x) * kHeadDim)[ch];
+          if (u.mt * kPfRows + lb + x < limit) qv[i] = src[(size_t)row * 16];
         }
+        const uint32_t a0 = base + kTrOffQ + (ch >> 3) * kTrQHalf + lb * 128;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t a = base + kTrOffQ + (ch >> 3) * kTrQHalf +
-                             sw128(lb + 2 * i + (lane >> 4), ch & 7);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
+        for (int i = 0; i < 16; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           a0 + sw128(2 * i + (lane >> 4), ch & 7)),
                        "r"((qv[i].x & p.q_and) ^ p.q_xor), "r"((qv[i].y & p.q_and) ^ p.q_xor),
-                       "r"((qv[i].z & p.q_and) ^ p.q_xor), "r"((qv[i].w & p.q_and) ^ p.q_xor)
-                       : "memory");
-        }
+                       "r"((qv[i].z & p.q_and) ^ p.q_xor), "r"((qv[i].w & p.q_and) ^ p.q_xor));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       mbar_arrive(b_q);
@@ -556,11 +682,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       // A tile's 64 keys are a window of 64 nodes, whose parents the warp holds,
       // two a lane: a step of the walk is a shuffle.
       int up = valid ? node : -1;
-      const int32_t *par = p.parents + u.q.q0;
-      auto climb = [&](int first, uint32_t (&vis)[2]) {  // window first .. first + 63
-        const int n0 = first + lane, n1 = n0 + 32;
-        const int par0 = n0 >= 0 && n0 < u.q.nodes ? par[n0] : -1;
-        const int par1 = n1 >= 0 && n1 < u.q.nodes ? par[n1] : -1;
+      auto climb = [&](int first, int par0, int par1, uint32_t (&vis)[2]) {
         while (__any_sync(kAll, up >= 0 && up >= first)) {
           const int k = up - first;
           const int next0 = __shfl_sync(kAll, par0, k & 31), next1 = __shfl_sync(kAll, par1, k & 31);
@@ -577,7 +699,10 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       if (alive && u.t1 * kPfKeys > done) {  // the windows above the piece's last tile
         uint32_t unused[2] = {0u, 0u};
         const int top = by_group(p, min(u.mt * kPfRows + lb + 31, limit - 1));
-        for (int j = (done + top) / kPfKeys; j >= u.t1; --j) climb(j * kPfKeys - done, unused);
+        for (int j = (done + top) / kPfKeys; j >= u.t1; --j) {
+          const int first = j * kPfKeys - done;
+          climb(first, parent(first + lane), parent(first + lane + 32), unused);
+        }
       }
       for (int j = u.t1 - 1; j >= u.t0 && ok; --j, ++it) {
         const int st = it % kTrVStages, buf = it & 1;
@@ -585,12 +710,23 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         const bool in_tree = key0 > done - kPfKeys;  // the tile holds drafted nodes
         uint32_t vis[2] = {0u, 0u};
         if (in_tree && alive) {
-          climb(key0 - done, vis);
+          climb(key0 - done, par0, par1, vis);
+          par0 = parent(key0 - kPfKeys - done + lane);
+          par1 = parent(key0 - kPfKeys - done + lane + 32);
           if (valid && key0 < done) {
             const int below = done - key0;  // 1 .. 63 committed keys
             vis[0] |= below >= 32 ? 0xffffffffu : (1u << below) - 1u;
             vis[1] |= below > 32 ? (1u << (below - 32)) - 1u : 0u;
           }
+        }
+        // V rows of the tile that some rows may not see: those past the end may
+        // hold anything and are cleared; a drafted node's infinities and NaN are
+        // cleared here and put into the rows that see it at the end
+        if (in_tree) {
+          ok = __all_sync(kAll, mbar_wait(b_v_full + 8 * st, (it / kTrVStages) & 1, abort_flag,
+                                          p.err));
+          if (!ok) break;
+          clean_v(base + kTrOffV + st * kTrTile, r, key0, done, u.q.keys, bad_piece, piece);
         }
         ok = __all_sync(kAll, mbar_wait(b_s + 8 * buf, (it >> 1) & 1, abort_flag, p.err));
         if (!ok) break;
@@ -678,37 +814,6 @@ __global__ void __launch_bounds__(kTrThreads, 2)
                            ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7])));
           tmem_wait_st();
         }
-        // V rows of the tile that some rows may not see: those past the end may
-        // hold anything and are cleared; a drafted node's infinities and NaN are
-        // cleared here and put into the rows that see it at the end
-        if (in_tree) {
-          ok = __all_sync(kAll, mbar_wait(b_v_full + 8 * st, (it / kTrVStages) & 1, abort_flag,
-                                          p.err));
-          if (!ok) break;
-          const uint32_t vb = base + kTrOffV + st * kTrTile;
-          for (int i = r; i < kPfKeys * 16; i += kPfRows) {
-            const int key = key0 + (i >> 4), ch = i & 15;
-            if (key < done) continue;
-            const uint32_t a = vb + (ch >> 3) * kTrHalf + sw128(i >> 4, ch & 7);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (key < u.q.keys) {
-              v = lds128(a);
-              const uint4 was = v;
-              uint32_t *w = &v.x;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
-                if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu;
-              }
-              if (v.x == was.x && v.y == was.y && v.z == was.z && v.w == was.w) continue;
-              *bad_piece = piece;
-            }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x),
-                         "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         tc_fence_before();
         mbar_arrive(b_p + 8 * buf);
       }
@@ -721,52 +826,54 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         const bool bad = *bad_piece == piece;
         const bool whole = u.t0 == 0 && u.t1 == u.tiles;
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (l NaN: a NaN row)
-        const long long slot = ((u.t0 > 0 ? 0 : (long long)p.splits) + blockIdx.x) * kPfRows + lb;
+        const long long slot = ((2 * u.list + (u.t0 == 0)) * (long long)p.splits + blockIdx.x) *
+                                   kPfRows + lb;
         // 32 columns of the warp's rows at a time go through its own Q rows (which
         // no MMA reads any more), so that eight lanes store a row's 128 bytes
         const uint32_t stage = base + kTrOffQ + lb * 128;
-        const int x0 = lane >> 3, col = 4 * (lane & 7);
-        char *dst[8];  // of rows x0 + 4 i; null: no such row
         const bool narrow = whole && !p.out_f32;
+        char *to = whole ? static_cast<char *>(p.out)
+                         : reinterpret_cast<char *>(p.part_o + slot * kHeadDim);
+        uint32_t rows[8];  // of this lane's stores
+        const int left = limit - (u.mt * kPfRows + lb + (lane >> 3));  // row 4 i is one: 4 i < left
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int x = u.mt * kPfRows + lb + x0 + 4 * i;
-          const long long at = whole ? head_row(x) : slot + x0 + 4 * i;
-          dst[i] = static_cast<char *>(whole ? p.out : static_cast<void *>(p.part_o)) +
-                   (at * kHeadDim + col) * (narrow ? 2 : 4);
-          if (x >= limit) dst[i] = nullptr;
-        }
+        for (int i = 0; i < 8; ++i)
+          rows[i] = __shfl_sync(kAll, whole ? my_row : (uint32_t)lane, 4 * i + (lane >> 3));
+        to += (size_t)(lane & 7) * (narrow ? 8 : 16);
 #pragma unroll 1
         for (int cc = 0; cc < kHeadDim / 32; ++cc) {
           float ov[32];
           tmem_ld32(tmem_o + trow + cc * 32, ov);
-          if (valid && bad TR_X) {
+          if (valid && bad) {
             const uint32_t dims = not_finite(p, u.s, u.q.q0, done, u.g, node, u.t0 * kPfKeys,
                                              u.t1 * kPfKeys - 1, cc);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((dims >> i) & 1u) ov[i] = __int_as_float(0x7fffffff);
           }
-          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + sw128(lane, i)),
                          "f"(ov[4 * i] * inv), "f"(ov[4 * i + 1] * inv), "f"(ov[4 * i + 2] * inv),
-                         "f"(ov[4 * i + 3] * inv)
-                         : "memory");
+                         "f"(ov[4 * i + 3] * inv));
           __syncwarp();
           uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = lds128(stage + sw128(x0 + 4 * i, lane & 7));
+          for (int i = 0; i < 8; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                         : "r"(stage + sw128(4 * i + (lane >> 3), lane & 7)));
+          __syncwarp();
+          if (narrow) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (dst[i] == nullptr) continue;
-            if (narrow)
-              *reinterpret_cast<uint2 *>(dst[i] + cc * 64) =
-                  make_uint2(float2_to_bf16x2(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
-                             float2_to_bf16x2(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
-            else
-              *reinterpret_cast<uint4 *>(dst[i] + cc * 128) = w[i];
+            for (int i = 0; i < 8; ++i)
+              store_if(4 * i < left, to + (size_t)rows[i] * 256 + cc * 64,
+                       float2_to_bf16x2(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
+                       float2_to_bf16x2(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              store_if(4 * i < left, to + (size_t)rows[i] * 512 + cc * 128, w[i]);
           }
         }
         __syncwarp();
@@ -792,7 +899,8 @@ __global__ void __launch_bounds__(kTrThreads, 2)
 // such a unit of n + 1 pieces has n of these CTAs, and the i-th of them takes
 // rows i, i + n, ..., so every CTA reads about one piece's worth of rows however
 // long the unit is.  A row is one warp's, or several warps' that share its pieces
-// where a CTA has few rows; eight loads of 512 bytes in flight each.
+// where a CTA has few rows; a warp has eight loads of 512 bytes in flight, of one
+// row or, where a row has few pieces, of four or two.
 constexpr int kTmWarps = 8;
 
 struct RowSum {
@@ -807,53 +915,114 @@ __device__ __forceinline__ void row_add(RowSum &a, float w, const float4 &o) {
   a.o.w = fmaf(w, o.w, a.o.w);
 }
 
+// Pieces x .. x + kPieces - 1 (below cb) of kRows rows (below 0: none), all loads first.
+template <int kRows, int kPieces>
+__device__ __forceinline__ void add_pieces(const TreeParams &p, const TreeCut &cut,
+                                           const int (&row)[kRows], int x, int cb,
+                                           RowSum *const (&a)[kRows]) {
+  const int lane = threadIdx.x & 31;
+  float lse[kRows][kPieces];
+  float4 o[kRows][kPieces];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k)
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      lse[k][i] = -INFINITY;
+      o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row[k] >= 0 && x + i < cb) {
+        const long long slot = ((2 * blockIdx.y + (x + i == cut.first)) * (long long)p.splits +
+                                cut.base + (long long)cut.step * (x + i)) * kPfRows + row[k];
+        lse[k][i] = p.part_lse[slot];
+        o[k][i] = reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim)[lane];
+      }
+    }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    RowSum &s = *a[k];
+    float top = s.m;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) top = fmaxf(top, lse[k][i]);
+    const float ref = top == -INFINITY ? 0.f : top;  // nothing seen so far: weights zero
+    const float old = exp2f(s.m - ref);
+    s.w *= old;
+    s.o.x *= old, s.o.y *= old, s.o.z *= old, s.o.w *= old;
+    s.m = top;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const float w = exp2f(lse[k][i] - ref);
+      if (!(w == 0.f)) row_add(s, w, o[k][i]);
+    }
+  }
+}
+
+__device__ __forceinline__ void write_row(const TreeParams &p, const TreeCut &cut, int r,
+                                          const RowSum &a) {
+  const float inv = a.w > 0.f ? 1.f / a.w : a.w;
+  const int R = cut.mt * kPfRows + r, node = by_group(p, R);
+  const long long at = ((long long)(cut.q0 + node) * p.hq + cut.g * p.group +
+                        (R - node * p.group)) * kHeadDim + (threadIdx.x & 31) * 4;
+  const float4 o = make_float4(a.o.x * inv, a.o.y * inv, a.o.z * inv, a.o.w * inv);
+  if (p.out_f32)
+    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = o;
+  else
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+        make_uint2(float2_to_bf16x2(o.x, o.y), float2_to_bf16x2(o.z, o.w));
+}
+
+// The CTA's rows, kRows at a time by a warp, of kPieces pieces at most.
+template <int kRows, int kPieces>
+__device__ __forceinline__ void merge_rows(const TreeParams &p, const TreeCut &cut, int n, int i0,
+                                           int rows, int warp) {
+  for (int k = warp * kRows; k < rows; k += kTmWarps * kRows) {
+    int row[kRows];
+    RowSum s[kRows], *to[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int r = i0 + (k + j) * n;
+      row[j] = k + j < rows && r < cut.rows ? r : -1;
+      s[j] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      to[j] = &s[j];
+    }
+    add_pieces<kRows, kPieces>(p, cut, row, cut.first, cut.last + 1, to);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      if (row[j] >= 0) write_row(p, cut, row[j], s[j]);
+  }
+}
+
 __global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreeParams p) {
   __shared__ float share_m[kTmWarps], share_w[kTmWarps];
   __shared__ float4 share_o[kTmWarps][32];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const TreeCut cut = p.cuts[blockIdx.x];
+  const TreeCut cut = p.cuts[blockIdx.y * p.splits + blockIdx.x];
   if (cut.rows == 0) return;
-  const int n = cut.last - cut.first, i0 = (int)blockIdx.x - cut.first - 1;
+  const int n = (cut.last - cut.first) * TR_Z;
+  const int i0 = ((int)blockIdx.x / cut.step - cut.first - 1) * TR_Z + (int)blockIdx.z;
+  const int pieces = cut.last - cut.first + 1;
   const int rows = (cut.rows - i0 + n - 1) / n;  // rows of this CTA
   // warps that share a row
   const int share = rows >= 5 ? 1 : rows >= 3 ? 2 : rows == 2 ? 4 : 8;
-  const int each = (n + share) / share;  // pieces of a warp
+  const int each = (pieces + share - 1) / share;  // pieces of a warp
   const int ca = cut.first + (warp % share) * each, cb = min(cut.last + 1, ca + each);
+  if (share == 1 && each <= 4) {
+    if (each <= 2)
+      merge_rows<4, 2>(p, cut, n, i0, rows, warp);
+    else
+      merge_rows<2, 4>(p, cut, n, i0, rows, warp);
+    return;
+  }
   for (int k = 0; k < rows; k += kTmWarps / share) {
     const int r = i0 + (k + warp / share) * n;
     const bool mine = r < cut.rows;
     RowSum a = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    constexpr int kBatch = 8;
-    for (int x = ca; mine && x < cb; x += kBatch) {
-      float lse[kBatch];
-      float4 o[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        lse[i] = -INFINITY;
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x + i < cb) {
-          const long long slot =
-              ((x + i == cut.first ? (long long)p.splits : 0) + x + i) * kPfRows + r;
-          lse[i] = p.part_lse[slot];
-          o[i] = reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim)[lane];
-        }
+    if (mine)
+      for (int x = ca; x < cb; x += 8) {
+        const int row[1] = {r};
+        RowSum *one[1] = {&a};
+        add_pieces<1, 8>(p, cut, row, x, cb, one);
       }
-      float top = a.m;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, lse[i]);
-      const float ref = top == -INFINITY ? 0.f : top;  // nothing seen so far: weights zero
-      const float old = exp2f(a.m - ref);
-      a.w *= old;
-      a.o.x *= old, a.o.y *= old, a.o.z *= old, a.o.w *= old;
-      a.m = top;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const float w = exp2f(lse[i] - ref);
-        if (!(w == 0.f)) row_add(a, w, o[i]);
-      }
-    }
     if (share > 1) {
       share_o[warp][lane] = a.o;
       if (lane == 0) {
@@ -880,27 +1049,18 @@ __global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreePar
       __syncthreads();
     }
     if (!mine || warp % share != 0) continue;
-    const float inv = a.w > 0.f ? 1.f / a.w : a.w;
-    const int R = cut.mt * kPfRows + r, node = by_group(p, R);
-    const long long at = ((long long)(cut.q0 + node) * p.hq + cut.g * p.group +
-                          (R - node * p.group)) * kHeadDim + lane * 4;
-    const float4 o = make_float4(a.o.x * inv, a.o.y * inv, a.o.z * inv, a.o.w * inv);
-    if (p.out_f32)
-      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = o;
-    else
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
-          make_uint2(float2_to_bf16x2(o.x, o.y), float2_to_bf16x2(o.z, o.w));
+    write_row(p, cut, r, a);
   }
 }
 
 constexpr size_t kTrHead = 256;  // the error word
 size_t tree_part_bytes(long long splits) {
-  return (size_t)splits * 2 * kPfRows * kHeadDim * sizeof(float);
+  return (size_t)splits * 4 * kPfRows * kHeadDim * sizeof(float);
 }
-size_t tree_lse_bytes(long long splits) { return (size_t)splits * 2 * kPfRows * sizeof(float); }
+size_t tree_lse_bytes(long long splits) { return (size_t)splits * 4 * kPfRows * sizeof(float); }
 size_t tree_workspace(long long splits) {
   return kTrHead + tree_part_bytes(splits) + tree_lse_bytes(splits) +
-         (size_t)splits * sizeof(TreeCut);
+         (size_t)splits * 2 * sizeof(TreeCut);
 }
 
 }  // namespace
@@ -967,6 +1127,12 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
   if (set_smem_once(configured, tree_kernel, device, kTrSmem) != cudaSuccess) return PA_ERR_LAUNCH;
   // two CTAs per SM: all of the unified L1 / shared memory as shared memory (a hint)
   cudaFuncSetAttribute(tree_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  // the lists' lengths fit an int, whatever the lengths on the device
+  const long long most_tiles = (long long)block_table_stride * kBlockSize / kPfKeys + 2;
+  const long long most_nodes = max_q_len < total_tokens ? max_q_len : total_tokens;
+  const long long rows = (most_nodes * (num_q_heads / num_kv_heads) + kPfRows - 1) / kPfRows;
+  if (most_tiles + kTrPieceTiles > (1ll << 31) / num_kv_heads / rows / num_seqs)
+    return PA_ERR_UNSUPPORTED;
   char *ws = static_cast<char *>(workspace);
   TreeParams p;
   p.out = out;
@@ -992,6 +1158,7 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
   p.q_and = scale == 0.f ? 0u : 0xFFFFFFFFu;
   p.q_xor = scale < 0.f ? 0x80008000u : 0u;
   p.splits = splits;
+  p.pairs = splits / 2;
   p.min_part = num_splits > 0 ? 1 : kTrMinPart;
   p.part_o = reinterpret_cast<float *>(ws + kTrHead);
   p.part_lse = reinterpret_cast<float *>(ws + kTrHead + tree_part_bytes(splits));
@@ -1003,7 +1170,7 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
                     tv, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   if (splits > 1 &&
-      launch_kernel(tree_merge_kernel, dim3((unsigned)splits), dim3(32 * kTmWarps), 0, s, true,
+      launch_kernel(tree_merge_kernel, dim3((unsigned)splits, 2, TR_Z), dim3(32 * kTmWarps), 0, s, true,
                     p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   return PA_OK;

@@ -27,7 +27,7 @@ def test_workspace_size(lib):
     size = lib.pa_decode_tree_workspace_size
     assert size(0) == 0 and size(-1) == 0 and size(4097) == 0
     for s in (1, 7, 304, 4096):
-        assert size(s) == 256 + s * (2 * 128 * 129 * 4 + 32)
+        assert size(s) == 256 + s * (4 * 128 * 129 * 4 + 64)
 
 
 def test_decode_tree(lib):
