@@ -869,7 +869,7 @@ PA_API pa_status pa_prefill_fp8_block(
  *   max_q_len      upper bound of every T.
  *   context_lens   int32 [num_seqs], the nodes included.
  *   scale          any finite value, of either sign.
- *   num_splits     CTAs that share the work; 0 = as many of
+ *   num_splits     CTAs that share the work (at most PA_DECODE_MAX_SPLITS); 0 = as many of
  *                  pa_decode_tree_default_splits as suit the work they find.
  *   workspace      >= pa_decode_tree_workspace_size(S) bytes, 16-byte aligned,
  *                  S = num_splits or the default: int32 error word at byte 0
@@ -887,6 +887,9 @@ PA_API pa_status pa_prefill_fp8_block(
  * those after it unspecified; a table entry outside the pool sets
  * PA_DEVERR_BLOCK_INDEX, with the sequence's rows unspecified.  Results are
  * deterministic for a fixed num_splits and do not depend on where pages lie.
+ * More than 2^26 tokens, or so many sequences, heads, nodes and table entries
+ * that their 64-key tiles, at every sequence's largest, would pass 2^31, return
+ * PA_ERR_UNSUPPORTED.
  */
 PA_API size_t pa_decode_tree_workspace_size(int32_t num_splits);
 PA_API int32_t pa_decode_tree_default_splits(int32_t device);
@@ -937,6 +940,7 @@ PA_API pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
  *   sample_uniforms  fp32 [num_seqs], in [0, 1).
  *   draws          PA_DRAWS_WITHOUT_REPLACEMENT or PA_DRAWS_WITH_REPLACEMENT:
  *                  how siblings were drawn from their row.
+ *   vocab_size     at most 2^20 (else PA_ERR_UNSUPPORTED).
  *   error_flags    optional int32 word (may be NULL): rows outside [0,
  *                  total_tokens) or more than max_q_len nodes set
  *                  PA_DEVERR_SHAPE (accepted 0); a node whose parent is its own

@@ -6,11 +6,14 @@
 // kv head.
 //
 // A unit is a 128-row tile of one (sequence, kv head); its keys are cut into
-// 64-key tiles.  All units' tiles form one list (sequence, kv head, row tile),
-// which is cut evenly over the CTAs, two per SM: a CTA runs the last tiles of
-// one unit, some whole units and the first tiles of another.  A unit in one
-// piece is written to `out`; the pieces of a cut one leave (O / l, m + log2 l)
-// in the workspace, and tree_merge_kernel joins them.
+// 64-key tiles.  Units' tiles form lists (sequence, kv head, row tile) that are cut
+// evenly over the CTAs, two per SM: a CTA runs the last tiles of one unit, some
+// whole units and the first tiles of another.  A unit in one piece is written to
+// `out`; the pieces of a cut one leave (O / l, m + log2 l) in the workspace, and
+// tree_merge_kernel joins them.  Row tiles that share their keys go in twos to
+// neighbouring CTAs that read the same tiles at the same time, the second from L2:
+// one list of all of them read DRAM 1.8 times over and took 182 us for 4 trees of 64
+// nodes behind 32768 keys (32/8 heads), against 152.
 //
 // Roles of the 8 warps: 0 loads K tiles and 2 V tiles (TMA, two stages each),
 // 1 issues the score MMAs and owns the tensor memory (two score buffers of 64
@@ -22,9 +25,16 @@
 // nodes it sees by one walk up its parents, which goes on where the tile before
 // left it: no mask is ever stored, and the tree may have any size.
 //
-// P is kept as two bf16 terms, hi the truncated weight and lo the rounded rest
-// (together 16 bits), each with its PV MMA: one term's error (2^-9 of a weight)
-// is as large as the output's own rounding.
+// P is kept as two bf16 terms, the rounded weight and the rounded rest (together
+// 17 bits), each with its PV MMA: one term's error (2^-9 of a weight) is as large
+// as the output's own rounding.
+//
+// What bounds it.  Few rows: HBM (8 rows of each of 8 kv heads behind 4 x 32768 keys,
+// 537 MB, 91 us, 5.9 TB/s with a start and a merge of some 12).  Full row tiles: the
+// MMAs' chain (scores, softmax, PV, the next scores into the same buffer), 0.75 us a
+// tile alone and 1.4 us for the two CTAs of an SM together, of which the tensor
+// pipe is busy 68 % (the two P terms, and score MMAs bound by shared memory at N =
+// 64).  Small calls: latency, 9 us for one tile of one sequence.
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -39,19 +49,9 @@ constexpr int kTrPages = kPfKeys / kBlockSize;  // pages per KV tile
 constexpr int kTrHalf = kPfKeys * 128;          // 64 keys x 64 dims, 128-byte swizzle
 constexpr int kTrTile = 2 * kTrHalf;            // one K or V tile
 constexpr int kTrQHalf = kPfRows * 128;         // 128 rows x 64 dims of Q
-// K is needed a step before V of the same tile, and a loaded memory system takes
-// longer than a step: three K stages and two V stages, all the shared memory that
-// leaves room for two CTAs on an SM (so nothing is declared static).
-#ifndef TR_VST
-#define TR_VST 2
-#endif
-#ifndef TR_Z
-#define TR_Z 1
-#endif
-#ifndef TR_KST
-#define TR_KST 3
-#endif
-constexpr int kTrKStages = TR_KST, kTrVStages = TR_VST;
+// Two stages of each: a third of K, or of V, made no difference (within 1 % from
+// one tile to 16384), as the loads run a step and a half ahead of their MMAs.
+constexpr int kTrKStages = 2, kTrVStages = 2;
 constexpr int kTrOffQ = 0;
 constexpr int kTrOffK = kTrOffQ + 2 * kTrQHalf;
 constexpr int kTrOffV = kTrOffK + kTrKStages * kTrTile;
@@ -68,16 +68,15 @@ static_assert(2 * (kTrSmem + 1024) <= 228 * 1024, "two CTAs do not fit an SM");
 constexpr int kTrCols = 256;    // tensor memory columns: S_0 0.., S_1 64.., O 128..
 constexpr int kTrSCols = 64, kTrO = 128;
 
-#ifndef TR_PIECE
-#define TR_PIECE 4
-#endif
-#ifndef TR_MIN
-#define TR_MIN 4
-#endif
-// A piece's start and end cost about as much as this many tiles.
-constexpr int kTrPieceTiles = TR_PIECE;
-// A CTA's part of the list is at least this long.
-constexpr int kTrMinPart = TR_MIN;
+// A piece's start and end (Q, the first tile's masks, the rows' way out) cost about
+// as much as this many tiles: with 2 / 4 / 5 / 6 the 64 ragged sequences of
+// perf's "tree 64" took 27.6 / 23.5 / 24.0 / 23.4 us, its "chain long 6" 52.4 / 48.3 /
+// 47.7 / 47.2, its "tree 1" 15.9 / 12.6 / 12.8 / 13.5.
+constexpr int kTrPieceTiles = 5;
+// A part of the list is at least this long, less than a piece of no tiles at all: a
+// merge costs less than the tiles that it lets run side by side (with 3 / 4 / 6 / 8
+// "tree 1" took 12.2 / 12.5 / 13.8 / 14.4 us, "tree 8" 21.8 / 21.5 / 20.6 / 22.7).
+constexpr int kTrMinPart = 4;
 
 // What the merge has to know of CTA c's first piece, where it goes on with a unit
 // that an earlier CTA began: the unit's rows, CTAs first .. last and output rows.
@@ -86,9 +85,6 @@ struct TreeCut {
   int q0, g, mt, step, base;  // piece i of the unit is CTA base + step i's
 };
 
-#ifndef TR_X
-#define TR_X
-#endif
 struct TreeParams {
   void *out;
   int out_f32;
@@ -794,13 +790,12 @@ __global__ void __launch_bounds__(kTrThreads, 2)
             for (int i = 0; i < 8; ++i) {
               const float e0 = sv[cc >> 1][16 * (cc & 1) + 2 * i];
               const float e1 = sv[cc >> 1][16 * (cc & 1) + 2 * i + 1];
-              const uint32_t u0 = __float_as_uint(e0), u1 = __float_as_uint(e1);
-              hi[i] = __byte_perm(u0, u1, 0x7632);
+              hi[i] = float2_to_bf16x2(e0, e1);
               const uint64_t e2 = pack_f32x2(e0, e1);
               ps4[i & 3] = add_f32x2(ps4[i & 3], e2);
               float d0, d1;
-              unpack_f32x2(sub_f32x2(e2, pack_f32x2(__uint_as_float(u0 & 0xFFFF0000u),
-                                                    __uint_as_float(u1 & 0xFFFF0000u))),
+              unpack_f32x2(sub_f32x2(e2, pack_f32x2(__uint_as_float(hi[i] << 16),
+                                                    __uint_as_float(hi[i] & 0xFFFF0000u))),
                            d0, d1);
               lo[i] = float2_to_bf16x2(d0, d1);
             }
@@ -998,13 +993,12 @@ __global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreePar
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const TreeCut cut = p.cuts[blockIdx.y * p.splits + blockIdx.x];
   if (cut.rows == 0) return;
-  const int n = (cut.last - cut.first) * TR_Z;
-  const int i0 = ((int)blockIdx.x / cut.step - cut.first - 1) * TR_Z + (int)blockIdx.z;
-  const int pieces = cut.last - cut.first + 1;
+  const int n = cut.last - cut.first;
+  const int i0 = (int)blockIdx.x / cut.step - cut.first - 1;
   const int rows = (cut.rows - i0 + n - 1) / n;  // rows of this CTA
   // warps that share a row
   const int share = rows >= 5 ? 1 : rows >= 3 ? 2 : rows == 2 ? 4 : 8;
-  const int each = (pieces + share - 1) / share;  // pieces of a warp
+  const int each = (n + share) / share;  // pieces of a warp
   const int ca = cut.first + (warp % share) * each, cb = min(cut.last + 1, ca + each);
   if (share == 1 && each <= 4) {
     if (each <= 2)
@@ -1170,7 +1164,7 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
                     tv, p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   if (splits > 1 &&
-      launch_kernel(tree_merge_kernel, dim3((unsigned)splits, 2, TR_Z), dim3(32 * kTmWarps), 0, s, true,
+      launch_kernel(tree_merge_kernel, dim3((unsigned)splits, 2), dim3(32 * kTmWarps), 0, s, true,
                     p) != cudaSuccess)
     return PA_ERR_LAUNCH;
   return PA_OK;

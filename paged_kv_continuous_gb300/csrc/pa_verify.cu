@@ -19,9 +19,10 @@
 // sums carry more than fp32: a weight is an unevaluated pair of floats (the
 // product's and the difference's rounding errors kept), and pairs are added into
 // pairs, in lanes, warps and over the segments, some 20 fp32 operations an
-// element.  fp64 is for the tests of single nodes alone: its rate on this chip is
-// so low that joining lanes and segments in it took 61 us for 64 sequences of
-// 32000 tokens against 12 for one.
+// element.  The tests of single nodes are taken in pairs too (their products are
+// exact).  fp64, whose rate on this chip is low, took 61 us where 64 sequences of
+// 32000 tokens joined lanes and segments in it (now 8), and 1 to 2 us of a rejection
+// where a node's test was in it.
 //
 // Bound by latency for few sequences, and by HBM for many: a pass reads 8 bytes
 // an element.
@@ -39,9 +40,10 @@ namespace cg = cooperative_groups;
 constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32;
 constexpr int kVfMaxCluster = 8;
 constexpr int kVfSegments = kVfMaxCluster * kVfWarps;
+constexpr int kVfPer = kVfSegments / 32;  // segments of a lane, where a warp scans their sums
 constexpr int kVfNodes = 256;          // nodes whose elements are held at a time
 constexpr int kVfMaxVocab = 1 << 20;   // (a bit for each token, in shared memory)
-constexpr double kVfLeast = 1.0 / (1 << 24);
+constexpr float kVfLeast = 1.f / (1 << 24);
 
 struct VerifyParams {
   int32_t *accepted, *path, *out_tokens;
@@ -73,6 +75,21 @@ __device__ __forceinline__ Pair plus(const Pair &a, const Pair &b) {
   const float hi = s + e;
   return {hi, e - (hi - s)};
 }
+__device__ __forceinline__ Pair minus(const Pair &a, const Pair &b) {
+  return plus(a, {-b.hi, -b.lo});
+}
+// a b and a / b, within 2^-44.
+__device__ __forceinline__ Pair times(const Pair &a, const Pair &b) {
+  const float h = a.hi * b.hi;
+  const float l = fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi);
+  const float hi = h + l;
+  return {hi, l - (hi - h)};
+}
+__device__ __forceinline__ Pair over(const Pair &a, const Pair &b) {
+  const float x = a.hi / b.hi;
+  const Pair rest = minus(a, times({x, 0.f}, b));
+  return plus({x, 0.f}, {rest.hi / b.hi, 0.f});
+}
 __device__ __forceinline__ Pair shfl_up(const Pair &a, int by) {
   return {__shfl_up_sync(0xffffffffu, a.hi, by), __shfl_up_sync(0xffffffffu, a.lo, by)};
 }
@@ -93,8 +110,9 @@ __device__ __forceinline__ Pair warp_upto(Pair x) {
 __device__ __forceinline__ Pair weight(float p, float q, float bh, float bl) {
   const float ph = q * bh;
   const float pl = fmaf(q, bl, fmaf(q, bh, -ph));
-  const float s = p - ph, bb = s - p;
-  const float lo = ((p - (s - bb)) - (ph + bb)) - pl;  // p - ph = s + ...
+  // p - ph = s + ((p - s) - ph) where p >= ph; elsewhere nothing is left anyway
+  const float s = p - ph;
+  const float lo = ((p - s) - ph) - pl;
   const float hi = s + lo;
   return {hi > 0.f ? hi : 0.f, hi > 0.f ? lo - (hi - s) : 0.f};
 }
@@ -144,24 +162,27 @@ __device__ __forceinline__ void weights4(const Rows &r, const float (&p)[4], con
 }
 
 // The sum of a warp's segment [s0, s1): a lane's four tokens of every 128.
-template <bool kVec>
-__device__ Pair segment_sum(const Rows &r, int s0, int s1, const uint32_t *out) {
+template <bool kVec, bool kDraft>
+__device__ __forceinline__ Pair segment_sum_of(const Rows &r, int s0, int s1,
+                                               const uint32_t *out) {
   const int lane = threadIdx.x & 31;
   Pair acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-  constexpr int kAhead = 4;
-  for (int i0 = s0 + 4 * lane; i0 - 4 * lane < s1; i0 += 128 * kAhead) {
+  constexpr int kAhead = kDraft ? 4 : 8;  // rows of 128 tokens, the loads in flight
+  const Rows mine{r.p, kDraft ? r.q : nullptr, r.bh, r.bl};
+  for (int b = s0; b < s1; b += 128 * kAhead) {
+    const int i0 = b + 4 * lane;
     float p[kAhead][4], q[kAhead][4];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int i = i0 + 128 * a;
       load4<kVec>(r.p, i, s1 - i, p[a]);
-      if (r.q) load4<kVec>(r.q, i, s1 - i, q[a]);
+      if (kDraft) load4<kVec>(r.q, i, s1 - i, q[a]);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       Pair w[4];
-      if (i0 + 128 * a < s1) {
-        weights4(r, p[a], q[a], out, i0 + 128 * a, w);
+      if (b + 128 * a < s1) {
+        weights4(mine, p[a], q[a], out, i0 + 128 * a, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) add(acc[k], w[k]);
       }
@@ -174,59 +195,62 @@ __device__ Pair segment_sum(const Rows &r, int s0, int s1, const uint32_t *out) 
                      __shfl_xor_sync(0xffffffffu, sum.lo, o)});
   return sum;
 }
+template <bool kVec>
+__device__ __forceinline__ Pair segment_sum(const Rows &r, int s0, int s1, const uint32_t *out) {
+  return r.q ? segment_sum_of<kVec, true>(r, s0, s1, out)
+             : segment_sum_of<kVec, false>(r, s0, s1, out);
+}
 
 // The first token of segment [s0, s1) where `before` plus the running sum is over
-// `target`; its last of positive weight if there is none (-1: no such).
+// `target`; its last of positive weight if there is none (-1: no such).  The whole
+// CTA looks, a warp at 128 tokens: rows holds their sums, best what was found.
 template <bool kVec>
 __device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, Pair before,
-                            const Pair &target) {
-  const int lane = threadIdx.x & 31;
-  int last = -1;
-  constexpr int kAhead = 2;
-  for (int b = s0; b < s1; b += 128 * kAhead) {
-    float p[kAhead][4], q[kAhead][4];
+                            const Pair &target, Pair *rows, int *best) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    best[0] = INT_MAX;
+    best[1] = -1;
+  }
+  for (int b = s0; b < s1; b += 128 * kVfWarps) {
+    const int i = b + 128 * warp + 4 * lane;
+    float p[4], q[4];
+    Pair w[4], c[4];
+    load4<kVec>(r.p, i, s1 - i, p);
+    if (r.q) load4<kVec>(r.q, i, s1 - i, q);
+    weights4(r, p, q, out, i, w);
+    c[0] = w[0];
+    int last = -1;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = b + 128 * a + 4 * lane;
-      load4<kVec>(r.p, i, s1 - i, p[a]);
-      if (r.q) load4<kVec>(r.q, i, s1 - i, q[a]);
-    }
-    Pair upto[kAhead], c[kAhead][4];
-    int mine = -1;
+    for (int k = 1; k < 4; ++k) c[k] = plus(c[k - 1], w[k]);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int i = b + 128 * a + 4 * lane;
-      Pair w[4];
-      weights4(r, p[a], q[a], out, i, w);
-      c[a][0] = w[0];
-#pragma unroll
-      for (int k = 1; k < 4; ++k) c[a][k] = plus(c[a][k - 1], w[k]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (w[k].hi > 0.f)
-          mine = i + k;
-        else
-          c[a][k].hi = -1.f;  // (no token to draw: below any target)
-      }
-      Pair run = plus(plus(w[0], w[1]), plus(w[2], w[3]));
-      upto[a] = warp_upto(run);
-    }
+    for (int k = 0; k < 4; ++k)
+      if (w[k].hi > 0.f) last = i + k;
+    const Pair upto = warp_upto(c[3]);
+    if (lane == 31) rows[warp] = upto;
+    __syncthreads();
+    // the rows before this one, and all of them
+    const Pair sums = warp_upto(lane < kVfWarps ? rows[lane] : Pair{0.f, 0.f});
+    Pair base = shfl(sums, max(warp - 1, 0));
+    if (warp == 0) base = {0.f, 0.f};
+    const Pair here = plus(before, base);
+    Pair mine = shfl_up(upto, 1);
+    mine = lane == 0 ? here : plus(here, mine);
     int found = INT_MAX;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      Pair base = shfl_up(upto[a], 1);
-      base = lane == 0 ? before : plus(before, base);
-#pragma unroll
-      for (int k = 3; k >= 0; --k)
-        if (c[a][k].hi > 0.f && above(plus(base, c[a][k]), target))
-          found = min(found, b + 128 * a + 4 * lane + k);
-      before = plus(before, shfl(upto[a], 31));
-    }
+    for (int k = 3; k >= 0; --k)
+      if (w[k].hi > 0.f && above(plus(mine, c[k]), target)) found = i + k;
     found = __reduce_min_sync(0xffffffffu, found);
-    if (found != INT_MAX) return found;
-    last = max(last, __reduce_max_sync(0xffffffffu, mine));
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0) {
+      if (found != INT_MAX) atomicMin(best, found);
+      if (last >= 0) atomicMax(best + 1, last);
+    }
+    before = plus(before, shfl(sums, 31));
+    __syncthreads();
+    if (best[0] != INT_MAX) break;
   }
-  return last;
+  return best[0] != INT_MAX ? best[0] : best[1];
 }
 
 // All segments' sums into `sums` of every CTA of the cluster.  Alternate passes use
@@ -248,19 +272,18 @@ __device__ void sum_rows(cg::cluster_group &cluster, const Rows &r, const uint32
   __syncthreads();
 }
 
-// What lies before the lane's four segments and up to each of them; returns the
-// total.  Every warp of every CTA adds in the same order.
-__device__ __forceinline__ Pair scan_sums(const Pair *sums, Pair &before, Pair (&upto)[4]) {
-  static_assert(kVfSegments == 128, "four segments a lane");
+// What lies before the lane's segments and up to each of them; returns the total.
+// Every warp of every CTA adds in the same order.
+__device__ __forceinline__ Pair scan_sums(const Pair *sums, Pair &before, Pair (&upto)[kVfPer]) {
   const int lane = threadIdx.x & 31;
-  upto[0] = sums[4 * lane];
+  upto[0] = sums[kVfPer * lane];
 #pragma unroll
-  for (int k = 1; k < 4; ++k) upto[k] = plus(upto[k - 1], sums[4 * lane + k]);
-  before = shfl_up(warp_upto(upto[3]), 1);
+  for (int k = 1; k < kVfPer; ++k) upto[k] = plus(upto[k - 1], sums[kVfPer * lane + k]);
+  before = shfl_up(warp_upto(upto[kVfPer - 1]), 1);
   if (lane == 0) before = {0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) upto[k] = plus(before, upto[k]);
-  return shfl(upto[3], 31);
+  for (int k = 0; k < kVfPer; ++k) upto[k] = plus(before, upto[k]);
+  return shfl(upto[kVfPer - 1], 31);
 }
 
 template <bool kVec>
@@ -269,8 +292,8 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   __shared__ float n_u[kVfNodes], n_p[kVfNodes], n_q[kVfNodes];
   __shared__ Pair mine[2][kVfWarps];  // this CTA's segment sums, of alternate passes
   __shared__ Pair sums[kVfSegments];  // all CTAs', of the last pass
-  __shared__ double s_beta;
-  __shared__ int s_cur, s_act, s_next, s_count;
+  __shared__ Pair s_beta, s_rows[kVfWarps];
+  __shared__ int s_cur, s_act, s_next, s_count, s_best[2];
   extern __shared__ uint32_t out_bits[];  // looked-up guesses rejected at this node
   cg::cluster_group cluster = cg::this_cluster();
   griddep_wait();
@@ -304,7 +327,8 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   enum { kLoad, kPass, kSum, kDone };
   int cur = 0, count = 1, at = 0;  // node, nodes so far, last node looked at
   int held = 0, passes = 0;        // nodes held .. held + kVfNodes - 1 are there
-  double beta = 0.0, mass = 1.0, gone = 0.0;
+  const Pair zero = {0.f, 0.f}, one = {1.f, 0.f};
+  Pair beta = zero, mass = one, gone = zero;
   bool dirty = false;   // a bit of out_bits is set
   bool summed = false;  // `sums` are those of the present weights
   if (first && tid == 0) path[0] = 0;
@@ -312,7 +336,7 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
     s_act = nodes > 1 ? kLoad : kSum;
     s_next = 1;
     s_cur = 0;
-    s_beta = 0.0;
+    s_beta = zero;
     s_count = 1;
   }
   __syncthreads();
@@ -336,19 +360,18 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
       }
       __syncthreads();
     } else {  // kPass, kSum
-      const float bh = (float)s_beta, bl = (float)(s_beta - (double)bh);
       const long long row = q0 + s_cur;
-      const bool plain = looked || s_beta == 0.0;
-      const Rows r{p.p + row * p.p_stride, plain ? nullptr : p.q + row * p.q_stride, bh, bl};
+      const bool plain = looked || s_beta.hi == 0.f;
+      const Rows r{p.p + row * p.p_stride, plain ? nullptr : p.q + row * p.q_stride, s_beta.hi,
+                   s_beta.lo};
       const bool last = s_act == kSum;
       sum_rows<kVec>(cluster, r, looked ? out_bits : nullptr, s0, s1, mine, sums, passes++);
       if (last) break;
     }
     if (warp == 0) {
       if (s_act == kPass) {
-        Pair before, upto[4];
-        const Pair total = scan_sums(sums, before, upto);
-        mass = (double)total.hi + (double)total.lo;
+        Pair before, upto[kVfPer];
+        mass = scan_sums(sums, before, upto);
         summed = true;
       }
       int act = kLoad;
@@ -376,10 +399,11 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
         bool ok;
         if (looked) {
           const bool was = (out_bits[tok >> 5] >> (tok & 31)) & 1u;
-          const double px = was ? 0.0 : (double)n_p[j];
-          ok = (double)n_u[j] * mass < px;
+          const Pair px = {was ? 0.f : n_p[j], 0.f};
+          ok = above(px, times({n_u[j], 0.f}, mass));
           if (!ok) {
-            if (px > 0.0) mass = fmax(mass - px, 0.0);
+            if (px.hi > 0.f) mass = minus(mass, px);
+            if (!(mass.hi > 0.f)) mass = zero;
             __syncwarp();
             if (lane == 0) out_bits[tok >> 5] |= 1u << (tok & 31);
             __syncwarp();
@@ -387,12 +411,21 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
           }
         } else {
           // (the first child of a node: u q < p, exact)
-          const double left = gone == 0.0 ? 1.0 : fmax(1.0 - gone, kVfLeast);
-          const double qx = (double)n_q[j];
-          ok = (double)n_u[j] * qx * mass < left * fma(-beta, qx, (double)n_p[j]);
+          const bool sole = gone.hi == 0.f;
+          Pair left = one;
+          if (!sole) left = minus(one, gone);
+          if (left.hi < kVfLeast) left = {kVfLeast, 0.f};
+          const Pair qx = {n_q[j], 0.f};
+          Pair rest = {n_p[j], 0.f}, draw = times({n_u[j], 0.f}, qx);
+          if (beta.hi != 0.f) {
+            rest = minus(rest, times(beta, qx));
+            draw = times(draw, mass);
+            if (!sole) rest = times(rest, left);
+          }
+          ok = above(rest, draw);
           if (!ok) {
-            beta += gone == 0.0 ? mass : mass / left;
-            if (!p.again) gone += qx;
+            beta = plus(beta, sole ? mass : over(mass, left));
+            if (!p.again) gone = plus(gone, qx);
             act = kPass;
             break;
           }
@@ -404,8 +437,8 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
           }
           ++count;
           cur = at;
-          beta = gone = 0.0;
-          mass = 1.0;
+          beta = gone = zero;
+          mass = one;
           summed = false;
           if (dirty) {
             for (int i = lane; i < (p.vocab + 31) / 32; i += 32) out_bits[i] = 0u;
@@ -429,11 +462,10 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   // The token after: its segment by the sums, then the segment alone.
   count = s_count;
   const long long row = q0 + s_cur;
-  const float bh = (float)s_beta, bl = (float)(s_beta - (double)bh);
-  Rows r{p.p + row * p.p_stride, looked || s_beta == 0.0 ? nullptr : p.q + row * p.q_stride, bh,
-         bl};
+  Rows r{p.p + row * p.p_stride, looked || s_beta.hi == 0.f ? nullptr : p.q + row * p.q_stride,
+         s_beta.hi, s_beta.lo};
   const uint32_t *out = looked ? out_bits : nullptr;
-  Pair before, upto[4], total = scan_sums(sums, before, upto);
+  Pair before, upto[kVfPer], total = scan_sums(sums, before, upto);
   if (!(total.hi > 0.f)) {  // nothing left, by rounding alone: the target's row
     __syncthreads();        // all warps have read `sums`
     r.q = nullptr;
@@ -446,21 +478,24 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   const Pair target = {t2, tl - (t2 - th)};
   int seg = INT_MAX, filled = -1;
 #pragma unroll
-  for (int k = 3; k >= 0; --k) {
-    if (sums[4 * lane + k].hi > 0.f) {
-      filled = max(filled, 4 * lane + k);
-      if (above(upto[k], target)) seg = 4 * lane + k;
+  for (int k = kVfPer - 1; k >= 0; --k) {
+    if (sums[kVfPer * lane + k].hi > 0.f) {
+      filled = max(filled, kVfPer * lane + k);
+      if (above(upto[k], target)) seg = kVfPer * lane + k;
     }
   }
   seg = __reduce_min_sync(0xffffffffu, seg);
   filled = __reduce_max_sync(0xffffffffu, filled);
   if (seg == INT_MAX) seg = filled;  // -1: no weight at all
-  if (seg == rank * kVfWarps + warp) {
-    const int k = seg & 3;
-    const Pair at0 = shfl(k == 0 ? before : k == 1 ? upto[0] : k == 2 ? upto[1] : upto[2],
-                          seg >> 2);
-    const int tok = segment_find<kVec>(r, s0, s1, out, at0, target);
-    if (lane == 0) toks[count - 1] = tok;
+  if (seg >= 0 && seg / kVfWarps == rank) {  // (the whole CTA)
+    Pair at0 = before;
+#pragma unroll
+    for (int k = 1; k < kVfPer; ++k)
+      if (seg % kVfPer == k) at0 = upto[k - 1];
+    at0 = shfl(at0, seg / kVfPer);
+    const int f0 = seg * p.segment, f1 = min(p.vocab, f0 + p.segment);
+    const int tok = segment_find<kVec>(r, f0, f1, out, at0, target, s_rows, s_best);
+    if (tid == 0) toks[count - 1] = tok;
   }
   if (first) {
     if (tid == 0) {
@@ -472,11 +507,15 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   cluster.sync();  // no CTA leaves while another reads its sums
 }
 
-// CTAs of a cluster, for a vocabulary: a warp has 128 tokens at a time, and none
-// without any.
-int verify_ranks(int vocab) {
+// CTAs of a sequence's cluster: more while every warp then has a row of 128 tokens
+// and all clusters run at once, two CTAs per SM.  Measured for 64 sequences, four
+// against eight CTAs each: 18.6 / 34 us at 32000 tokens, 40 / 64 at 151936 (two:
+// 83); for 256 sequences, one against eight: 31 / 93.  CTAs of 1024 threads instead,
+// one per SM, took 25 / 21 us for 16 sequences and 11 / 7.4 for one.
+int verify_ranks(int vocab, int seqs, int sms) {
   int ranks = 1;
-  while (ranks < kVfMaxCluster && vocab > ranks * kVfWarps * 128) ranks *= 2;
+  while (ranks < kVfMaxCluster && vocab > ranks * kVfWarps * 128 && ranks * (long long)seqs <= sms)
+    ranks *= 2;
   return ranks;
 }
 
@@ -514,7 +553,10 @@ extern "C" pa_status pa_verify_tree(int32_t *accepted, int32_t *path, int32_t *o
     if (reinterpret_cast<uintptr_t>(x) & 3) return PA_ERR_INVALID_ARG;
   int device = -1;
   if (cudaGetDevice(&device) != cudaSuccess) return PA_ERR_DEVICE;
-  const int ranks = verify_ranks(vocab_size);
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return PA_ERR_DEVICE;
+  const int ranks = verify_ranks(vocab_size, num_seqs, sms);
   VerifyParams p;
   p.accepted = accepted;
   p.path = path;

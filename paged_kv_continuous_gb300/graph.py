@@ -152,3 +152,117 @@ class DecodeStepGraph:
     def read_error_word(self) -> int:
         """Device error bits of the store calls (and the decode workspace's)."""
         return int(self.error_word.item()) | ops.read_error_word(self.workspace)
+
+
+class TreeStepGraph:
+    """One speculative step over ``len(layers)`` layers: :meth:`replay` stores
+    the drafted nodes' K/V rows and attends to every sequence's tree in all
+    layers (one CUDA graph), and, once the target's probabilities of the nodes
+    are there, :meth:`verify` accepts a walk down each tree, draws the token
+    after it and commits the accepted rows in all pools (another).
+
+    layers: list of dicts with bf16 CUDA tensors ``q`` [T, Hq, D] (contiguous),
+    ``k``, ``v`` [T, Hkv, D] (the nodes' rows, packed by cu_seqlens), ``k_cache``,
+    ``v_cache`` (the layer's pools) and ``out`` [T, Hq, D].
+    cu_seqlens int32 [N + 1], parents, tokens, slot_mapping int32 [T],
+    block_tables int32 [N, max_blocks], context_lens int32 [N] (the nodes
+    included): the initial values of the static index buffers (copied).
+    target_probs (and draft_probs, if there are) float32 [T, V], uniforms
+    float32 [T] and sample_uniforms float32 [N]: read where they are.
+    ref_counts int32 [num_blocks]: the pages' counts, changed where they are.
+
+    After :meth:`verify`, ``context_lens`` holds the committed lengths, the
+    accepted nodes included: the next step's are those plus its trees' nodes.
+    """
+
+    def __init__(self, layers, cu_seqlens, parents, tokens, block_tables, context_lens,
+                 slot_mapping, scale, max_q_len, target_probs, uniforms, sample_uniforms,
+                 draft_probs=None, with_replacement=False, ref_counts=None, num_splits=0,
+                 device=None):
+        if not layers:
+            raise ops.PagedAttentionError("TreeStepGraph needs at least one layer")
+        dev = layers[0]["q"].device if device is None else torch.device(device)
+        self.layers = layers
+        i32 = lambda t: t.to(dev, torch.int32).clone()
+        # static index buffers: one copy, shared by every layer
+        self.cu_seqlens, self.parents, self.tokens = map(i32, (cu_seqlens, parents, tokens))
+        self.block_tables, self.context_lens = i32(block_tables), i32(context_lens)
+        self.slot_mapping = i32(slot_mapping)
+        self.error_word = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.workspace = ops.tree_workspace(num_splits, dev)
+        self._store = [(x["k"], x["v"], x["k_cache"], x["v_cache"]) for x in layers]
+        self._attend = [
+            ops.DecodeTreeCall(x["q"], self.cu_seqlens, self.parents, x["k_cache"], x["v_cache"],
+                               self.block_tables, self.context_lens, scale, max_q_len, x["out"],
+                               num_splits, self.workspace, pdl=True) for x in layers]
+        B = self.cu_seqlens.shape[0] - 1
+        self.accepted = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.path, self.out_tokens = (torch.full((B, int(max_q_len)), -1, dtype=torch.int32,
+                                                 device=dev) for _ in range(2))
+        self._verify = ops.VerifyTreeCall(
+            self.tokens, self.parents, self.cu_seqlens, target_probs, uniforms, sample_uniforms,
+            max_q_len, draft_probs, with_replacement, self.accepted, self.path, self.out_tokens,
+            self.error_word, pdl=True)
+        pools = ops.PagePools([x[name] for x in layers for name in ("k_cache", "v_cache")])
+        self._commit = ops.CommitTreeCall(pools, self.cu_seqlens, self.block_tables,
+                                          self.context_lens, self.path, self.accepted, ref_counts,
+                                          self.error_word, pdl=True)
+        self.stream = torch.cuda.Stream(device=dev)
+        self._graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+        self._capture(dev)
+
+    def _capture(self, dev):
+        # Eager calls first, so that no kernel's first launch falls into a capture.  They write
+        # what every replay rewrites; the commit's is one of a sequence without nodes.
+        self._attend[0]()
+        self._verify()
+        none = torch.zeros(2, dtype=torch.int32, device=dev)
+        page = torch.zeros((1, 16, 16), dtype=torch.uint8, device=dev)
+        ops.commit_tree(ops.PagePools([page]), none, none[:1].view(1, 1), none[:1],
+                        none[:1].view(1, 1), none[:1])
+        torch.cuda.synchronize()
+        self.error_word.zero_()  # (the tensors may hold anything yet)
+        self.workspace[:4].zero_()
+        self.stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(self._graphs[0], stream=self.stream):
+            for rows, attend in zip(self._store, self._attend):
+                ops.store_kv(*rows, self.slot_mapping, error_flags=self.error_word, pdl=True)
+                attend()
+        with torch.cuda.graph(self._graphs[1], stream=self.stream):
+            self._verify()
+            self._commit()
+        torch.cuda.current_stream().wait_stream(self.stream)
+
+    def update(self, cu_seqlens=None, parents=None, tokens=None, block_tables=None,
+               context_lens=None, slot_mapping=None):
+        """Write new values into the static index buffers (same shapes), in
+        stream order before the next replay.  Trees may have other sizes as long
+        as they fit the rows and max_q_len."""
+        for src, dst, name in ((cu_seqlens, self.cu_seqlens, "cu_seqlens"),
+                               (parents, self.parents, "parents"),
+                               (tokens, self.tokens, "tokens"),
+                               (block_tables, self.block_tables, "block_tables"),
+                               (context_lens, self.context_lens, "context_lens"),
+                               (slot_mapping, self.slot_mapping, "slot_mapping")):
+            if src is None:
+                continue
+            if tuple(src.shape) != tuple(dst.shape):
+                raise ops.PagedAttentionError(
+                    f"{name} has shape {tuple(src.shape)}; the graph was captured with "
+                    f"{tuple(dst.shape)}")
+            dst.copy_(src.to(torch.int32), non_blocking=True)
+
+    def replay(self):
+        """Run the layers' stores and attention on the current stream."""
+        self._graphs[0].replay()
+
+    def verify(self):
+        """Verify and commit on the current stream (once a step, after
+        :meth:`replay` and the target's probabilities).  Returns the static
+        (accepted [N], path [N, max_q_len], out_tokens [N, max_q_len])."""
+        self._graphs[1].replay()
+        return self.accepted, self.path, self.out_tokens
+
+    def read_error_word(self) -> int:
+        """Device error bits of the calls so far."""
+        return int(self.error_word.item()) | ops.read_error_word(self.workspace)

@@ -50,6 +50,7 @@ def test_decode_tree(lib):
     assert call(d=64) == UNSUPPORTED and call(bs=32) == UNSUPPORTED
     assert call(hkv=3) == UNSUPPORTED and call(hq=13) == UNSUPPORTED
     assert call(hq=18) == UNSUPPORTED and call(hq=1) == UNSUPPORTED
+    assert call(total=(1 << 26) + 1) == UNSUPPORTED
     for name in ("out", "q", "kc", "vc", "ws"):
         assert call(**{name: FAKE + 8}) == INVALID, name
     for name in ("cu", "par", "bt", "ctx"):
