@@ -37,10 +37,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32;
-constexpr int kVfMaxCluster = 8;
-constexpr int kVfSegments = kVfMaxCluster * kVfWarps;
-constexpr int kVfPer = kVfSegments / 32;  // segments of a lane, where a warp scans their sums
+constexpr int kVfThreads = 256, kVfWarps = kVfThreads / 32;
 constexpr int kVfNodes = 256;          // nodes whose elements are held at a time
 constexpr int kVfMaxVocab = 1 << 20;   // (a bit for each token, in shared memory)
 constexpr float kVfLeast = 1.f / (1 << 24);
@@ -256,14 +253,14 @@ __device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, 
 // All segments' sums into `sums` of every CTA of the cluster.  Alternate passes use
 // alternate halves of `mine`: a CTA still reads one pass's while another writes the
 // next one's, and the pass after that waits for it at the barrier between.
-template <bool kVec>
+template <bool kVec, int kRanks>
 __device__ void sum_rows(cg::cluster_group &cluster, const Rows &r, const uint32_t *out, int s0,
                          int s1, Pair (&mine)[2][kVfWarps], Pair *sums, int pass) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const Pair sum = segment_sum<kVec>(r, s0, s1, out);
   if ((tid & 31) == 0) mine[pass & 1][warp] = sum;
   cluster.sync();
-  if (tid < kVfSegments) {
+  if (tid < kRanks * kVfWarps) {
     const int from = tid / kVfWarps;
     sums[tid] = from < (int)cluster.num_blocks()
                     ? *cluster.map_shared_rank(&mine[pass & 1][tid % kVfWarps], from)
@@ -274,24 +271,29 @@ __device__ void sum_rows(cg::cluster_group &cluster, const Rows &r, const uint32
 
 // What lies before the lane's segments and up to each of them; returns the total.
 // Every warp of every CTA adds in the same order.
-__device__ __forceinline__ Pair scan_sums(const Pair *sums, Pair &before, Pair (&upto)[kVfPer]) {
+template <int kPer>
+__device__ __forceinline__ Pair scan_sums(const Pair *sums, Pair &before, Pair (&upto)[kPer]) {
   const int lane = threadIdx.x & 31;
-  upto[0] = sums[kVfPer * lane];
+  upto[0] = sums[kPer * lane];
 #pragma unroll
-  for (int k = 1; k < kVfPer; ++k) upto[k] = plus(upto[k - 1], sums[kVfPer * lane + k]);
-  before = shfl_up(warp_upto(upto[kVfPer - 1]), 1);
+  for (int k = 1; k < kPer; ++k) upto[k] = plus(upto[k - 1], sums[kPer * lane + k]);
+  before = shfl_up(warp_upto(upto[kPer - 1]), 1);
   if (lane == 0) before = {0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < kVfPer; ++k) upto[k] = plus(before, upto[k]);
-  return shfl(upto[kVfPer - 1], 31);
+  for (int k = 0; k < kPer; ++k) upto[k] = plus(before, upto[k]);
+  return shfl(upto[kPer - 1], 31);
 }
 
-template <bool kVec>
-__global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParams p) {
+// kRanks: CTAs of a cluster, at most.
+template <bool kVec, int kRanks>
+__global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyParams p) {
   __shared__ int n_par[kVfNodes], n_tok[kVfNodes];
   __shared__ float n_u[kVfNodes], n_p[kVfNodes], n_q[kVfNodes];
   __shared__ Pair mine[2][kVfWarps];  // this CTA's segment sums, of alternate passes
-  __shared__ Pair sums[kVfSegments];  // all CTAs', of the last pass
+  // segments of a lane, where a warp scans their sums
+  constexpr int kPer = kRanks * kVfWarps / 32;
+  static_assert(kRanks * kVfWarps <= kVfThreads, "a thread fetches each segment's sum");
+  __shared__ Pair sums[kRanks * kVfWarps];  // all CTAs', of the last pass
   __shared__ Pair s_beta, s_rows[kVfWarps];
   __shared__ int s_cur, s_act, s_next, s_count, s_best[2];
   extern __shared__ uint32_t out_bits[];  // looked-up guesses rejected at this node
@@ -365,12 +367,12 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
       const Rows r{p.p + row * p.p_stride, plain ? nullptr : p.q + row * p.q_stride, s_beta.hi,
                    s_beta.lo};
       const bool last = s_act == kSum;
-      sum_rows<kVec>(cluster, r, looked ? out_bits : nullptr, s0, s1, mine, sums, passes++);
+      sum_rows<kVec, kRanks>(cluster, r, looked ? out_bits : nullptr, s0, s1, mine, sums, passes++);
       if (last) break;
     }
     if (warp == 0) {
       if (s_act == kPass) {
-        Pair before, upto[kVfPer];
+        Pair before, upto[kPer];
         mass = scan_sums(sums, before, upto);
         summed = true;
       }
@@ -465,12 +467,12 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   Rows r{p.p + row * p.p_stride, looked || s_beta.hi == 0.f ? nullptr : p.q + row * p.q_stride,
          s_beta.hi, s_beta.lo};
   const uint32_t *out = looked ? out_bits : nullptr;
-  Pair before, upto[kVfPer], total = scan_sums(sums, before, upto);
+  Pair before, upto[kPer], total = scan_sums(sums, before, upto);
   if (!(total.hi > 0.f)) {  // nothing left, by rounding alone: the target's row
     __syncthreads();        // all warps have read `sums`
     r.q = nullptr;
     out = nullptr;
-    sum_rows<kVec>(cluster, r, out, s0, s1, mine, sums, passes++);
+    sum_rows<kVec, kRanks>(cluster, r, out, s0, s1, mine, sums, passes++);
     total = scan_sums(sums, before, upto);
   }
   const float ul = p.u_last[seq], th = ul * total.hi;  // u' times the total
@@ -478,10 +480,10 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   const Pair target = {t2, tl - (t2 - th)};
   int seg = INT_MAX, filled = -1;
 #pragma unroll
-  for (int k = kVfPer - 1; k >= 0; --k) {
-    if (sums[kVfPer * lane + k].hi > 0.f) {
-      filled = max(filled, kVfPer * lane + k);
-      if (above(upto[k], target)) seg = kVfPer * lane + k;
+  for (int k = kPer - 1; k >= 0; --k) {
+    if (sums[kPer * lane + k].hi > 0.f) {
+      filled = max(filled, kPer * lane + k);
+      if (above(upto[k], target)) seg = kPer * lane + k;
     }
   }
   seg = __reduce_min_sync(0xffffffffu, seg);
@@ -490,9 +492,9 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
   if (seg >= 0 && seg / kVfWarps == rank) {  // (the whole CTA)
     Pair at0 = before;
 #pragma unroll
-    for (int k = 1; k < kVfPer; ++k)
-      if (seg % kVfPer == k) at0 = upto[k - 1];
-    at0 = shfl(at0, seg / kVfPer);
+    for (int k = 1; k < kPer; ++k)
+      if (seg % kPer == k) at0 = upto[k - 1];
+    at0 = shfl(at0, seg / kPer);
     const int f0 = seg * p.segment, f1 = min(p.vocab, f0 + p.segment);
     const int tok = segment_find<kVec>(r, f0, f1, out, at0, target, s_rows, s_best);
     if (tid == 0) toks[count - 1] = tok;
@@ -508,15 +510,34 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VerifyParam
 }
 
 // CTAs of a sequence's cluster: more while every warp then has a row of 128 tokens
-// and all clusters run at once, two CTAs per SM.  Measured for 64 sequences, four
-// against eight CTAs each: 18.6 / 34 us at 32000 tokens, 40 / 64 at 151936 (two:
-// 83); for 256 sequences, one against eight: 31 / 93.  CTAs of 1024 threads instead,
-// one per SM, took 25 / 21 us for 16 sequences and 11 / 7.4 for one.
+// and all clusters run at once, four CTAs per SM; sixteen (more than is portable)
+// only where a warp still has four rows.  Measured, us: 64 sequences at 151936
+// tokens, 8 CTAs of 256 threads 35 (4 of 512 40, 8 of 512 64, 16 of 128 36); 16 at
+// 128000, 16 CTAs 19.5, 8 23.2; one at 32000, 8 CTAs 6.3, 16 7.0; 256 at 32000, 2 CTAs
+// 27.5, one of 512 threads 31, 8 of 512 93.
+constexpr int kVfRanks = 8, kVfMoreRanks = 16;
 int verify_ranks(int vocab, int seqs, int sms) {
   int ranks = 1;
-  while (ranks < kVfMaxCluster && vocab > ranks * kVfWarps * 128 && ranks * (long long)seqs <= sms)
+  while (ranks < kVfRanks && vocab > ranks * kVfWarps * 128 && ranks * (long long)seqs <= 2 * sms)
     ranks *= 2;
+  if (ranks == kVfRanks && vocab >= kVfMoreRanks * kVfWarps * 512 &&
+      kVfMoreRanks * (long long)seqs <= 4 * sms)
+    ranks = kVfMoreRanks;
   return ranks;
+}
+
+template <bool kVec, int kRanks>
+cudaError_t launch_verify(const VerifyParams &p, int ranks, size_t bits, int device,
+                          cudaStream_t s) {
+  static std::atomic<bool> configured[64] = {};
+  cudaError_t e =
+      set_smem_once(configured, verify_kernel<kVec, kRanks>, device, kVfMaxVocab / 8);
+  if (e == cudaSuccess && kRanks > 8)
+    e = cudaFuncSetAttribute(verify_kernel<kVec, kRanks>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(verify_kernel<kVec, kRanks>, dim3((unsigned)(p.num_seqs * ranks)),
+                        dim3(kVfThreads), (unsigned)ranks, bits, s, p);
 }
 
 }  // namespace
@@ -538,7 +559,7 @@ extern "C" pa_status pa_verify_tree(int32_t *accepted, int32_t *path, int32_t *o
     return PA_ERR_INVALID_ARG;
   if (vocab_size > kVfMaxVocab) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
-  if (num_seqs > INT_MAX / kVfMaxCluster) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > INT_MAX / kVfMoreRanks) return PA_ERR_UNSUPPORTED;
   if (!accepted || !cu_seqlens || !sample_uniforms) return PA_ERR_INVALID_ARG;
   if (max_q_len > 0 && (!path || !out_tokens)) return PA_ERR_INVALID_ARG;
   if (total_tokens > 0 && (!tokens || !parents || !target_probs || !uniforms || vocab_size < 1))
@@ -582,14 +603,13 @@ extern "C" pa_status pa_verify_tree(int32_t *accepted, int32_t *path, int32_t *o
                      reinterpret_cast<uintptr_t>(draft_probs)) % 16 == 0) &&
                    target_stride % 4 == 0 && (!draft_probs || draft_stride % 4 == 0);
   const size_t bits = draft_probs ? 0 : (size_t)(vocab_size + 31) / 32 * 4;
-  constexpr int kMostBits = kVfMaxVocab / 8;
-  static std::atomic<bool> set_vec[64] = {}, set_any[64] = {};
-  const cudaError_t e = vec ? set_smem_once(set_vec, verify_kernel<true>, device, kMostBits)
-                            : set_smem_once(set_any, verify_kernel<false>, device, kMostBits);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      ranks <= kVfRanks
+          ? vec ? launch_verify<true, kVfRanks>(p, ranks, bits, device, st)
+                : launch_verify<false, kVfRanks>(p, ranks, bits, device, st)
+          : vec ? launch_verify<true, kVfMoreRanks>(p, ranks, bits, device, st)
+                : launch_verify<false, kVfMoreRanks>(p, ranks, bits, device, st);
   if (e != cudaSuccess) return PA_ERR_LAUNCH;
-  if (launch_cluster(vec ? verify_kernel<true> : verify_kernel<false>,
-                     dim3((unsigned)(num_seqs * ranks)), dim3(kVfThreads), (unsigned)ranks, bits,
-                     static_cast<cudaStream_t>(stream), p) != cudaSuccess)
-    return PA_ERR_LAUNCH;
   return PA_OK;
 }
