@@ -912,7 +912,7 @@ __device__ __forceinline__ void row_add(RowSum &a, float w, const float4 &o) {
 
 // Pieces x .. x + kPieces - 1 (below cb) of kRows rows (below 0: none), all loads first.
 template <int kRows, int kPieces>
-__device__ __forceinline__ void add_pieces(const TreeParams &p, const TreeCut &cut,
+__device__ __forceinline__ void add_pieces(const TreeParams &p, const TreeCut &cut, int list,
                                            const int (&row)[kRows], int x, int cb,
                                            RowSum *const (&a)[kRows]) {
   const int lane = threadIdx.x & 31;
@@ -925,7 +925,7 @@ __device__ __forceinline__ void add_pieces(const TreeParams &p, const TreeCut &c
       lse[k][i] = -INFINITY;
       o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row[k] >= 0 && x + i < cb) {
-        const long long slot = ((2 * blockIdx.y + (x + i == cut.first)) * (long long)p.splits +
+        const long long slot = ((2 * list + (x + i == cut.first)) * (long long)p.splits +
                                 cut.base + (long long)cut.step * (x + i)) * kPfRows + row[k];
         lse[k][i] = p.part_lse[slot];
         o[k][i] = reinterpret_cast<const float4 *>(p.part_o + slot * kHeadDim)[lane];
@@ -966,7 +966,8 @@ __device__ __forceinline__ void write_row(const TreeParams &p, const TreeCut &cu
 
 // The CTA's rows, kRows at a time by a warp, of kPieces pieces at most.
 template <int kRows, int kPieces>
-__device__ __forceinline__ void merge_rows(const TreeParams &p, const TreeCut &cut, int n, int i0,
+__device__ __forceinline__ void merge_rows(const TreeParams &p, const TreeCut &cut, int list,
+                                           int n, int i0,
                                            int rows, int warp) {
   for (int k = warp * kRows; k < rows; k += kTmWarps * kRows) {
     int row[kRows];
@@ -978,33 +979,30 @@ __device__ __forceinline__ void merge_rows(const TreeParams &p, const TreeCut &c
       s[j] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       to[j] = &s[j];
     }
-    add_pieces<kRows, kPieces>(p, cut, row, cut.first, cut.last + 1, to);
+    add_pieces<kRows, kPieces>(p, cut, list, row, cut.first, cut.last + 1, to);
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
       if (row[j] >= 0) write_row(p, cut, row[j], s[j]);
   }
 }
 
-__global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreeParams p) {
+__device__ __forceinline__ void merge_cut(const TreeParams &p, const TreeCut &cut, int list) {
   __shared__ float share_m[kTmWarps], share_w[kTmWarps];
   __shared__ float4 share_o[kTmWarps][32];
-  griddep_wait();
-  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const TreeCut cut = p.cuts[blockIdx.y * p.splits + blockIdx.x];
-  if (cut.rows == 0) return;
   const int n = cut.last - cut.first;
   const int i0 = (int)blockIdx.x / cut.step - cut.first - 1;
   const int rows = (cut.rows - i0 + n - 1) / n;  // rows of this CTA
   // warps that share a row
-  const int share = rows >= 5 ? 1 : rows >= 3 ? 2 : rows == 2 ? 4 : 8;
+  const int share = rows > kTmWarps / 2 ? 1 : rows > kTmWarps / 4 ? 2 : rows > kTmWarps / 8 ? 4
+                    : rows > kTmWarps / 16 ? 8 : kTmWarps;
   const int each = (n + share) / share;  // pieces of a warp
   const int ca = cut.first + (warp % share) * each, cb = min(cut.last + 1, ca + each);
   if (share == 1 && each <= 4) {
     if (each <= 2)
-      merge_rows<4, 2>(p, cut, n, i0, rows, warp);
+      merge_rows<4, 2>(p, cut, list, n, i0, rows, warp);
     else
-      merge_rows<2, 4>(p, cut, n, i0, rows, warp);
+      merge_rows<2, 4>(p, cut, list, n, i0, rows, warp);
     return;
   }
   for (int k = 0; k < rows; k += kTmWarps / share) {
@@ -1015,7 +1013,7 @@ __global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreePar
       for (int x = ca; x < cb; x += 8) {
         const int row[1] = {r};
         RowSum *one[1] = {&a};
-        add_pieces<1, 8>(p, cut, row, x, cb, one);
+        add_pieces<1, 8>(p, cut, list, row, x, cb, one);
       }
     if (share > 1) {
       share_o[warp][lane] = a.o;
@@ -1044,6 +1042,16 @@ __global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreePar
     }
     if (!mine || warp % share != 0) continue;
     write_row(p, cut, r, a);
+  }
+}
+
+__global__ void __launch_bounds__(32 * kTmWarps) tree_merge_kernel(const TreeParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  {
+    const int list = blockIdx.y;
+    const TreeCut cut = p.cuts[list * p.splits + blockIdx.x];
+    if (cut.rows) merge_cut(p, cut, list);
   }
 }
 
