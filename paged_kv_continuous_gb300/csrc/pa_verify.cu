@@ -103,7 +103,9 @@ __device__ __forceinline__ Pair warp_upto(Pair x) {
   return x;
 }
 
-// max(p - beta q, 0) as a pair, beta = bh + bl.
+// max(p - beta q, 0) as a pair, beta = bh + bl; where it is only added up, hi need
+// not be the sum's rounding.
+template <bool kRounded>
 __device__ __forceinline__ Pair weight(float p, float q, float bh, float bl) {
   const float ph = q * bh;
   const float pl = fmaf(q, bl, fmaf(q, bh, -ph));
@@ -111,6 +113,7 @@ __device__ __forceinline__ Pair weight(float p, float q, float bh, float bl) {
   const float s = p - ph;
   const float lo = ((p - s) - ph) - pl;
   const float hi = s + lo;
+  if constexpr (!kRounded) return {hi > 0.f ? s : 0.f, hi > 0.f ? lo : 0.f};
   return {hi > 0.f ? hi : 0.f, hi > 0.f ? lo - (hi - s) : 0.f};
 }
 // a + x without bringing hi up to date: x's low part and the error go to lo.
@@ -145,12 +148,13 @@ __device__ __forceinline__ void load4(const float *row, int i, int n, float (&v)
   }
 }
 // Their weights; a bit of `out` (where there are such) marks a rejected guess.
+template <bool kRounded>
 __device__ __forceinline__ void weights4(const Rows &r, const float (&p)[4], const float (&q)[4],
                                          const uint32_t *out, int i, Pair (&w)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (r.q) {
-      w[k] = weight(p[k], q[k], r.bh, r.bl);
+      w[k] = weight<kRounded>(p[k], q[k], r.bh, r.bl);
     } else {
       const bool pos = p[k] > 0.f && !(out && ((out[(i + k) >> 5] >> ((i + k) & 31)) & 1u));
       w[k] = {pos ? p[k] : 0.f, 0.f};
@@ -179,7 +183,7 @@ __device__ __forceinline__ Pair segment_sum_of(const Rows &r, int s0, int s1,
     for (int a = 0; a < kAhead; ++a) {
       Pair w[4];
       if (b + 128 * a < s1) {
-        weights4(mine, p[a], q[a], out, i0 + 128 * a, w);
+        weights4<false>(mine, p[a], q[a], out, i0 + 128 * a, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) add(acc[k], w[k]);
       }
@@ -215,7 +219,7 @@ __device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, 
     Pair w[4], c[4];
     load4<kVec>(r.p, i, s1 - i, p);
     if (r.q) load4<kVec>(r.q, i, s1 - i, q);
-    weights4(r, p, q, out, i, w);
+    weights4<true>(r, p, q, out, i, w);
     c[0] = w[0];
     int last = -1;
 #pragma unroll
