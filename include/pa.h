@@ -869,8 +869,8 @@ PA_API pa_status pa_prefill_fp8_block(
  *   max_q_len      upper bound of every T.
  *   context_lens   int32 [num_seqs], the nodes included.
  *   scale          any finite value, of either sign.
- *   num_splits     CTAs that share the work (at most PA_DECODE_MAX_SPLITS); 0 = as many of
- *                  pa_decode_tree_default_splits as suit the work they find.
+ *   num_splits     CTAs that share the work, at most PA_DECODE_MAX_SPLITS;
+ *                  0 = pa_decode_tree_default_splits (two per SM).
  *   workspace      >= pa_decode_tree_workspace_size(S) bytes, 16-byte aligned,
  *                  S = num_splits or the default: int32 error word at byte 0
  *                  (zero it once; the library only ORs bits in), the rest is

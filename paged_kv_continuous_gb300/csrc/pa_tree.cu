@@ -69,14 +69,10 @@ constexpr int kTrCols = 256;    // tensor memory columns: S_0 0.., S_1 64.., O 1
 constexpr int kTrSCols = 64, kTrO = 128;
 
 // A piece's start and end (Q, the first tile's masks, the rows' way out) cost about
-// as much as this many tiles: with 2 / 4 / 5 / 6 the 64 ragged sequences of
-// perf's "tree 64" took 27.6 / 23.5 / 24.0 / 23.4 us, its "chain long 6" 52.4 / 48.3 /
-// 47.7 / 47.2, its "tree 1" 15.9 / 12.6 / 12.8 / 13.5.
+// as much as this many tiles: with 2 / 4 / 5 / 6, 64 trees of up to 8 nodes behind 1 to
+// 8192 keys (12/2 heads) took 27.6 / 23.5 / 24.0 / 23.4 us, six chains behind 9 to 30
+// thousand (20/4 heads) 52.4 / 48.3 / 47.7 / 47.2.
 constexpr int kTrPieceTiles = 5;
-// A part of the list is at least this long, less than a piece of no tiles at all: a
-// merge costs less than the tiles that it lets run side by side (with 3 / 4 / 6 / 8
-// "tree 1" took 12.2 / 12.5 / 13.8 / 14.4 us, "tree 8" 21.8 / 21.5 / 20.6 / 22.7).
-constexpr int kTrMinPart = 4;
 
 // What the merge has to know of CTA c's first piece, where it goes on with a unit
 // that an earlier CTA began: the unit's rows, CTAs first .. last and output rows.
@@ -101,7 +97,6 @@ struct TreeParams {
   float scale_log2;       // > 0: a scale <= 0 is folded into q as staged
   uint32_t q_and, q_xor;  // staged q pairs = (q & q_and) ^ q_xor
   int splits;             // CTAs of the launch
-  int min_part;
   int pairs;              // splits / 2
   TreeCut *cuts;          // [2 lists][splits]
   float *part_o;          // [2 lists][2][splits][128 rows][128]
@@ -159,9 +154,12 @@ __device__ __forceinline__ void head_weight(const TreeParams &p, const TreeSeq &
   for (int i = two; i < m; ++i) w[1] += unit_tiles(p, q, i) + kTrPieceTiles;
 }
 
-// A list is cut into parts of this length, while it lasts.
-__device__ __forceinline__ int part_length(const TreeParams &p, int N, int parts) {
-  return max(p.min_part, (int)(((unsigned)N + (unsigned)parts - 1u) / (unsigned)parts));
+// A list is cut into parts of this length, while it lasts: down to a tile each, since
+// tiles side by side save more than a merge of more pieces costs (parts of four
+// tiles at least took 13.0 us for one sequence of 308 keys, against 11.3, 15.5 / 13.3
+// for one of 2000; no difference from 600 tiles on).
+__device__ __forceinline__ int part_length(int N, int parts) {
+  return (int)(((unsigned)N + (unsigned)parts - 1u) / (unsigned)parts);
 }
 __device__ __forceinline__ int part_of(int x, int len) {
   return (int)((unsigned)x / (unsigned)len);
@@ -272,7 +270,7 @@ __device__ __forceinline__ void tree_plan(const TreeParams &p, TreePlace (&place
     r.x = r.end = 0;
     len[l] = 1;
     if (N == 0 || part >= parts) continue;
-    len[l] = part_length(p, N, parts);
+    len[l] = part_length(N, parts);
     if (part > (N - 1) / len[l]) continue;
     const int x0 = part * len[l];
     const unsigned has = __ballot_sync(kAll, x0 >= upto[l] - mine[l] && x0 < upto[l]);
@@ -1112,6 +1110,12 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
   if (off(out, 16) || off(q, 16) || off(k_cache, 16) || off(v_cache, 16) || off(workspace, 16) ||
       off(cu_seqlens, 4) || off(parents, 4) || off(block_tables, 4) || off(context_lens, 4))
     return PA_ERR_INVALID_ARG;
+  // the lists' lengths fit an int, whatever the lengths on the device
+  const long long most_tiles = (long long)block_table_stride * kBlockSize / kPfKeys + 2;
+  const long long most_nodes = max_q_len < total_tokens ? max_q_len : total_tokens;
+  const long long rows = (most_nodes * (num_q_heads / num_kv_heads) + kPfRows - 1) / kPfRows;
+  if (most_tiles + kTrPieceTiles > (1ll << 31) / num_kv_heads / rows / num_seqs)
+    return PA_ERR_UNSUPPORTED;
   if (!workspace) return PA_ERR_WORKSPACE;
   if (num_splits > 0 && workspace_bytes < tree_workspace(num_splits)) return PA_ERR_WORKSPACE;
   int device = -1;
@@ -1129,12 +1133,6 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
   if (set_smem_once(configured, tree_kernel, device, kTrSmem) != cudaSuccess) return PA_ERR_LAUNCH;
   // two CTAs per SM: all of the unified L1 / shared memory as shared memory (a hint)
   cudaFuncSetAttribute(tree_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  // the lists' lengths fit an int, whatever the lengths on the device
-  const long long most_tiles = (long long)block_table_stride * kBlockSize / kPfKeys + 2;
-  const long long most_nodes = max_q_len < total_tokens ? max_q_len : total_tokens;
-  const long long rows = (most_nodes * (num_q_heads / num_kv_heads) + kPfRows - 1) / kPfRows;
-  if (most_tiles + kTrPieceTiles > (1ll << 31) / num_kv_heads / rows / num_seqs)
-    return PA_ERR_UNSUPPORTED;
   char *ws = static_cast<char *>(workspace);
   TreeParams p;
   p.out = out;
@@ -1161,7 +1159,6 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
   p.q_xor = scale < 0.f ? 0x80008000u : 0u;
   p.splits = splits;
   p.pairs = splits / 2;
-  p.min_part = num_splits > 0 ? 1 : kTrMinPart;
   p.part_o = reinterpret_cast<float *>(ws + kTrHead);
   p.part_lse = reinterpret_cast<float *>(ws + kTrHead + tree_part_bytes(splits));
   p.cuts = reinterpret_cast<TreeCut *>(ws + kTrHead + tree_part_bytes(splits) +

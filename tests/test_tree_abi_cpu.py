@@ -51,6 +51,8 @@ def test_decode_tree(lib):
     assert call(hkv=3) == UNSUPPORTED and call(hq=13) == UNSUPPORTED
     assert call(hq=18) == UNSUPPORTED and call(hq=1) == UNSUPPORTED
     assert call(total=(1 << 26) + 1) == UNSUPPORTED
+    # lists of tiles past an int: 1000 sequences of 2^27 table entries each
+    assert call(num_seqs=1000, stride=1 << 27) == UNSUPPORTED
     for name in ("out", "q", "kc", "vc", "ws"):
         assert call(**{name: FAKE + 8}) == INVALID, name
     for name in ("cu", "par", "bt", "ctx"):
