@@ -27,7 +27,15 @@
 //
 // P is kept as two bf16 terms, the rounded weight and the rounded rest (together
 // 17 bits), each with its PV MMA: one term's error (2^-9 of a weight) is as large
-// as the output's own rounding.
+// as a bf16 output's own rounding.  A third term for fp32 outputs (in shared memory,
+// 146 to 181 us for the case above) left them as far off, 4e-6 of their size: what
+// remains is the tensor cores' own accumulation.
+//
+// Registers are what the softmax threads are short of (128 with two CTAs per SM):
+// Q goes to shared memory without them (cp.async), a warp's place in the list waits
+// there while it works on a piece, and exponentials are taken where they are split.
+// Spills cost more than their instructions in calls of a few tiles (their first
+// touch misses): 11.4 to 10.9 us for 308 keys, 150 to 144 for the case above.
 //
 // What bounds it.  Few rows: HBM (8 rows of each of 8 kv heads behind 4 x 32768 keys,
 // 537 MB, 91 us, 5.9 TB/s with a start and a merge of some 12).  Full row tiles: the
@@ -58,11 +66,12 @@ constexpr int kTrOffV = kTrOffK + kTrKStages * kTrTile;
 constexpr int kTrOffBar = kTrOffV + kTrVStages * kTrTile;
 // 8-byte slots: K full / empty and V full / empty per stage, Q, two score, two
 // P and two PV barriers, the TMEM address, the abort flag, the last piece with
-// a V row that is not finite, the CTA's place in the second list
+// a V row that is not finite, the CTA's place in the second list and, for each of
+// the softmax warps, its place while it works on a piece
 constexpr int kTsKFull = 0, kTsKEmpty = kTsKFull + kTrKStages, kTsVFull = kTsKEmpty + kTrKStages;
 constexpr int kTsVEmpty = kTsVFull + kTrVStages, kTsQ = kTsVEmpty + kTrVStages, kTsS = kTsQ + 1;
 constexpr int kTsP = kTsS + 2, kTsO = kTsP + 2, kTsTmem = kTsO + 2, kTsAbort = kTsTmem + 1;
-constexpr int kTsBad = kTsAbort + 1, kTsPlace = kTsBad + 1, kTsSlots = 32;
+constexpr int kTsBad = kTsAbort + 1, kTsPlace = kTsBad + 1, kTsSlots = 48;
 constexpr int kTrSmem = kTrOffBar + kTsSlots * 8;
 static_assert(2 * (kTrSmem + 1024) <= 228 * 1024, "two CTAs do not fit an SM");
 constexpr int kTrCols = 256;    // tensor memory columns: S_0 0.., S_1 64.., O 128..
@@ -171,7 +180,7 @@ struct TreePlace {
   int s, g, mt;
   TreeSeq q;
 };
-static_assert(sizeof(TreePlace) <= (kTsSlots - kTsPlace) * 8, "the place does not fit");
+static_assert(5 * sizeof(TreePlace) <= (kTsSlots - kTsPlace) * 8, "the place does not fit");
 
 struct TreePiece {
   TreeSeq q;
@@ -522,6 +531,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       };
       int chunk = (u.t1 - 1) / kChunk;
       int ph_lane = entry(chunk), ph_next = entry(chunk - 1);
+#pragma unroll 1
       for (int j = u.t1 - 1; j >= u.t0; --j, ++it) {
         if (j / kChunk != chunk) {
           --chunk;
@@ -573,6 +583,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         tc_fence_after();
       }
       const int n = u.t1 - u.t0;
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j, ++it) {
         const int buf = it & 1;
         if (warp == 1) {
@@ -629,7 +640,9 @@ __global__ void __launch_bounds__(kTrThreads, 2)
     const float c = p.scale_log2;
     bool ok = true;
     int piece = 0;
+    TreePlace *const save = second + 1 + (warp & 3);
     while (ok && walk.next(p, u)) {
+      if (lane == 0) *save = walk.at;  // (registers are short in between)
       const int R = u.mt * kPfRows + r, limit = u.q.nodes * p.group;
       const bool valid = R < limit;
       const bool alive = u.mt * kPfRows + lb < limit;  // any row of the warp
@@ -649,23 +662,28 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       }
       // Q rows, half a warp a row, into the layout the TMA gives K tiles
       if (alive) {
-        uint4 qv[16];
         const int ch = lane & 15;
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q) + ch;
+        const uint32_t a0 = base + kTrOffQ + (ch >> 3) * kTrQHalf + lb * 128;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int x = 2 * i + (lane >> 4);
-          const uint32_t row = __shfl_sync(kAll, my_row, x);
-          qv[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (u.mt * kPfRows + lb + x < limit) qv[i] = src[(size_t)row * 16];
+          const bool there = u.mt * kPfRows + lb + x < limit;
+          const uint32_t from = __shfl_sync(kAll, my_row, x), row = there ? from : 0u;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(a0 + sw128(x, ch & 7)),
+                       "l"(p.q + (size_t)row * kHeadDim + 8 * ch), "r"(there ? 16 : 0)
+                       : "memory");
         }
-        const uint32_t a0 = base + kTrOffQ + (ch >> 3) * kTrQHalf + lb * 128;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           a0 + sw128(2 * i + (lane >> 4), ch & 7)),
-                       "r"((qv[i].x & p.q_and) ^ p.q_xor), "r"((qv[i].y & p.q_and) ^ p.q_xor),
-                       "r"((qv[i].z & p.q_and) ^ p.q_xor), "r"((qv[i].w & p.q_and) ^ p.q_xor));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (p.q_and != 0xffffffffu || p.q_xor != 0u) {  // a scale <= 0, folded into q
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t a = a0 + sw128(2 * i + (lane >> 4), ch & 7);
+            const uint4 v = lds128(a);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
+                         "r"((v.x & p.q_and) ^ p.q_xor), "r"((v.y & p.q_and) ^ p.q_xor),
+                         "r"((v.z & p.q_and) ^ p.q_xor), "r"((v.w & p.q_and) ^ p.q_xor)
+                         : "memory");
+          }
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       mbar_arrive(b_q);
@@ -698,6 +716,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           climb(first, parent(first + lane), parent(first + lane + 32), unused);
         }
       }
+#pragma unroll 1
       for (int j = u.t1 - 1; j >= u.t0 && ok; --j, ++it) {
         const int st = it % kTrVStages, buf = it & 1;
         const int key0 = j * kPfKeys;
@@ -751,17 +770,6 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           const float m_new = grow ? mxc : m;
           const float alpha = grow && m != -INFINITY ? exp2f(m - m_new) : 1.f;
           m = m_new;
-          const float neg_m = m == -INFINITY ? 0.f : -m;
-          const uint64_t c2 = pack_f32x2(c, c), nm2 = pack_f32x2(neg_m, neg_m);
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x0, x1;
-              unpack_f32x2(fma_f32x2(pack_f32x2(sv[cc][i], sv[cc][i + 1]), c2, nm2), x0, x1);
-              sv[cc][i] = ex2_approx(x0);
-              sv[cc][i + 1] = ex2_approx(x1);
-            }
           // rows whose reference moved rescale O between the PV of the tile
           // before and this one's
           if (__any_sync(kAll, alpha != 1.f)) {
@@ -778,6 +786,8 @@ __global__ void __launch_bounds__(kTrThreads, 2)
               tmem_st32(tmem_o + trow + cc * 32, ov);
             }
           }
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          const uint64_t c2 = pack_f32x2(c, c), nm2 = pack_f32x2(neg_m, neg_m);
           // P over the scores: hi parts (two keys a column) in the buffer's
           // columns 0 .. 31, lo parts in 32 .. 63
           uint64_t ps4[4] = {0ull, 0ull, 0ull, 0ull};
@@ -786,8 +796,12 @@ __global__ void __launch_bounds__(kTrThreads, 2)
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float e0 = sv[cc >> 1][16 * (cc & 1) + 2 * i];
-              const float e1 = sv[cc >> 1][16 * (cc & 1) + 2 * i + 1];
+              float x0, x1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(sv[cc >> 1][16 * (cc & 1) + 2 * i],
+                                                sv[cc >> 1][16 * (cc & 1) + 2 * i + 1]),
+                                     c2, nm2),
+                           x0, x1);
+              const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
               hi[i] = float2_to_bf16x2(e0, e1);
               const uint64_t e2 = pack_f32x2(e0, e1);
               ps4[i & 3] = add_f32x2(ps4[i & 3], e2);
@@ -835,15 +849,19 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         to += (size_t)(lane & 7) * (narrow ? 8 : 16);
 #pragma unroll 1
         for (int cc = 0; cc < kHeadDim / 32; ++cc) {
+          uint32_t dims = 0;
+          if (valid && bad)
+            dims = not_finite(p, u.s, u.q.q0, done, u.g, node, u.t0 * kPfKeys,
+                              u.t1 * kPfKeys - 1, cc);
+          __syncwarp();
           float ov[32];
           tmem_ld32(tmem_o + trow + cc * 32, ov);
-          if (valid && bad) {
-            const uint32_t dims = not_finite(p, u.s, u.q.q0, done, u.g, node, u.t0 * kPfKeys,
-                                             u.t1 * kPfKeys - 1, cc);
+          if (dims != 0) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((dims >> i) & 1u) ov[i] = __int_as_float(0x7fffffff);
           }
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + sw128(lane, i)),
@@ -874,6 +892,8 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           p.part_lse[slot + lane] = l == 0.f ? -INFINITY : m + log2f(l);
       }
       tc_fence_before();
+      __syncwarp();
+      walk.at = *save;
       ++piece;
     }
   }
