@@ -878,8 +878,9 @@ PA_API pa_status pa_prefill_fp8_block(
  *   flags          0 or PA_LAUNCH_PDL, which mean the same here: nothing is
  *                  read or written before the kernel before is over, and the
  *                  kernel after may be set up early.
- * Products run on the tensor cores with fp32 accumulation, the softmax weights
- * as two bf16 terms (16 bits).  A V row's infinities and NaN among the drafted
+ * Products run on the tensor cores with fp32 accumulation (which truncates: fp32
+ * rows come out some 2^-27 of their size smaller for every eight keys that one CTA
+ * adds up), the softmax weights as two bf16 terms (17 bits).  A V row's infinities and NaN among the drafted
  * nodes give NaN to the nodes that see it, and to no others.  A sequence with
  * rows outside [0, total_tokens), more than max_q_len nodes, fewer keys than
  * nodes, or a context past its table row sets PA_DEVERR_SHAPE and is skipped; a

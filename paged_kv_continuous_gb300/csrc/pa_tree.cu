@@ -13,7 +13,7 @@
 // tree_merge_kernel joins them.  Row tiles that share their keys go in twos to
 // neighbouring CTAs that read the same tiles at the same time, the second from L2:
 // one list of all of them read DRAM 1.8 times over and took 182 us for 4 trees of 64
-// nodes behind 32768 keys (32/8 heads), against 152.
+// nodes behind 32768 keys (32/8 heads), against 152 (now 142).
 //
 // Roles of the 8 warps: 0 loads K tiles and 2 V tiles (TMA, two stages each),
 // 1 issues the score MMAs and owns the tensor memory (two score buffers of 64
@@ -28,8 +28,9 @@
 // P is kept as two bf16 terms, the rounded weight and the rounded rest (together
 // 17 bits), each with its PV MMA: one term's error (2^-9 of a weight) is as large
 // as a bf16 output's own rounding.  A third term for fp32 outputs (in shared memory,
-// 146 to 181 us for the case above) left them as far off, 4e-6 of their size: what
-// remains is the tensor cores' own accumulation.
+// 146 to 181 us for the case above) left them as far off: what remains is the tensor
+// cores' accumulation of O, which truncates, 2^-27 of it or so for each MMA of a
+// piece (4e-6 of an fp32 row where pieces have 21 tiles, 2.7e-5 where they have 330).
 //
 // Registers are what the softmax threads are short of (128 with two CTAs per SM):
 // Q goes to shared memory without them (cp.async), a warp's place in the list waits
@@ -40,8 +41,8 @@
 // What bounds it.  Few rows: HBM (8 rows of each of 8 kv heads behind 4 x 32768 keys,
 // 537 MB, 91 us, 5.9 TB/s with a start and a merge of some 12).  Full row tiles: the
 // MMAs' chain (scores, softmax, PV, the next scores into the same buffer), 0.75 us a
-// tile alone and 1.4 us for the two CTAs of an SM together, of which the tensor
-// pipe is busy 68 % (the two P terms, and score MMAs bound by shared memory at N =
+// tile alone and 1.3 us for the two CTAs of an SM together, of which the tensor
+// pipe is busy 72 % (the two P terms, and score MMAs bound by shared memory at N =
 // 64).  Small calls: latency, 9 us for one tile of one sequence.
 #include <climits>
 #include <cmath>

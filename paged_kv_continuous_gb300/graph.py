@@ -26,6 +26,10 @@ place, so it must be refilled before every replay; the fused call leaves q
 as it is).  The decode kernel partitions its work from
 ``context_lens`` on the device, so a replay follows new lengths without a
 new capture.
+
+``TreeStepGraph`` is a speculative step in two graphs: the stores and the
+``pa_decode_tree`` calls of all layers, and ``pa_verify_tree`` with
+``pa_commit_tree``.
 """
 from __future__ import annotations
 
