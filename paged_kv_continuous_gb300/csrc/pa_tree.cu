@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       const int32_t *par = p.parents + u.q.q0;
       auto parent = [&](int n) { return n >= 0 && n < u.q.nodes ? par[n] : -1; };
       int par0 = -1, par1 = -1;
-      if (alive && u.t1 * kPfKeys > done) {
+      if (alive && (u.t1 - 1) * kPfKeys > done - kPfKeys) {
         const int first = (u.t1 - 1) * kPfKeys - done;
         par0 = parent(first + lane);
         par1 = parent(first + lane + 32);
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           up = next < up && next >= -1 ? next : -1;
         }
       };
-      if (alive && u.t1 * kPfKeys > done) {  // the windows above the piece's last tile
+      if (alive && (u.t1 - 1) * kPfKeys > done - kPfKeys) {  // the windows above the piece's last tile
         uint32_t unused[2] = {0u, 0u};
         const int top = by_group(p, min(u.mt * kPfRows + lb + 31, limit - 1));
         for (int j = (done + top) / kPfKeys; j >= u.t1; --j) {
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           uint32_t dims = 0;
           if (valid && bad)
             dims = not_finite(p, u.s, u.q.q0, done, u.g, node, u.t0 * kPfKeys,
-                              u.t1 * kPfKeys - 1, cc);
+                              (u.t1 - 1) * kPfKeys + (kPfKeys - 1), cc);
           __syncwarp();
           float ov[32];
           tmem_ld32(tmem_o + trow + cc * 32, ov);

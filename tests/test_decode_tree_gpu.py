@@ -125,6 +125,33 @@ def test_long_context(ops):
     c.check(c.run(ops, torch.bfloat16))
 
 
+def test_the_longest_context(ops):
+    """2^31 - 1 keys, all but the last pages the same one: offsets, tiles and windows at the end
+    of an int.  K is zero and V one, so every row is one, but where a drafted node's NaN is
+    seen: nodes 0 and 1 (its child) see node 0's, node 2 does not."""
+    n = 2**31 - 1
+    entries = (n + 15) // 16
+    tables = torch.zeros((1, entries), dtype=torch.int32, device="cuda")
+    tables[0, -1] = 1
+    k = torch.zeros((2, 16, 1, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.ones((2, 16, 1, 128), dtype=torch.bfloat16, device="cuda")
+    last = (n - 1) % 16
+    v[1, last - 2, 0, 5] = float("nan")  # node 0
+    v[1, last + 1:] = float("nan")  # past the end
+    q = torch.randn((3, 1, 128), device="cuda").to(torch.bfloat16)
+    ws = ops.tree_workspace()
+    out = ops.decode_tree(q, to_dev_i32([0, 3]), to_dev_i32([-1, 0, -1]), k, v, tables,
+                          to_dev_i32([n]), SCALE, 3, out_dtype=torch.float32, workspace=ws)
+    assert ops.read_error_word(ws) == 0
+    o = out[:, 0].cpu()
+    nan = torch.zeros((3, 128), dtype=torch.bool)
+    nan[:2, 5] = True
+    assert torch.equal(torch.isnan(o), nan)
+    # a part is some 2^31 / 304 = 7.1 million keys: its sums of ones are whole numbers below 2^24,
+    # exact in fp32, and the merge adds 2^-20
+    assert (o[~nan] - 1).abs().max() <= 2.0 ** -20
+
+
 @pytest.mark.parametrize("scale", [-SCALE, 0.0, 1.0])
 def test_scales(ops, scale):
     c = Case(8, [100], [20], 6, 2)
