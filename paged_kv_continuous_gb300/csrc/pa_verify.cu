@@ -77,7 +77,7 @@ __device__ __forceinline__ Pair minus(const Pair &a, const Pair &b) {
 }
 // a b and a / b, within 2^-44.
 __device__ __forceinline__ Pair times(const Pair &a, const Pair &b) {
-  const float h = a.hi * b.hi;
+  const float h = __fmul_rn(a.hi, b.hi);
   const float l = fmaf(a.hi, b.hi, -h) + fmaf(a.hi, b.lo, a.lo * b.hi);
   const float hi = h + l;
   return {hi, l - (hi - h)};
@@ -103,24 +103,41 @@ __device__ __forceinline__ Pair warp_upto(Pair x) {
   return x;
 }
 
-// max(p - beta q, 0) as a pair, beta = bh + bl; where it is only added up, hi need
-// not be the sum's rounding.
-template <bool kRounded>
+// max(p - beta q, 0) as a pair, beta = bh + bl.
 __device__ __forceinline__ Pair weight(float p, float q, float bh, float bl) {
-  const float ph = q * bh;
+  const float ph = __fmul_rn(q, bh);
   const float pl = fmaf(q, bl, fmaf(q, bh, -ph));
   // p - ph = s + ((p - s) - ph) where p >= ph; elsewhere nothing is left anyway
-  const float s = p - ph;
+  const float s = __fadd_rn(p, -ph);
   const float lo = ((p - s) - ph) - pl;
   const float hi = s + lo;
-  if constexpr (!kRounded) return {hi > 0.f ? s : 0.f, hi > 0.f ? lo : 0.f};
   return {hi > 0.f ? hi : 0.f, hi > 0.f ? lo - (hi - s) : 0.f};
 }
-// a + x without bringing hi up to date: x's low part and the error go to lo.
-__device__ __forceinline__ void add(Pair &a, const Pair &x) {
-  const float s = a.hi + x.hi, bb = s - a.hi;
-  a.lo += ((a.hi - (s - bb)) + (x.hi - bb)) + x.lo;
+
+// Two running sums side by side, two floats an instruction: hi's, and what adding
+// to them lost.
+struct Sum2 {
+  uint64_t hi, lo;
+};
+__device__ __forceinline__ void add2(Sum2 &a, uint64_t x) {
+  const uint64_t s = add_f32x2(a.hi, x), b = sub_f32x2(s, a.hi);
+  a.lo = add_f32x2(a.lo, add_f32x2(sub_f32x2(a.hi, sub_f32x2(s, b)), sub_f32x2(x, b)));
   a.hi = s;
+}
+// The weights of two tokens, as weight() takes them, added.
+__device__ __forceinline__ void add_weights2(Sum2 &a, uint64_t p, uint64_t q, uint64_t bh,
+                                             uint64_t bl) {
+  const uint64_t ph = mul_f32x2(q, bh);
+  const uint64_t minus = ph ^ 0x8000000080000000ull;
+  const uint64_t pl = fma_f32x2(q, bl, fma_f32x2(q, bh, minus));
+  const uint64_t s = add_f32x2(p, minus);
+  const uint64_t lo = sub_f32x2(add_f32x2(sub_f32x2(p, s), minus), pl);
+  float s0, s1, l0, l1, h0, h1;
+  unpack_f32x2(add_f32x2(s, lo), h0, h1);
+  unpack_f32x2(s, s0, s1);
+  unpack_f32x2(lo, l0, l1);
+  add2(a, pack_f32x2(h0 > 0.f ? s0 : 0.f, h1 > 0.f ? s1 : 0.f));
+  a.lo = add_f32x2(a.lo, pack_f32x2(h0 > 0.f ? l0 : 0.f, h1 > 0.f ? l1 : 0.f));
 }
 
 // The rows of a node and the scalars of its weights.
@@ -148,13 +165,12 @@ __device__ __forceinline__ void load4(const float *row, int i, int n, float (&v)
   }
 }
 // Their weights; a bit of `out` (where there are such) marks a rejected guess.
-template <bool kRounded>
 __device__ __forceinline__ void weights4(const Rows &r, const float (&p)[4], const float (&q)[4],
                                          const uint32_t *out, int i, Pair (&w)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (r.q) {
-      w[k] = weight<kRounded>(p[k], q[k], r.bh, r.bl);
+      w[k] = weight(p[k], q[k], r.bh, r.bl);
     } else {
       const bool pos = p[k] > 0.f && !(out && ((out[(i + k) >> 5] >> ((i + k) & 31)) & 1u));
       w[k] = {pos ? p[k] : 0.f, 0.f};
@@ -163,13 +179,14 @@ __device__ __forceinline__ void weights4(const Rows &r, const float (&p)[4], con
 }
 
 // The sum of a warp's segment [s0, s1): a lane's four tokens of every 128.
-template <bool kVec, bool kDraft>
+// kAhead: rows of 128 tokens whose loads are in flight.
+template <bool kVec, bool kDraft, int kAhead>
 __device__ __forceinline__ Pair segment_sum_of(const Rows &r, int s0, int s1,
                                                const uint32_t *out) {
   const int lane = threadIdx.x & 31;
-  Pair acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-  constexpr int kAhead = kDraft ? 4 : 8;  // rows of 128 tokens, the loads in flight
-  const Rows mine{r.p, kDraft ? r.q : nullptr, r.bh, r.bl};
+  Sum2 acc[2] = {{0, 0}, {0, 0}};
+  const uint64_t bh = pack_f32x2(r.bh, r.bh), bl = pack_f32x2(r.bl, r.bl);
+  const Rows plain{r.p, nullptr, 0.f, 0.f};
   for (int b = s0; b < s1; b += 128 * kAhead) {
     const int i0 = b + 4 * lane;
     float p[kAhead][4], q[kAhead][4];
@@ -181,25 +198,37 @@ __device__ __forceinline__ Pair segment_sum_of(const Rows &r, int s0, int s1,
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      Pair w[4];
-      if (b + 128 * a < s1) {
-        weights4<false>(mine, p[a], q[a], out, i0 + 128 * a, w);
+      if (b + 128 * a >= s1) continue;
+      if constexpr (kDraft) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add(acc[k], w[k]);
+        for (int k = 0; k < 2; ++k)
+          add_weights2(acc[k], pack_f32x2(p[a][2 * k], p[a][2 * k + 1]),
+                       pack_f32x2(q[a][2 * k], q[a][2 * k + 1]), bh, bl);
+      } else {
+        Pair w[4];
+        weights4(plain, p[a], q[a], out, i0 + 128 * a, w);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) add2(acc[k], pack_f32x2(w[2 * k].hi, w[2 * k + 1].hi));
       }
     }
   }
-  Pair sum = plus(plus(acc[0], acc[1]), plus(acc[2], acc[3]));
+  Pair part[4];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    unpack_f32x2(acc[k].hi, part[2 * k].hi, part[2 * k + 1].hi);
+    unpack_f32x2(acc[k].lo, part[2 * k].lo, part[2 * k + 1].lo);
+  }
+  Pair sum = plus(plus(part[0], part[1]), plus(part[2], part[3]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     sum = plus(sum, {__shfl_xor_sync(0xffffffffu, sum.hi, o),
                      __shfl_xor_sync(0xffffffffu, sum.lo, o)});
   return sum;
 }
-template <bool kVec>
+template <bool kVec, int kAhead>
 __device__ __forceinline__ Pair segment_sum(const Rows &r, int s0, int s1, const uint32_t *out) {
-  return r.q ? segment_sum_of<kVec, true>(r, s0, s1, out)
-             : segment_sum_of<kVec, false>(r, s0, s1, out);
+  return r.q ? segment_sum_of<kVec, true, kAhead>(r, s0, s1, out)
+             : segment_sum_of<kVec, false, 8>(r, s0, s1, out);
 }
 
 // The first token of segment [s0, s1) where `before` plus the running sum is over
@@ -219,7 +248,7 @@ __device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, 
     Pair w[4], c[4];
     load4<kVec>(r.p, i, s1 - i, p);
     if (r.q) load4<kVec>(r.q, i, s1 - i, q);
-    weights4<true>(r, p, q, out, i, w);
+    weights4(r, p, q, out, i, w);
     c[0] = w[0];
     int last = -1;
 #pragma unroll
@@ -257,11 +286,11 @@ __device__ int segment_find(const Rows &r, int s0, int s1, const uint32_t *out, 
 // All segments' sums into `sums` of every CTA of the cluster.  Alternate passes use
 // alternate halves of `mine`: a CTA still reads one pass's while another writes the
 // next one's, and the pass after that waits for it at the barrier between.
-template <bool kVec, int kRanks>
+template <bool kVec, int kRanks, int kAhead>
 __device__ void sum_rows(cg::cluster_group &cluster, const Rows &r, const uint32_t *out, int s0,
                          int s1, Pair (&mine)[2][kVfWarps], Pair *sums, int pass) {
   const int tid = threadIdx.x, warp = tid >> 5;
-  const Pair sum = segment_sum<kVec>(r, s0, s1, out);
+  const Pair sum = segment_sum<kVec, kAhead>(r, s0, s1, out);
   if ((tid & 31) == 0) mine[pass & 1][warp] = sum;
   cluster.sync();
   if (tid < kRanks * kVfWarps) {
@@ -288,9 +317,10 @@ __device__ __forceinline__ Pair scan_sums(const Pair *sums, Pair &before, Pair (
   return shfl(upto[kPer - 1], 31);
 }
 
-// kRanks: CTAs of a cluster, at most.
-template <bool kVec, int kRanks>
-__global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyParams p) {
+// kRanks: CTAs of a cluster, at most; kAhead: rows of both probabilities in flight,
+// four with four CTAs on an SM, eight with two.
+template <bool kVec, int kRanks, int kAhead>
+__global__ void __launch_bounds__(kVfThreads, 16 / kAhead) verify_kernel(const VerifyParams p) {
   __shared__ int n_par[kVfNodes], n_tok[kVfNodes];
   __shared__ float n_u[kVfNodes], n_p[kVfNodes], n_q[kVfNodes];
   __shared__ Pair mine[2][kVfWarps];  // this CTA's segment sums, of alternate passes
@@ -371,7 +401,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyParam
       const Rows r{p.p + row * p.p_stride, plain ? nullptr : p.q + row * p.q_stride, s_beta.hi,
                    s_beta.lo};
       const bool last = s_act == kSum;
-      sum_rows<kVec, kRanks>(cluster, r, looked ? out_bits : nullptr, s0, s1, mine, sums, passes++);
+      sum_rows<kVec, kRanks, kAhead>(cluster, r, looked ? out_bits : nullptr, s0, s1, mine, sums, passes++);
       if (last) break;
     }
     if (warp == 0) {
@@ -476,7 +506,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(const VerifyParam
     __syncthreads();        // all warps have read `sums`
     r.q = nullptr;
     out = nullptr;
-    sum_rows<kVec, kRanks>(cluster, r, out, s0, s1, mine, sums, passes++);
+    sum_rows<kVec, kRanks, kAhead>(cluster, r, out, s0, s1, mine, sums, passes++);
     total = scan_sums(sums, before, upto);
   }
   const float ul = p.u_last[seq], th = ul * total.hi;  // u' times the total
@@ -530,18 +560,52 @@ int verify_ranks(int vocab, int seqs, int sms) {
   return ranks;
 }
 
-template <bool kVec, int kRanks>
+template <bool kVec, int kRanks, int kAhead>
 cudaError_t launch_verify(const VerifyParams &p, int ranks, size_t bits, int device,
                           cudaStream_t s) {
   static std::atomic<bool> configured[64] = {};
-  cudaError_t e =
-      set_smem_once(configured, verify_kernel<kVec, kRanks>, device, kVfMaxVocab / 8);
+  auto kernel = verify_kernel<kVec, kRanks, kAhead>;
+  cudaError_t e = set_smem_once(configured, kernel, device, kVfMaxVocab / 8);
   if (e == cudaSuccess && kRanks > 8)
-    e = cudaFuncSetAttribute(verify_kernel<kVec, kRanks>,
-                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  return launch_cluster(verify_kernel<kVec, kRanks>, dim3((unsigned)(p.num_seqs * ranks)),
-                        dim3(kVfThreads), (unsigned)ranks, bits, s, p);
+  return launch_cluster(kernel, dim3((unsigned)(p.num_seqs * ranks)), dim3(kVfThreads),
+                        (unsigned)ranks, bits, s, p);
+}
+// Clusters of sixteen CTAs, two per SM, that the device runs at once (a cluster stays
+// within a part of the chip, so fewer than its SMs would hold); asked once.
+template <bool kVec>
+int wide_clusters(int device) {
+  static std::atomic<int> known[64] = {};
+  const bool tracked = device >= 0 && device < 64;
+  int n = tracked ? known[device].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n - 1;
+  auto kernel = verify_kernel<kVec, kVfMoreRanks, 8>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kVfMoreRanks);
+  cfg.blockDim = dim3(kVfThreads);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kVfMoreRanks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (tracked) known[device].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+template <bool kVec>
+cudaError_t launch_verify(const VerifyParams &p, int ranks, size_t bits, int device,
+                          cudaStream_t s) {
+  if (ranks <= kVfRanks) return launch_verify<kVec, kVfRanks, 4>(p, ranks, bits, device, s);
+  return p.num_seqs <= wide_clusters<kVec>(device)
+             ? launch_verify<kVec, kVfMoreRanks, 8>(p, ranks, bits, device, s)
+             : launch_verify<kVec, kVfMoreRanks, 4>(p, ranks, bits, device, s);
 }
 
 }  // namespace
@@ -608,12 +672,8 @@ extern "C" pa_status pa_verify_tree(int32_t *accepted, int32_t *path, int32_t *o
                    target_stride % 4 == 0 && (!draft_probs || draft_stride % 4 == 0);
   const size_t bits = draft_probs ? 0 : (size_t)(vocab_size + 31) / 32 * 4;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      ranks <= kVfRanks
-          ? vec ? launch_verify<true, kVfRanks>(p, ranks, bits, device, st)
-                : launch_verify<false, kVfRanks>(p, ranks, bits, device, st)
-          : vec ? launch_verify<true, kVfMoreRanks>(p, ranks, bits, device, st)
-                : launch_verify<false, kVfMoreRanks>(p, ranks, bits, device, st);
+  const cudaError_t e = vec ? launch_verify<true>(p, ranks, bits, device, st)
+                            : launch_verify<false>(p, ranks, bits, device, st);
   if (e != cudaSuccess) return PA_ERR_LAUNCH;
   return PA_OK;
 }
