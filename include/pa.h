@@ -880,7 +880,8 @@ PA_API pa_status pa_prefill_fp8_block(
  *                  kernel after may be set up early.
  * Products run on the tensor cores with fp32 accumulation (which truncates: fp32
  * rows come out some 2^-27 of their size smaller for every eight keys that one CTA
- * adds up), the softmax weights as two bf16 terms (17 bits).  A V row's infinities and NaN among the drafted
+ * adds up), the softmax weights as two bf16 terms (17 bits; three, 24 bits, for
+ * fp32 rows where a CTA adds up 768 keys or fewer).  A V row's infinities and NaN among the drafted
  * nodes give NaN to the nodes that see it, and to no others.  A sequence with
  * rows outside [0, total_tokens), more than max_q_len nodes, fewer keys than
  * nodes, or a context past its table row sets PA_DEVERR_SHAPE and is skipped; a

@@ -27,10 +27,10 @@
 //
 // P is kept as two bf16 terms, the rounded weight and the rounded rest (together
 // 17 bits), each with its PV MMA: one term's error (2^-9 of a weight) is as large
-// as a bf16 output's own rounding.  A third term for fp32 outputs (in shared memory,
-// 146 to 181 us for the case above) left them as far off: what remains is the tensor
-// cores' accumulation of O, which truncates, 2^-27 of it or so for each MMA of a
-// piece (4e-6 of an fp32 row where pieces have 21 tiles, 2.7e-5 where they have 330).
+// as a bf16 output's own rounding.  fp32 rows have a third term, in shared memory,
+// where a piece is short (kTrThird); in long ones the tensor cores' accumulation of
+// O, which truncates, outweighs what it would mend (4e-6 of a row where pieces have
+// 21 tiles, 1.6e-5 for 108).
 //
 // Registers are what the softmax threads are short of (128 with two CTAs per SM):
 // Q goes to shared memory without them (cp.async), a warp's place in the list waits
@@ -64,7 +64,8 @@ constexpr int kTrKStages = 2, kTrVStages = 2;
 constexpr int kTrOffQ = 0;
 constexpr int kTrOffK = kTrOffQ + 2 * kTrQHalf;
 constexpr int kTrOffV = kTrOffK + kTrKStages * kTrTile;
-constexpr int kTrOffBar = kTrOffV + kTrVStages * kTrTile;
+constexpr int kTrOffP = kTrOffV + kTrVStages * kTrTile;  // third P term: 128 rows x 64 keys
+constexpr int kTrOffBar = kTrOffP + kPfRows * 128;
 // 8-byte slots: K full / empty and V full / empty per stage, Q, two score, two
 // P and two PV barriers, the TMEM address, the abort flag, the last piece with
 // a V row that is not finite, the CTA's place in the second list and, for each of
@@ -83,6 +84,11 @@ constexpr int kTrSCols = 64, kTrO = 128;
 // 8192 keys (12/2 heads) took 27.6 / 23.5 / 24.0 / 23.4 us, six chains behind 9 to 30
 // thousand (20/4 heads) 52.4 / 48.3 / 47.7 / 47.2.
 constexpr int kTrPieceTiles = 5;
+
+// fp32 rows of a piece of up to this many tiles have a third P term.  Two leave
+// 2e-6 of a row, three 4e-7, while the accumulation's truncation grows by 1.3e-7 a
+// tile with two and 2e-7 with three: even at 13 tiles.
+constexpr int kTrThird = 12;
 
 // What the merge has to know of CTA c's first piece, where it goes on with a unit
 // that an earlier CTA began: the unit's rows, CTAs first .. last and output rows.
@@ -412,6 +418,7 @@ __device__ __forceinline__ void clean_v(uint32_t tile, int r, int key0, int done
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+template <bool kF32>  // fp32 rows, else bf16
 __global__ void __launch_bounds__(kTrThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
@@ -584,6 +591,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         tc_fence_after();
       }
       const int n = u.t1 - u.t0;
+      const bool third = kF32 && n <= kTrThird;
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j, ++it) {
         const int buf = it & 1;
@@ -619,6 +627,12 @@ __global__ void __launch_bounds__(kTrThreads, 2)
               umma_f16_ta(tmem_o, tmem + buf * kTrSCols + part * (kTrSCols / 2) + ks * 8,
                           umma_desc(vb + ks * 16 * 128, kTrHalf, 1024), idesc_pv,
                           (j > 0 || part > 0 || ks > 0) ? 1u : 0u);
+          if (third) {
+#pragma unroll
+            for (int ks = 0; ks < kPfKeys / 16; ++ks)
+              umma_f16_ss(tmem_o, umma_desc(base + kTrOffP + ks * 32, 16, 1024),
+                          umma_desc(vb + ks * 16 * 128, kTrHalf, 1024), idesc_pv, 1u);
+          }
           umma_commit(b_o + 8 * buf);
           umma_commit(b_v_empty + 8 * st);
           last_bar = b_o + 8 * buf;
@@ -692,6 +706,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
       // a tile's largest exceeds it by more than 8, so P <= 256 and O is rescaled
       // rarely.  l: the row's sum.  up: the next node of the walk to the root.
       float m = -INFINITY, l = 0.f;
+      const bool third = kF32 && u.t1 - u.t0 <= kTrThird;
       // A tile's 64 keys are a window of 64 nodes, whose parents the warp holds,
       // two a lane: a step of the walk is a shuffle.
       int up = valid ? node : -1;
@@ -789,6 +804,11 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           }
           const float neg_m = m == -INFINITY ? 0.f : -m;
           const uint64_t c2 = pack_f32x2(c, c), nm2 = pack_f32x2(neg_m, neg_m);
+          if (third && it > 0) {  // the third term's place is read until the PV before is over
+            ok = __all_sync(kAll, mbar_wait(b_o + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1,
+                                            abort_flag, p.err));
+            if (!ok) break;
+          }
           // P over the scores: hi parts (two keys a column) in the buffer's
           // columns 0 .. 31, lo parts in 32 .. 63
           uint64_t ps4[4] = {0ull, 0ull, 0ull, 0ull};
@@ -814,6 +834,29 @@ __global__ void __launch_bounds__(kTrThreads, 2)
             }
             tmem_st8(sb + trow + cc * 8, hi);
             tmem_st8(sb + trow + kTrSCols / 2 + cc * 8, lo);
+            if (third) {  // 16 keys of the row (the weights again: keeping them spills)
+              uint32_t low[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float x0, x1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(sv[cc >> 1][16 * (cc & 1) + 2 * i],
+                                                  sv[cc >> 1][16 * (cc & 1) + 2 * i + 1]),
+                                       c2, nm2),
+                             x0, x1);
+                low[i] = float2_to_bf16x2(
+                    (ex2_approx(x0) - __uint_as_float(hi[i] << 16)) - __uint_as_float(lo[i] << 16),
+                    (ex2_approx(x1) - __uint_as_float(hi[i] & 0xFFFF0000u)) -
+                        __uint_as_float(lo[i] & 0xFFFF0000u));
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 base + kTrOffP + sw128(r, 2 * cc + h)),
+                             "r"(low[4 * h]), "r"(low[4 * h + 1]), "r"(low[4 * h + 2]),
+                             "r"(low[4 * h + 3])
+                             : "memory");
+              }
+            }
           }
           float ps8[8];
 #pragma unroll
@@ -821,6 +864,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
           l = l * alpha + (((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) +
                            ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7])));
           tmem_wait_st();
+          if (third) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         tc_fence_before();
         mbar_arrive(b_p + 8 * buf);
@@ -839,7 +883,7 @@ __global__ void __launch_bounds__(kTrThreads, 2)
         // 32 columns of the warp's rows at a time go through its own Q rows (which
         // no MMA reads any more), so that eight lanes store a row's 128 bytes
         const uint32_t stage = base + kTrOffQ + lb * 128;
-        const bool narrow = whole && !p.out_f32;
+        const bool narrow = whole && !kF32;
         char *to = whole ? static_cast<char *>(p.out)
                          : reinterpret_cast<char *>(p.part_o + slot * kHeadDim);
         uint32_t rows[8];  // of this lane's stores
@@ -1084,6 +1128,18 @@ size_t tree_workspace(long long splits) {
          (size_t)splits * 2 * sizeof(TreeCut);
 }
 
+template <bool kF32>
+cudaError_t launch_tree(const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                        int device, cudaStream_t s) {
+  static std::atomic<bool> configured[64] = {};
+  const cudaError_t e = set_smem_once(configured, tree_kernel<kF32>, device, kTrSmem);
+  if (e != cudaSuccess) return e;
+  // two CTAs per SM: all of the unified L1 / shared memory as shared memory (a hint)
+  cudaFuncSetAttribute(tree_kernel<kF32>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  return launch_kernel(tree_kernel<kF32>, dim3((unsigned)p.splits), dim3(kTrThreads), kTrSmem, s,
+                       true, tk, tv, p);
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -1150,10 +1206,6 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
   if (!pf_pool_map(&tk, k_cache, num_blocks, num_kv_heads) ||
       !pf_pool_map(&tv, v_cache, num_blocks, num_kv_heads))
     return PA_ERR_DEVICE;
-  static std::atomic<bool> configured[64] = {};
-  if (set_smem_once(configured, tree_kernel, device, kTrSmem) != cudaSuccess) return PA_ERR_LAUNCH;
-  // two CTAs per SM: all of the unified L1 / shared memory as shared memory (a hint)
-  cudaFuncSetAttribute(tree_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   char *ws = static_cast<char *>(workspace);
   TreeParams p;
   p.out = out;
@@ -1186,9 +1238,9 @@ extern "C" pa_status pa_decode_tree(void *out, int32_t out_dtype, const void *q,
                                        tree_lse_bytes(splits));
   p.err = static_cast<int32_t *>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_kernel(tree_kernel, dim3((unsigned)splits), dim3(kTrThreads), kTrSmem, s, true, tk,
-                    tv, p) != cudaSuccess)
-    return PA_ERR_LAUNCH;
+  const cudaError_t e = p.out_f32 ? launch_tree<true>(tk, tv, p, device, s)
+                                  : launch_tree<false>(tk, tv, p, device, s);
+  if (e != cudaSuccess) return PA_ERR_LAUNCH;
   if (splits > 1 &&
       launch_kernel(tree_merge_kernel, dim3((unsigned)splits, 2), dim3(32 * kTmWarps), 0, s, true,
                     p) != cudaSuccess)

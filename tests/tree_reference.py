@@ -60,12 +60,13 @@ def attention_bound(out, a, big, scale, keys, bf16_out):
     truncating adder) of the sum of magnitudes; the scaling, the subtraction of the
     reference and the exponential (2^-22) add 2^-20 to a weight's relative
     error for scores up to 8 or so past the reference; the last of a weight's bf16
-    terms is rounded, the second of two for a bf16 output (at 2^-16 of the weight or
-    less), the third of three for fp32 (2^-24); weights and products are added in fp32 (2 u for
+    terms is rounded, the second of two (at 2^-16 of the weight or less), or for
+    fp32 rows of few keys the third of three; weights and products are added in fp32 (2 u for
     each of `keys` additions, numerator and denominator); the merge of pieces and the
     division add 2^-20.  The output is rounded by half a step."""
     score = abs(scale) * 128 * 2.0 ** -23 * big[..., None]
-    terms = 2.0 ** -16 if bf16_out else 2.0 ** -24
+    # (up to 12 tiles of 64 keys a piece, of which 512 keys are eight at most)
+    terms = 2.0 ** -16 if bf16_out or keys > 512 else 2.0 ** -24
     rel = 2 * score + terms + 2 * 2.0 ** -20 + 2 * keys * 2.0 ** -23
     return rel * a + (2.0 ** -8 if bf16_out else 2.0 ** -24) * np.abs(out) + 1e-30
 
