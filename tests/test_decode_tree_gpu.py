@@ -112,6 +112,25 @@ def test_splits_agree(ops, splits):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("nodes,hq,hkv", [([300], 8, 1), ([45, 200, 64], 8, 2), ([86], 12, 2)])
+@pytest.mark.parametrize("splits", [0, 1, 2, 5, 9])
+def test_row_tiles_in_pairs(ops, nodes, hq, hkv, splits):
+    """Row tiles in twos and left over, on an even or odd number of CTAs, both output types."""
+    c = Case(sum(nodes), [130, 700, 3][:len(nodes)], nodes, hq, hkv)
+    refs = c.reference()
+    c.check(c.run(ops, num_splits=splits), refs=refs)
+    c.check(c.run(ops, torch.bfloat16, num_splits=splits), refs=refs)
+
+
+def test_both_output_types_of_long_and_short_pieces(ops):
+    """fp32 rows of pieces around the length where a weight's third term ends."""
+    for keys in (700, 768, 832, 1500):
+        c = Case(keys, [keys - 5], [5], 4, 1)
+        refs = c.reference()
+        for splits in (1, 2):
+            c.check(c.run(ops, num_splits=splits), refs=refs)
+
+
 def test_many_sequences(ops):
     rng = np.random.default_rng(5)
     nodes = rng.integers(0, 4, 700)

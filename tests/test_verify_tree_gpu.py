@@ -113,6 +113,23 @@ def test_large_vocabularies(ops, vocab, sharp):
     c.check(ops)
 
 
+@pytest.mark.parametrize("vocab", [1 << 20, (1 << 20) - 3])
+@pytest.mark.parametrize("drafts", [True, False])
+def test_the_largest_vocabulary(ops, vocab, drafts):
+    c = Case(3, [3, 2], vocab, 2, drafts=drafts, sharp=1.0)
+    c.check(ops)
+    c.u[:] = np.float32(1 - 2.0 ** -24)
+    c.check(ops)
+
+
+@pytest.mark.parametrize("seqs", [1, 14, 30, 45, 90])
+@pytest.mark.parametrize("vocab", [70000, 70001, 9000])
+def test_clusters_of_every_size(ops, seqs, vocab):
+    """The batch sets how many CTAs share a sequence, and the rows' length how many are worth it."""
+    c = Case(seqs + vocab, [2, 3] * (seqs // 2) + [4] * (seqs % 2), vocab, 2, likeness=0.6)
+    c.check(ops)
+
+
 @pytest.mark.parametrize("drafts", [True, False])
 def test_siblings_all_rejected(ops, drafts):
     """A star of guesses that the random numbers reject one after the other."""
